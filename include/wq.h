@@ -236,6 +236,105 @@ wq_status wq_q4k_matmul_ex(const void *X, int64_t M, const void *blocks, int64_t
                            int64_t K, void *Y, int out_dtype, unsigned int flags,
                            wq_stream_t stream);
 
+/* ---- key/value cache in 4 bits -------------------------------------------
+ * What a decode step streams besides the weights: the cached keys and values
+ * of every sequence ("vLLM 量化与推测解码", KV payload; "量化" (llminference
+ * s08), KV cache quantization).  The pages fix no format; this one quantizes
+ * each token's key and value per head in groups along the head dimension,
+ * with the asymmetric map of section 1 as in wq_quantize:
+ *   x is taken to binary16 (nearest, saturating at +-65504), lo = min(0, min
+ *   x), hi = max(0, max x); s = smallest binary16 >= (hi - lo)/15 (1 if hi =
+ *   lo); z = clamp(round(-lo/s), 0, 15); u = clamp(round(x/s) + z, 0, 15);
+ *   every rounding half-to-even of the exact value.  It stands for s (u - z).
+ * A value that is NaN or infinite makes the codes of its group unspecified.
+ *
+ * A cache is a pool of pages of `page_size` tokens, in four device buffers
+ * that the caller owns (16-byte aligned):
+ *   k_codes, v_codes [pages][kv_heads][page_size][head_dim/2] bytes
+ *   k_meta, v_meta   [pages][kv_heads][page_size][head_dim/group][2] binary16:
+ *                    scale, zero (an integer)
+ * Two codes a byte, the even element low.  Within a row the codes are stored
+ * in the order the attention kernels read them: a key row, seen as
+ * [head_dim/32][4] words of 8 codes, is stored as [4][head_dim/32]; a value
+ * row, seen as [head_dim/32][8] halfwords of 4 codes, as [8][head_dim/32].
+ * head_dim in {64, 128}; group in {32, 64, 128}, at most head_dim; page_size
+ * in {16, 32, 64, 128, 256}; slots never written may hold anything. */
+typedef struct wq_kv4_cache {
+    void *k_codes, *k_meta, *v_codes, *v_meta;
+    int64_t pages;
+    int32_t page_size, kv_heads, head_dim, group;
+} wq_kv4_cache;
+
+/* A batch of sequences and their rows (the tokens a call writes, reads or
+ * asks for), packed one sequence after the other.  Sequence b has the rows
+ * row_starts[b] .. row_starts[b + 1] - 1, which are its last tokens: with
+ * T = row_starts[b + 1] - row_starts[b], row row_starts[b] + i is token
+ * seq_lens[b] - T + i.  A row whose token would be negative holds none.
+ * Token p is in slot p % page_size of page page_table[b][p / page_size].
+ *
+ * All arrays are int32 in device memory and read when the call runs, so a
+ * captured graph may be replayed with other contents.  What they hold is
+ * checked there: a row range outside 0 .. rows, a length above table_width *
+ * page_size and, for a token the call needs, a page outside 0 .. pages - 1
+ * record WQ_ERR_INVALID_ARG in the device status word; the results of that
+ * sequence are unspecified and nothing outside the caller's buffers is
+ * touched.  Rows behind the last sequence (row_starts[seqs] .. rows - 1) are
+ * left as they were. */
+typedef struct wq_kv4_batch {
+    int32_t seqs;             /* >= 1 where rows > 0                              */
+    int32_t rows;             /* rows of the packed tensors                       */
+    const int32_t *row_starts;/* [seqs + 1], or NULL: rows/seqs rows each         */
+    const int32_t *seq_lens;  /* [seqs], tokens with the rows included            */
+    const int32_t *page_table;/* [seqs][table_stride]                             */
+    int32_t table_width;      /* entries of a table row that may be used          */
+    int64_t table_stride;     /* elements from one table row to the next          */
+    int32_t max_rows;         /* with row_starts: no sequence has more rows (used
+                               * to choose a kernel; a sequence with more is
+                               * computed all the same); 0: not known             */
+} wq_kv4_batch;
+
+/* Errors of the four calls below, checked on the host before any launch:
+ * WQ_ERR_INVALID_ARG for a size or pointer outside what is described here,
+ * WQ_ERR_UNSUPPORTED for a head_dim, group or page_size outside the lists,
+ * WQ_ERR_ALIGNMENT for a tensor not 16-byte aligned or a row stride not a
+ * multiple of 8 elements.  rows = 0 is a call without work. */
+
+/* Quantize the rows' keys and values, bfloat16 [rows][kv_heads][head_dim]
+ * with row strides of k_stride and v_stride elements (at least kv_heads *
+ * head_dim; heads contiguous), into the cache.  Rows that hold no token are
+ * not written.  Two sequences whose tables share a page must not both write
+ * the same slot of it. */
+wq_status wq_kv4_write(const void *K, int64_t k_stride, const void *V, int64_t v_stride,
+                       const wq_kv4_cache *cache, const wq_kv4_batch *batch,
+                       wq_stream_t stream);
+
+/* The values that the rows' cached tokens stand for, bfloat16 (nearest even)
+ * [rows][kv_heads][head_dim], contiguous.  A sequence's rows that hold no
+ * token get zeros. */
+wq_status wq_kv4_read(const wq_kv4_cache *cache, const wq_kv4_batch *batch, void *K, void *V,
+                      wq_stream_t stream);
+
+/* Bytes of the attention workspace: a device buffer, 16-byte aligned, filled
+ * with zeros before its first use and left ready by every call.  Calls that
+ * may run at the same time (other streams, graphs replayed concurrently)
+ * need different workspaces. */
+size_t wq_kv4_attention_workspace_bytes(void);
+
+/* Causal attention of the rows' queries over the cache:
+ *   O[r][h] = sum_t softmax_t(scale * Q[r][h] . k_t) v_t,
+ * t over the tokens of the row's sequence up to and including the row's own,
+ * k and v the values of kv head h / (q_heads / kv_heads), read from their
+ * codes and never written to memory in 16 bits.  Q and O bfloat16
+ * [rows][q_heads][head_dim], heads contiguous, row strides in elements;
+ * q_heads a multiple of kv_heads; scale finite.  A row that sees no token
+ * gets zeros.  Products are of exact codes with binary16 operands (queries
+ * scaled by a power of two per row, weights rounded within 2^-11), sums and
+ * softmax in binary32.  Deterministic. */
+wq_status wq_kv4_attention(const void *Q, int64_t q_stride, int32_t q_heads,
+                           const wq_kv4_cache *cache, const wq_kv4_batch *batch, float scale,
+                           void *O, int64_t o_stride, void *workspace, size_t workspace_bytes,
+                           wq_stream_t stream);
+
 /* Read and clear the device status word (WQ_OK if no kernel recorded an
  * error).  Synchronizes `stream` first. */
 wq_status wq_get_device_error(wq_stream_t stream);

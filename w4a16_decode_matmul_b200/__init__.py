@@ -12,11 +12,19 @@ Functions keep the C names without the ``wq_`` prefix:
     W_hat = dequantize(codes, scales, zeros, N, K, bits=4, group=128)
 
 ``QuantizedWeight`` bundles the three tensors with their format.
+
+Key/value cache in 4 bits (``KV4Cache``, made by ``kv4_cache``), over the
+packed rows of a batch of sequences:
+
+    kv4_write(k, v, cache, seq_lens, page_table)
+    O = kv4_attention(q, cache, seq_lens, page_table)
+    k, v = kv4_read(cache, seq_lens, page_table, rows=n)
 """
 from __future__ import annotations
 
 import ctypes
 import dataclasses
+import math
 import os
 
 import torch
@@ -40,6 +48,21 @@ class WQError(RuntimeError):
         if status == 4:
             detail += ": " + lib.wq_internal_last_cuda_error().decode()
         super().__init__(f"{what}: {STATUS_NAMES.get(status, status)} ({detail})")
+
+
+class _KV4CacheStruct(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_meta", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_meta", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("group", ctypes.c_int32)]
+
+
+class _KV4BatchStruct(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("row_starts", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("table_width", ctypes.c_int32),
+                ("table_stride", ctypes.c_int64), ("max_rows", ctypes.c_int32)]
 
 
 def _load() -> ctypes.CDLL:
@@ -74,6 +97,16 @@ def _load() -> ctypes.CDLL:
     lib.wq_q4k_matmul.restype = i32
     lib.wq_q4k_matmul_ex.argtypes = [vp, i64, vp, i64, i64, vp, i32, ctypes.c_uint, vp]
     lib.wq_q4k_matmul_ex.restype = i32
+    cache, batch = ctypes.POINTER(_KV4CacheStruct), ctypes.POINTER(_KV4BatchStruct)
+    lib.wq_kv4_write.argtypes = [vp, i64, vp, i64, cache, batch, vp]
+    lib.wq_kv4_write.restype = i32
+    lib.wq_kv4_read.argtypes = [cache, batch, vp, vp, vp]
+    lib.wq_kv4_read.restype = i32
+    lib.wq_kv4_attention_workspace_bytes.argtypes = []
+    lib.wq_kv4_attention_workspace_bytes.restype = sz
+    lib.wq_kv4_attention.argtypes = [vp, i64, i32, cache, batch, ctypes.c_float, vp, i64, vp, sz,
+                                     vp]
+    lib.wq_kv4_attention.restype = i32
     lib.wq_get_device_error.argtypes = [vp]
     lib.wq_get_device_error.restype = i32
     lib.wq_status_string.argtypes = [i32]
@@ -290,6 +323,200 @@ def q4k_matmul(X: torch.Tensor, blocks: torch.Tensor, N: int, K: int,
                                     WQ_MATMUL_STATIC_WEIGHTS if static_weights else 0,
                                     _stream(dev)), "wq_q4k_matmul_ex")
     return Y
+
+
+@dataclasses.dataclass
+class KV4Cache:
+    """A pool of pages of keys and values in 4 bits (see ``include/wq.h``):
+    codes uint8 [pages, kv_heads, page_size, head_dim/2] and (scale, zero)
+    pairs float16 [pages, kv_heads, page_size, head_dim/group, 2], for keys and
+    for values."""
+    k_codes: torch.Tensor
+    k_meta: torch.Tensor
+    v_codes: torch.Tensor
+    v_meta: torch.Tensor
+    group: int
+
+    def __post_init__(self):
+        _require_cuda(self.k_codes, self.k_meta, self.v_codes, self.v_meta)
+        if self.k_codes.dim() != 4 or self.k_codes.dtype != torch.uint8:
+            raise ValueError("k_codes must be uint8 [pages, kv_heads, page_size, head_dim/2]")
+        if self.group < 1 or self.head_dim % self.group:
+            raise ValueError("group must divide the head dimension")
+        meta = (*self.k_codes.shape[:3], self.head_dim // self.group, 2)
+        if self.v_codes.shape != self.k_codes.shape or self.v_codes.dtype != torch.uint8:
+            raise ValueError("v_codes must have the shape and type of k_codes")
+        for m in (self.k_meta, self.v_meta):
+            if m.dtype != torch.float16 or tuple(m.shape) != meta:
+                raise ValueError(f"metadata must be float16 {list(meta)}")
+
+    @property
+    def pages(self) -> int:
+        return self.k_codes.shape[0]
+
+    @property
+    def kv_heads(self) -> int:
+        return self.k_codes.shape[1]
+
+    @property
+    def page_size(self) -> int:
+        return self.k_codes.shape[2]
+
+    @property
+    def head_dim(self) -> int:
+        return self.k_codes.shape[3] * 2
+
+    @property
+    def nbytes(self) -> int:
+        return (self.k_codes.nbytes + self.k_meta.nbytes + self.v_codes.nbytes
+                + self.v_meta.nbytes)
+
+    def _struct(self) -> _KV4CacheStruct:
+        return _KV4CacheStruct(self.k_codes.data_ptr(), self.k_meta.data_ptr(),
+                               self.v_codes.data_ptr(), self.v_meta.data_ptr(), self.pages,
+                               self.page_size, self.kv_heads, self.head_dim, self.group)
+
+
+def kv4_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, group: int = 64,
+              device: torch.device | str = "cuda") -> KV4Cache:
+    """An empty cache (slots never written hold whatever the memory held)."""
+    if min(pages, kv_heads, head_dim, page_size, group) < 1 or head_dim % group or head_dim % 2:
+        raise ValueError("sizes must be positive and group must divide head_dim")
+
+    def codes():
+        return torch.empty((pages, kv_heads, page_size, head_dim // 2), dtype=torch.uint8,
+                           device=device)
+
+    def meta():
+        return torch.empty((pages, kv_heads, page_size, head_dim // group, 2),
+                           dtype=torch.float16, device=device)
+    return KV4Cache(codes(), meta(), codes(), meta(), group)
+
+
+def _kv4_batch(cache: KV4Cache, rows: int, seq_lens, page_table, row_starts, max_rows):
+    """The batch struct after the checks the C ABI cannot make (types, shapes
+    and devices of the int32 arrays)."""
+    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1:
+        raise ValueError("seq_lens must be a 1-D int32 tensor")
+    seqs = seq_lens.shape[0]
+    if (page_table.dtype != torch.int32 or page_table.dim() != 2
+            or page_table.shape[0] != seqs):
+        raise ValueError("page_table must be an int32 tensor [sequences, pages]")
+    if page_table.shape[1] > 1 and page_table.stride(1) != 1:
+        raise ValueError("rows of page_table must be contiguous")
+    if row_starts is not None and (row_starts.dtype != torch.int32
+                                   or tuple(row_starts.shape) != (seqs + 1,)):
+        raise ValueError("row_starts must be an int32 tensor [sequences + 1]")
+    _require_cuda(cache.k_codes, seq_lens, row_starts)
+    if page_table.device != cache.k_codes.device:
+        raise ValueError("page_table is on another device than the cache")
+    width = page_table.shape[1]
+    return _KV4BatchStruct(seqs, rows, None if row_starts is None else row_starts.data_ptr(),
+                           seq_lens.data_ptr(), page_table.data_ptr(), width,
+                           page_table.stride(0) if seqs > 1 else width,
+                           int(max_rows) if max_rows is not None else 0)
+
+
+def _kv4_rows(x: torch.Tensor, heads: int | None, cache: KV4Cache, what: str) -> int:
+    """The row stride in elements of a bfloat16 tensor [rows, heads, head_dim]
+    whose heads are contiguous (a slice of a fused projection's rows, say)."""
+    if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[2] != cache.head_dim or (
+            heads is not None and x.shape[1] != heads):
+        raise ValueError(f"{what} must be bfloat16 [rows, {heads or 'heads'}, {cache.head_dim}]")
+    if x.device != cache.k_codes.device:
+        raise ValueError(f"{what} is on another device than the cache")
+    if x.numel() and (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2])):
+        raise ValueError(f"the heads of a row of {what} must be contiguous")
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+
+def kv4_write(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, seq_lens: torch.Tensor,
+              page_table: torch.Tensor, row_starts: torch.Tensor | None = None) -> None:
+    """``wq_kv4_write``: quantize the rows' keys and values, bfloat16 [rows,
+    kv_heads, head_dim], into the cache as the last tokens of their sequences.
+
+    seq_lens int32 [seqs] counts the tokens with the new rows included;
+    page_table int32 [seqs, width]; row_starts int32 [seqs + 1] gives the rows
+    of each sequence (None: rows/seqs each).  All on the GPU."""
+    ks = _kv4_rows(k, cache.kv_heads, cache, "k")
+    vs = _kv4_rows(v, cache.kv_heads, cache, "v")
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must have the same rows")
+    batch = _kv4_batch(cache, k.shape[0], seq_lens, page_table, row_starts, None)
+    dev = cache.k_codes.device
+    with torch.cuda.device(dev):
+        _check(lib.wq_kv4_write(_ptr(k), ks, _ptr(v), vs, ctypes.byref(cache._struct()),
+                                ctypes.byref(batch), _stream(dev)), "wq_kv4_write")
+
+
+def kv4_read(cache: KV4Cache, seq_lens: torch.Tensor, page_table: torch.Tensor,
+             row_starts: torch.Tensor | None = None, rows: int | None = None,
+             out: tuple[torch.Tensor, torch.Tensor] | None = None):
+    """``wq_kv4_read``: the values (k, v) that the last tokens of the sequences
+    stand for, bfloat16 [rows, kv_heads, head_dim]; the arguments as for
+    ``kv4_write``.  ``rows`` or ``out`` gives the number of rows; rows behind
+    the last sequence are left as they were in ``out`` (zeros without it)."""
+    dev = cache.k_codes.device
+    if out is None:
+        if rows is None:
+            raise ValueError("rows or out is required")
+        make = torch.empty if row_starts is None else torch.zeros
+        out = tuple(make((rows, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16, device=dev)
+                    for _ in range(2))
+    k, v = out
+    for x, what in ((k, "out[0]"), (v, "out[1]")):
+        _kv4_rows(x, cache.kv_heads, cache, what)
+    if k.shape[0] != v.shape[0] or (rows is not None and rows != k.shape[0]):
+        raise ValueError("the outputs must have the same rows")
+    _require_cuda(k, v)
+    batch = _kv4_batch(cache, k.shape[0], seq_lens, page_table, row_starts, None)
+    with torch.cuda.device(dev):
+        _check(lib.wq_kv4_read(ctypes.byref(cache._struct()), ctypes.byref(batch), _ptr(k),
+                               _ptr(v), _stream(dev)), "wq_kv4_read")
+    return k, v
+
+
+def kv4_workspace(device: torch.device | str = "cuda") -> torch.Tensor:
+    """A zero-filled ``wq_kv4_attention`` workspace.  One serves all calls of a
+    stream; calls that may run at the same time need one each."""
+    return torch.zeros(lib.wq_kv4_attention_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def kv4_attention(q: torch.Tensor, cache: KV4Cache, seq_lens: torch.Tensor,
+                  page_table: torch.Tensor, row_starts: torch.Tensor | None = None,
+                  max_rows: int | None = None, scale: float | None = None,
+                  out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """``wq_kv4_attention``: causal attention of the rows' queries, bfloat16
+    [rows, q_heads, head_dim], over their sequences' cached tokens (the rows'
+    own included: write them first).
+
+    ``max_rows`` bounds the rows of one sequence where ``row_starts`` is given
+    (it chooses the kernel; the result does not depend on it).  ``scale`` is
+    1/sqrt(head_dim) by default.  ``workspace`` is a ``kv4_workspace`` that the
+    caller keeps, for instance in a captured graph; without it each call makes
+    its own.  Rows behind the last sequence are left as they were in ``out``
+    (zeros without it)."""
+    qs = _kv4_rows(q, None, cache, "q")
+    dev = cache.k_codes.device
+    if out is None:
+        make = torch.empty if row_starts is None else torch.zeros
+        out = make(q.shape, dtype=torch.bfloat16, device=dev)
+    os_ = _kv4_rows(out, q.shape[1], cache, "out")
+    if out.shape[0] != q.shape[0]:
+        raise ValueError("out must have the rows of q")
+    if q.shape[1] % cache.kv_heads or q.shape[1] == 0:
+        raise ValueError("q_heads must be a multiple of kv_heads")
+    if workspace is None:
+        workspace = kv4_workspace(dev)
+    _require_cuda(cache.k_codes, workspace)
+    batch = _kv4_batch(cache, q.shape[0], seq_lens, page_table, row_starts, max_rows)
+    with torch.cuda.device(dev):
+        _check(lib.wq_kv4_attention(
+            _ptr(q), qs, q.shape[1], ctypes.byref(cache._struct()), ctypes.byref(batch),
+            1.0 / math.sqrt(cache.head_dim) if scale is None else float(scale), _ptr(out), os_,
+            _ptr(workspace), workspace.nbytes, _stream(dev)), "wq_kv4_attention")
+    return out
 
 
 def matmul_noalloc(X: torch.Tensor, qw: QuantizedWeight, out_dtype: torch.dtype = torch.float32,

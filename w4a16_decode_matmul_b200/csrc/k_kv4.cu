@@ -1,0 +1,150 @@
+// k_kv4.cu -- launchers of the 4-bit key/value cache's kernels: rows in,
+// rows out, and attention of a few rows per sequence.
+#include <algorithm>
+#include <cmath>
+
+#include "kv4_host.h"
+#include "kv4.cuh"
+#include "kv4_attn.cuh"
+
+namespace wqh {
+namespace {
+
+namespace kv4 = wq::kv4;
+
+kv4::Cache device_cache(const wq_kv4_cache& c) {
+  kv4::Cache d = {};
+  d.k_codes = static_cast<uint8_t*>(c.k_codes);
+  d.k_meta = static_cast<__half2*>(c.k_meta);
+  d.v_codes = static_cast<uint8_t*>(c.v_codes);
+  d.v_meta = static_cast<__half2*>(c.v_meta);
+  d.pages = c.pages;
+  while ((1 << d.page_shift) < c.page_size) ++d.page_shift;
+  d.kv_heads = c.kv_heads;
+  return d;
+}
+
+kv4::Batch device_batch(const wq_kv4_batch& b, int page_size) {
+  kv4::Batch d = {};
+  d.row_starts = b.row_starts;
+  d.seq_lens = b.seq_lens;
+  d.page_table = b.page_table;
+  d.table_stride = b.table_stride;
+  d.seqs = b.seqs;
+  d.rows = b.rows;
+  d.rows_per_seq = b.row_starts ? 0 : b.rows / b.seqs;
+  d.max_len = int(std::min<int64_t>(int64_t(b.table_width) * page_size, 0x7fffff00));
+  return d;
+}
+
+// Calls every (head dim, group) the cache supports through F<D, G>::run.
+template <template <int, int> class F, typename... Args>
+cudaError_t dispatch_kv4(int head_dim, int group, const Args&... args) {
+#define WQ_CASE(D, G) \
+  if (head_dim == D && group == G) return F<D, G>::run(args...);
+  WQ_CASE(64, 32) WQ_CASE(64, 64)
+  WQ_CASE(128, 32) WQ_CASE(128, 64) WQ_CASE(128, 128)
+#undef WQ_CASE
+  return cudaErrorInvalidValue;
+}
+
+// Warps per row (each takes up to kRowIterations * 32 pieces of 8 elements),
+// and the CTAs that all rows make.
+int row_chunks(const wq_kv4_cache& c) {
+  const int pieces = c.kv_heads * (c.head_dim / 8), per_warp = kv4::kRowIterations * 32;
+  return (pieces + per_warp - 1) / per_warp;
+}
+
+int64_t row_ctas(const wq_kv4_cache& c, int rows) {
+  return (int64_t(rows) * row_chunks(c) + kv4::kRowWarps - 1) / kv4::kRowWarps;
+}
+
+template <int D, int G>
+struct WriteOp {
+  static cudaError_t run(const void* K, int64_t ks, const void* V, int64_t vs,
+                         const wq_kv4_cache& c, const wq_kv4_batch& b, cudaStream_t s) {
+    const int64_t ctas = row_ctas(c, b.rows);
+    if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    kv4::write_kernel<D, G><<<unsigned(ctas), kv4::kRowWarps * 32, 0, s>>>(
+        static_cast<const __nv_bfloat16*>(K), ks, static_cast<const __nv_bfloat16*>(V), vs,
+        device_cache(c), device_batch(b, c.page_size), row_chunks(c));
+    return cudaGetLastError();
+  }
+};
+
+template <int D, int G>
+struct ReadOp {
+  static cudaError_t run(const wq_kv4_cache& c, const wq_kv4_batch& b, void* K, void* V,
+                         cudaStream_t s) {
+    const int64_t ctas = row_ctas(c, b.rows);
+    if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    kv4::read_kernel<D, G><<<unsigned(ctas), kv4::kRowWarps * 32, 0, s>>>(
+        device_cache(c), device_batch(b, c.page_size), static_cast<__nv_bfloat16*>(K),
+        static_cast<__nv_bfloat16*>(V), row_chunks(c));
+    return cudaGetLastError();
+  }
+};
+
+template <int D, int G, int NT, int WARPS>
+cudaError_t launch_attn(const kv4::AttnParams& p, cudaStream_t s, int sms) {
+  using C = kv4::AttnConfig<D, G, NT, WARPS>;
+  constexpr size_t smem = C::kOffCtl + sizeof(kv4::AttnControl<WARPS>);
+  static_assert(smem <= 232448, "shared memory of one CTA");
+  static int configured[kMaxDevices] = {};
+  auto kernel = kv4::attn_kernel<D, G, NT, WARPS>;
+  const cudaError_t e = configure_smem(kernel, configured, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<unsigned(std::min(sms, kv4::kMaxCtas)), C::kThreads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D, int G>
+struct AttnOp {
+  static cudaError_t run(const kv4::AttnParams& p, int max_columns, cudaStream_t s, int sms) {
+    if (max_columns <= 8) return launch_attn<D, G, 1, 16>(p, s, sms);
+    return launch_attn<D, G, 2, 8>(p, s, sms);
+  }
+};
+
+constexpr size_t kCounterBytes = kv4::kMaxCtas * 4;
+
+}  // namespace
+
+size_t kv4_workspace_bytes() {
+  constexpr size_t partial = kv4::AttnConfig<128, 32, 2, 8>::kPartialBytes;
+  return round_up(kCounterBytes, 256) + partial;
+}
+
+cudaError_t run_kv4_write(const void* K, int64_t k_stride, const void* V, int64_t v_stride,
+                          const wq_kv4_cache& cache, const wq_kv4_batch& batch, cudaStream_t s) {
+  return dispatch_kv4<WriteOp>(cache.head_dim, cache.group, K, k_stride, V, v_stride, cache,
+                               batch, s);
+}
+
+cudaError_t run_kv4_read(const wq_kv4_cache& cache, const wq_kv4_batch& batch, void* K, void* V,
+                         cudaStream_t s) {
+  return dispatch_kv4<ReadOp>(cache.head_dim, cache.group, cache, batch, K, V, s);
+}
+
+cudaError_t run_kv4_attention(const void* Q, int64_t q_stride, int q_heads,
+                              const wq_kv4_cache& cache, const wq_kv4_batch& batch, float scale,
+                              void* O, int64_t o_stride, void* workspace, cudaStream_t s,
+                              const DeviceInfo& dev) {
+  kv4::AttnParams p = {};
+  p.cache = device_cache(cache);
+  p.batch = device_batch(batch, cache.page_size);
+  p.Q = static_cast<const __nv_bfloat16*>(Q);
+  p.q_stride = q_stride;
+  p.O = static_cast<__nv_bfloat16*>(O);
+  p.o_stride = o_stride;
+  p.gqa = q_heads / cache.kv_heads;
+  p.scale_log2 = float(double(scale) * 1.4426950408889634);
+  p.arrived = static_cast<unsigned*>(workspace);
+  p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
+                                       round_up(kCounterBytes, 256));
+  const int64_t max_rows = batch.row_starts ? batch.max_rows : batch.rows / batch.seqs;
+  const int max_columns = int(std::min<int64_t>(max_rows * p.gqa, 1 << 20));
+  return dispatch_kv4<AttnOp>(cache.head_dim, cache.group, p, max_columns, s, dev.sms);
+}
+
+}  // namespace wqh

@@ -4,12 +4,14 @@
 // kernel family is planned and launched in its own translation unit
 // (k_*.cu).
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
 
 #include "wq.h"
 #include "host.h"
+#include "kv4_host.h"
 #include "common.cuh"
 #include "stream.cuh"
 
@@ -471,6 +473,102 @@ wq_status wq_q4k_matmul_ex(const void* X, int64_t M, const void* blocks, int64_t
 wq_status wq_q4k_matmul(const void* X, int64_t M, const void* blocks, int64_t N, int64_t K,
                         void* Y, int out_dtype, wq_stream_t stream) {
   return wq_q4k_matmul_ex(X, M, blocks, N, K, Y, out_dtype, 0u, stream);
+}
+
+// ------------------------------------------------- key/value cache in 4 bits
+
+}  // extern "C"
+
+namespace {
+
+wq_status check_kv4_cache(const wq_kv4_cache* c) {
+  if (!c || !c->k_codes || !c->k_meta || !c->v_codes || !c->v_meta) return WQ_ERR_INVALID_ARG;
+  if (c->pages < 1 || c->pages >= (int64_t(1) << 31) || c->kv_heads < 1 ||
+      c->kv_heads > (1 << 20) || c->page_size < 1 || c->head_dim < 1 || c->group < 1)
+    return WQ_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128) return WQ_ERR_UNSUPPORTED;
+  if (c->group != 32 && c->group != 64 && c->group != 128) return WQ_ERR_UNSUPPORTED;
+  if (c->group > c->head_dim) return WQ_ERR_INVALID_ARG;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)) != 0)
+    return WQ_ERR_UNSUPPORTED;
+  if (!aligned16(c->k_codes) || !aligned16(c->k_meta) || !aligned16(c->v_codes) ||
+      !aligned16(c->v_meta))
+    return WQ_ERR_ALIGNMENT;
+  return WQ_OK;
+}
+
+// Of a batch with rows > 0 (the callers return before this otherwise).
+wq_status check_kv4_batch(const wq_kv4_batch* b) {
+  if (b->seqs < 1 || !b->seq_lens || !b->page_table) return WQ_ERR_INVALID_ARG;
+  if (b->table_width < 1 || b->table_stride < b->table_width) return WQ_ERR_INVALID_ARG;
+  if (!b->row_starts && b->rows % b->seqs != 0) return WQ_ERR_INVALID_ARG;
+  if (b->max_rows < 0) return WQ_ERR_INVALID_ARG;
+  return WQ_OK;
+}
+
+// A packed row tensor: [rows][heads][head_dim] with a stride in elements.
+wq_status check_kv4_rows(const void* p, int64_t stride, int64_t heads, int head_dim) {
+  if (!p || stride < heads * head_dim) return WQ_ERR_INVALID_ARG;
+  if (!aligned16(p) || stride % 8 != 0) return WQ_ERR_ALIGNMENT;
+  return WQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+wq_status wq_kv4_write(const void* K, int64_t k_stride, const void* V, int64_t v_stride,
+                       const wq_kv4_cache* cache, const wq_kv4_batch* batch,
+                       wq_stream_t stream) {
+  wq_status st = check_kv4_cache(cache);
+  if (st != WQ_OK) return st;
+  if (!batch || batch->rows < 0) return WQ_ERR_INVALID_ARG;
+  if (batch->rows == 0) return WQ_OK;
+  if ((st = check_kv4_batch(batch)) != WQ_OK) return st;
+  if ((st = check_kv4_rows(K, k_stride, cache->kv_heads, cache->head_dim)) != WQ_OK) return st;
+  if ((st = check_kv4_rows(V, v_stride, cache->kv_heads, cache->head_dim)) != WQ_OK) return st;
+  return from_cuda(wqh::run_kv4_write(K, k_stride, V, v_stride, *cache, *batch,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+wq_status wq_kv4_read(const wq_kv4_cache* cache, const wq_kv4_batch* batch, void* K, void* V,
+                      wq_stream_t stream) {
+  wq_status st = check_kv4_cache(cache);
+  if (st != WQ_OK) return st;
+  if (!batch || batch->rows < 0) return WQ_ERR_INVALID_ARG;
+  if (batch->rows == 0) return WQ_OK;
+  if ((st = check_kv4_batch(batch)) != WQ_OK) return st;
+  if (!K || !V) return WQ_ERR_INVALID_ARG;
+  if (!aligned16(K) || !aligned16(V)) return WQ_ERR_ALIGNMENT;
+  return from_cuda(wqh::run_kv4_read(*cache, *batch, K, V,
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t wq_kv4_attention_workspace_bytes(void) { return wqh::kv4_workspace_bytes(); }
+
+wq_status wq_kv4_attention(const void* Q, int64_t q_stride, int32_t q_heads,
+                           const wq_kv4_cache* cache, const wq_kv4_batch* batch, float scale,
+                           void* O, int64_t o_stride, void* workspace, size_t workspace_bytes,
+                           wq_stream_t stream) {
+  wq_status st = check_kv4_cache(cache);
+  if (st != WQ_OK) return st;
+  if (!batch || batch->rows < 0 || q_heads < 1 || q_heads % cache->kv_heads != 0 ||
+      !std::isfinite(scale))
+    return WQ_ERR_INVALID_ARG;
+  if (batch->rows == 0) return WQ_OK;
+  if ((st = check_kv4_batch(batch)) != WQ_OK) return st;
+  // a row index times the heads of its group stays inside 32 bits
+  if (int64_t(batch->rows) * (q_heads / cache->kv_heads) >= (int64_t(1) << 30))
+    return WQ_ERR_INVALID_ARG;
+  if ((st = check_kv4_rows(Q, q_stride, q_heads, cache->head_dim)) != WQ_OK) return st;
+  if ((st = check_kv4_rows(O, o_stride, q_heads, cache->head_dim)) != WQ_OK) return st;
+  if (!workspace || workspace_bytes < wqh::kv4_workspace_bytes()) return WQ_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return WQ_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  if (!wqh::device_info(&dev)) return WQ_ERR_CUDA;
+  return from_cuda(wqh::run_kv4_attention(Q, q_stride, q_heads, *cache, *batch, scale, O,
+                                          o_stride, workspace,
+                                          reinterpret_cast<cudaStream_t>(stream), dev));
 }
 
 }  // extern "C"
