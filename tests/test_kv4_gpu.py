@@ -12,6 +12,7 @@ pytestmark = pytest.mark.gpu
 
 FORMATS = [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128)]
 SENTINEL = 0xA5
+COUNTERS = 160 * 16 * 4        # bytes of the attention workspace's counters
 
 
 def new_cache(pages, heads, d, page, group):
@@ -195,7 +196,7 @@ def run_attention(d, group, page, heads, gqa, lens, rows, seed=0, strong=8.0, sc
                              workspace=ws)
     torch.cuda.synchronize()
     assert wq().get_device_error() == 0
-    assert not ws[:640].any(), "the workspace's counters are not zero again"
+    assert not ws[:COUNTERS].any(), "the workspace's counters are not zero again"
     s = d ** -0.5 if scale is None else scale
     o, bound = reference(q, cache, lens, rows, table, s)
     ref.check(got, o, bound)
@@ -340,7 +341,7 @@ def test_repeated_and_captured_calls_give_the_same_bits():
     torch.cuda.synchronize()
     o, e = reference(q, cache, [1500, 39, 1], [1, 1, 1], table, 128 ** -0.5)
     ref.check(out, o, e)
-    assert not ws[:640].any()
+    assert not ws[:COUNTERS].any()
 
 
 def test_two_streams_with_a_workspace_each():

@@ -325,7 +325,7 @@ def q4k_matmul(X: torch.Tensor, blocks: torch.Tensor, N: int, K: int,
     return Y
 
 
-@dataclasses.dataclass
+@dataclasses.dataclass(frozen=True)
 class KV4Cache:
     """A pool of pages of keys and values in 4 bits (see ``include/wq.h``):
     codes uint8 [pages, kv_heads, page_size, head_dim/2] and (scale, zero)
@@ -349,6 +349,9 @@ class KV4Cache:
         for m in (self.k_meta, self.v_meta):
             if m.dtype != torch.float16 or tuple(m.shape) != meta:
                 raise ValueError(f"metadata must be float16 {list(meta)}")
+        # the format as the C ABI takes it; the addresses are set at each call
+        object.__setattr__(self, "_c", _KV4CacheStruct(
+            0, 0, 0, 0, self.pages, self.page_size, self.kv_heads, self.head_dim, self.group))
 
     @property
     def pages(self) -> int:
@@ -372,9 +375,10 @@ class KV4Cache:
                 + self.v_meta.nbytes)
 
     def _struct(self) -> _KV4CacheStruct:
-        return _KV4CacheStruct(self.k_codes.data_ptr(), self.k_meta.data_ptr(),
-                               self.v_codes.data_ptr(), self.v_meta.data_ptr(), self.pages,
-                               self.page_size, self.kv_heads, self.head_dim, self.group)
+        c = self._c
+        c.k_codes, c.k_meta = self.k_codes.data_ptr(), self.k_meta.data_ptr()
+        c.v_codes, c.v_meta = self.v_codes.data_ptr(), self.v_meta.data_ptr()
+        return c
 
 
 def kv4_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, group: int = 64,
@@ -396,38 +400,55 @@ def kv4_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, gro
 def _kv4_batch(cache: KV4Cache, rows: int, seq_lens, page_table, row_starts, max_rows):
     """The batch struct after the checks the C ABI cannot make (types, shapes
     and devices of the int32 arrays)."""
-    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1:
-        raise ValueError("seq_lens must be a 1-D int32 tensor")
+    dev = cache.k_codes.device
+    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be a contiguous 1-D int32 tensor")
     seqs = seq_lens.shape[0]
     if (page_table.dtype != torch.int32 or page_table.dim() != 2
             or page_table.shape[0] != seqs):
         raise ValueError("page_table must be an int32 tensor [sequences, pages]")
-    if page_table.shape[1] > 1 and page_table.stride(1) != 1:
-        raise ValueError("rows of page_table must be contiguous")
-    if row_starts is not None and (row_starts.dtype != torch.int32
-                                   or tuple(row_starts.shape) != (seqs + 1,)):
-        raise ValueError("row_starts must be an int32 tensor [sequences + 1]")
-    _require_cuda(cache.k_codes, seq_lens, row_starts)
-    if page_table.device != cache.k_codes.device:
-        raise ValueError("page_table is on another device than the cache")
     width = page_table.shape[1]
-    return _KV4BatchStruct(seqs, rows, None if row_starts is None else row_starts.data_ptr(),
-                           seq_lens.data_ptr(), page_table.data_ptr(), width,
-                           page_table.stride(0) if seqs > 1 else width,
-                           int(max_rows) if max_rows is not None else 0)
+    stride, step = page_table.stride()
+    if width > 1 and step != 1:
+        raise ValueError("rows of page_table must be contiguous")
+    if seq_lens.device != dev or page_table.device != dev:
+        raise ValueError("seq_lens and page_table must be on the cache's device")
+    starts = None
+    if row_starts is not None:
+        if (row_starts.dtype != torch.int32 or row_starts.shape != (seqs + 1,)
+                or not row_starts.is_contiguous()):
+            raise ValueError("row_starts must be a contiguous int32 tensor [sequences + 1]")
+        if row_starts.device != dev:
+            raise ValueError("row_starts must be on the cache's device")
+        starts = row_starts.data_ptr()
+    return _KV4BatchStruct(seqs, rows, starts, seq_lens.data_ptr(), page_table.data_ptr(), width,
+                           stride if seqs > 1 else width, max_rows or 0)
 
 
 def _kv4_rows(x: torch.Tensor, heads: int | None, cache: KV4Cache, what: str) -> int:
     """The row stride in elements of a bfloat16 tensor [rows, heads, head_dim]
     whose heads are contiguous (a slice of a fused projection's rows, say)."""
-    if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[2] != cache.head_dim or (
-            heads is not None and x.shape[1] != heads):
-        raise ValueError(f"{what} must be bfloat16 [rows, {heads or 'heads'}, {cache.head_dim}]")
+    shape = x.shape
+    d = cache._c.head_dim
+    if x.dtype != torch.bfloat16 or len(shape) != 3 or shape[2] != d or (
+            heads is not None and shape[1] != heads):
+        raise ValueError(f"{what} must be bfloat16 [rows, {heads or 'heads'}, {d}]")
     if x.device != cache.k_codes.device:
         raise ValueError(f"{what} is on another device than the cache")
-    if x.numel() and (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2])):
+    row, head, step = x.stride()
+    if x.numel() and (step != 1 or (shape[1] > 1 and head != d)):
         raise ValueError(f"the heads of a row of {what} must be contiguous")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+    return row if shape[0] > 1 else shape[1] * d
+
+
+def _on(device: torch.device, call, *args) -> int:
+    """call(*args, the device's current stream) with the device current."""
+    index = device.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
+        return call(*args, stream)
+    with torch.cuda.device(device):
+        return call(*args, stream)
 
 
 def kv4_write(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, seq_lens: torch.Tensor,
@@ -438,15 +459,13 @@ def kv4_write(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, seq_lens: torch
     seq_lens int32 [seqs] counts the tokens with the new rows included;
     page_table int32 [seqs, width]; row_starts int32 [seqs + 1] gives the rows
     of each sequence (None: rows/seqs each).  All on the GPU."""
-    ks = _kv4_rows(k, cache.kv_heads, cache, "k")
-    vs = _kv4_rows(v, cache.kv_heads, cache, "v")
+    ks = _kv4_rows(k, cache._c.kv_heads, cache, "k")
+    vs = _kv4_rows(v, cache._c.kv_heads, cache, "v")
     if k.shape[0] != v.shape[0]:
         raise ValueError("k and v must have the same rows")
     batch = _kv4_batch(cache, k.shape[0], seq_lens, page_table, row_starts, None)
-    dev = cache.k_codes.device
-    with torch.cuda.device(dev):
-        _check(lib.wq_kv4_write(_ptr(k), ks, _ptr(v), vs, ctypes.byref(cache._struct()),
-                                ctypes.byref(batch), _stream(dev)), "wq_kv4_write")
+    _check(_on(cache.k_codes.device, lib.wq_kv4_write, k.data_ptr(), ks, v.data_ptr(), vs,
+               cache._struct(), batch), "wq_kv4_write")
 
 
 def kv4_read(cache: KV4Cache, seq_lens: torch.Tensor, page_table: torch.Tensor,
@@ -465,14 +484,14 @@ def kv4_read(cache: KV4Cache, seq_lens: torch.Tensor, page_table: torch.Tensor,
                     for _ in range(2))
     k, v = out
     for x, what in ((k, "out[0]"), (v, "out[1]")):
-        _kv4_rows(x, cache.kv_heads, cache, what)
+        _kv4_rows(x, cache._c.kv_heads, cache, what)
+        if not x.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
     if k.shape[0] != v.shape[0] or (rows is not None and rows != k.shape[0]):
         raise ValueError("the outputs must have the same rows")
-    _require_cuda(k, v)
     batch = _kv4_batch(cache, k.shape[0], seq_lens, page_table, row_starts, None)
-    with torch.cuda.device(dev):
-        _check(lib.wq_kv4_read(ctypes.byref(cache._struct()), ctypes.byref(batch), _ptr(k),
-                               _ptr(v), _stream(dev)), "wq_kv4_read")
+    _check(_on(dev, lib.wq_kv4_read, cache._struct(), batch, k.data_ptr(), v.data_ptr()),
+           "wq_kv4_read")
     return k, v
 
 
@@ -505,17 +524,16 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, seq_lens: torch.Tensor,
     os_ = _kv4_rows(out, q.shape[1], cache, "out")
     if out.shape[0] != q.shape[0]:
         raise ValueError("out must have the rows of q")
-    if q.shape[1] % cache.kv_heads or q.shape[1] == 0:
+    if q.shape[1] % cache._c.kv_heads or q.shape[1] == 0:
         raise ValueError("q_heads must be a multiple of kv_heads")
     if workspace is None:
         workspace = kv4_workspace(dev)
-    _require_cuda(cache.k_codes, workspace)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the cache's device")
     batch = _kv4_batch(cache, q.shape[0], seq_lens, page_table, row_starts, max_rows)
-    with torch.cuda.device(dev):
-        _check(lib.wq_kv4_attention(
-            _ptr(q), qs, q.shape[1], ctypes.byref(cache._struct()), ctypes.byref(batch),
-            1.0 / math.sqrt(cache.head_dim) if scale is None else float(scale), _ptr(out), os_,
-            _ptr(workspace), workspace.nbytes, _stream(dev)), "wq_kv4_attention")
+    _check(_on(dev, lib.wq_kv4_attention, q.data_ptr(), qs, q.shape[1], cache._struct(), batch,
+               1.0 / math.sqrt(cache._c.head_dim) if scale is None else float(scale),
+               out.data_ptr(), os_, workspace.data_ptr(), workspace.nbytes), "wq_kv4_attention")
     return out
 
 

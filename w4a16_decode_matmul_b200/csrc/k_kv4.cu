@@ -88,7 +88,7 @@ struct ReadOp {
 template <int D, int G, int NT, int WARPS>
 cudaError_t launch_attn(const kv4::AttnParams& p, cudaStream_t s, int sms) {
   using C = kv4::AttnConfig<D, G, NT, WARPS>;
-  constexpr size_t smem = C::kOffCtl + sizeof(kv4::AttnControl<WARPS>);
+  constexpr size_t smem = C::kOffCtl + C::kCtlBytes;
   static_assert(smem <= 232448, "shared memory of one CTA");
   static int configured[kMaxDevices] = {};
   auto kernel = kv4::attn_kernel<D, G, NT, WARPS>;
@@ -101,12 +101,19 @@ cudaError_t launch_attn(const kv4::AttnParams& p, cudaStream_t s, int sms) {
 template <int D, int G>
 struct AttnOp {
   static cudaError_t run(const kv4::AttnParams& p, int max_columns, cudaStream_t s, int sms) {
-    if (max_columns <= 8) return launch_attn<D, G, 1, 16>(p, s, sms);
+    if (max_columns <= 8) return launch_attn<D, G, 1, 12>(p, s, sms);
     return launch_attn<D, G, 2, 8>(p, s, sms);
   }
 };
 
-constexpr size_t kCounterBytes = kv4::kMaxCtas * 4;
+kv4::FastDiv fast_div(uint32_t d) {
+  uint32_t shift = 0;
+  while ((uint64_t(1) << shift) < d) ++shift;
+  const uint64_t one = uint64_t(1) << 32;
+  return {uint32_t(one * ((uint64_t(1) << shift) - d) / d + 1), shift};
+}
+
+constexpr size_t kCounterBytes = kv4::kMaxCtas * kv4::kMaxRows * 4;
 
 }  // namespace
 
@@ -138,6 +145,7 @@ cudaError_t run_kv4_attention(const void* Q, int64_t q_stride, int q_heads,
   p.O = static_cast<__nv_bfloat16*>(O);
   p.o_stride = o_stride;
   p.gqa = q_heads / cache.kv_heads;
+  p.by_gqa = fast_div(uint32_t(p.gqa));
   p.scale_log2 = float(double(scale) * 1.4426950408889634);
   p.arrived = static_cast<unsigned*>(workspace);
   p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +

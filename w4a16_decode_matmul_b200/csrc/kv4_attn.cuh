@@ -18,9 +18,10 @@
 // within 2^-21 of that magnitude.  The weights W_t = 2^(S_t - m) s'_{t,g} are
 // rounded to binary16 (half a step is 2^-11, an eighth of the output's bfloat16
 // half step).  m is the running maximum not of S_t but of S_t + log2 max_g
-// s'_{t,g}, so that the largest W_t is near 1 whatever the values' scale, and
-// it is raised only when a W_t would pass 2^8 (a warp vote; binary16 holds
-// 2^15).  Scores, sums, statistics and outputs are held in binary32.
+// s'_{t,g}, so that W_t fits binary16 whatever the values' scale, and
+// it is raised only when a W_t would pass 2^15 (a warp vote), then so that the
+// largest becomes 2^7: weights down to 2^-21 of the largest keep all their bits.
+// Scores, sums, statistics and outputs are held in binary32.
 //
 // Work split.  A unit is 32 tokens of one (sequence, block of rows, head); the
 // units of the whole batch, in that order, are cut into equal ranges for the
@@ -44,6 +45,15 @@ namespace kv4 {
 
 constexpr int kUnit = 32;      // tokens of a unit
 constexpr int kMaxCtas = 160;  // CTAs the workspace has room for
+constexpr int kMaxRows = 16;   // rows of a block
+
+// Quotient by a divisor known at launch, for 0 <= n < 2^31.
+struct FastDiv {
+  uint32_t mul, shift;
+  __device__ __forceinline__ int operator()(int n) const {
+    return int((__umulhi(uint32_t(n), mul) + uint32_t(n)) >> shift);
+  }
+};
 
 struct AttnParams {
   Cache cache;
@@ -53,8 +63,9 @@ struct AttnParams {
   __nv_bfloat16* O;  // [rows][q_heads][D], rows o_stride elements apart
   int64_t o_stride;
   int gqa;            // query heads per kv head
+  FastDiv by_gqa;
   float scale_log2;   // softmax scale times log2 e
-  unsigned* arrived;  // [kMaxCtas] zero counters
+  unsigned* arrived;  // [kMaxCtas][kMaxRows] zero counters
   float* partial;     // [2 kMaxCtas][piece]
 };
 
@@ -70,13 +81,17 @@ struct AttnConfig {
   // a piece: O [rows][D], m [rows], l [rows]
   static constexpr int kPieceFloats = kRows * (D + 2);
   static constexpr int kPieceBytes = kPieceFloats * 4;
-  // the last piece of a warp reuses its drained ring
-  static constexpr int kStages = D == 64 ? 4 : (WARPS == 8 ? 4 : 2);
+  static constexpr int kCtlBytes = 8192;
+  // as many stages of each warp's ring as fit, four at most; the last piece
+  // of a warp reuses its drained ring
+  static constexpr int kFit = (232448 - kCtlBytes) / WARPS - kPieceBytes;
+  static constexpr int kStages = kFit / kStageBytes < 4 ? kFit / kStageBytes : 4;
   static constexpr int kRingBytes = kStages * kStageBytes;
-  static_assert(kRingBytes >= kPieceBytes && kRingBytes % 16 == 0 && kPieceBytes % 16 == 0, "");
+  static_assert(kStages >= 2 && kRingBytes >= kPieceBytes && kRingBytes % 16 == 0 &&
+                    kPieceBytes % 16 == 0,
+                "");
   static constexpr int kOffHead = WARPS * kRingBytes;
-  static constexpr int kOffBars = kOffHead + WARPS * kPieceBytes;
-  static constexpr int kOffCtl = kOffBars + WARPS * kStages * 8;
+  static constexpr int kOffCtl = kOffHead + WARPS * kPieceBytes;
   static constexpr int kPartialBytes = 2 * kMaxCtas * kPieceBytes;
 };
 
@@ -85,37 +100,36 @@ struct AttnConfig {
 struct Segment {
   int b, rb, h;
   int row0, rows, len;  // of the sequence
+  int limit;            // tokens that some row of the block sees
   int units;            // of one head of this block of rows
   int64_t u0;
 };
 
 struct PieceInfo {
-  int valid;
-  int b, rb, h;
-  int row0, rows;
+  int rb, h, row0, rows;
   int64_t u0, u1;
 };
 
 template <int WARPS>
 struct AttnControl {
+  uint64_t full[WARPS][4];
   int64_t warp_sum[WARPS];
-  int64_t start_rem[WARPS];  // units from the start of sequence start_b
-  int start_b[WARPS];
-  int last[2];
+  int64_t upto[WARPS * 32];     // inclusive prefix of a thread inside its warp
+  unsigned has_head, has_tail;  // a bit per warp
   PieceInfo head[WARPS], tail[WARPS];
 };
 
-// Tokens that some row of block rb sees, and the units they make (one at
-// least, so that rows that see nothing are written too).
+// Tokens that some row of block rb sees.
 template <int ROWS>
-__device__ __forceinline__ int block_limit(const Sequence& s, int rb, int gqa) {
-  const int last = min(s.rows * gqa, (rb + 1) * ROWS) - 1;
-  return max(0, s.len - s.rows + last / gqa + 1);
+__device__ __forceinline__ int block_limit(const Sequence& s, int rb, const AttnParams& p) {
+  const int last = min(s.rows * p.gqa, (rb + 1) * ROWS) - 1;
+  return max(0, s.len - s.rows + p.by_gqa(last) + 1);
 }
 
-template <int ROWS>
-__device__ __forceinline__ int block_units(const Sequence& s, int rb, int gqa) {
-  return max(1, (block_limit<ROWS>(s, rb, gqa) + kUnit - 1) / kUnit);
+// The units they make: one at least, so that rows that see nothing are
+// written too.
+__device__ __forceinline__ int limit_units(int limit) {
+  return max(1, (limit + kUnit - 1) / kUnit);
 }
 
 template <int ROWS>
@@ -124,11 +138,10 @@ __device__ __forceinline__ int row_blocks(const Sequence& s, int gqa) {
 }
 
 template <int ROWS>
-__device__ __forceinline__ int64_t sequence_units(const AttnParams& p, int b) {
-  const Sequence s = load_sequence(p.batch, b);
+__device__ __forceinline__ int64_t sequence_units(const AttnParams& p, const Sequence& s) {
   int64_t n = 0;
   const int blocks = row_blocks<ROWS>(s, p.gqa);
-  for (int rb = 0; rb < blocks; ++rb) n += block_units<ROWS>(s, rb, p.gqa);
+  for (int rb = 0; rb < blocks; ++rb) n += limit_units(block_limit<ROWS>(s, rb, p));
   return n * p.cache.kv_heads;
 }
 
@@ -148,7 +161,8 @@ __device__ __forceinline__ void next_segment(const AttnParams& p, Segment& s) {
     s.rows = q.rows;
     s.len = q.len;
   }
-  s.units = block_units<ROWS>(q, s.rb, p.gqa);
+  s.limit = block_limit<ROWS>(q, s.rb, p);
+  s.units = limit_units(s.limit);
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -168,6 +182,11 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // Transpose of an 8x8 matrix of binary16 held as pairs (lane (g, t): row g,
 // columns 2t and 2t + 1).
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -178,15 +197,15 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 
 // N 32-bit words of shared memory in one load.
 template <int N>
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&r)[N]) {
+__device__ __forceinline__ void load_words(const unsigned char* p, uint32_t (&r)[N]) {
   if constexpr (N == 4) {
-    const uint4 v = lds128(addr);
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
     r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
   } else if constexpr (N == 2) {
-    const uint2 v = lds64(addr);
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
     r[0] = v.x, r[1] = v.y;
   } else {
-    r[0] = lds32(addr);
+    r[0] = *reinterpret_cast<const uint32_t*>(p);
   }
 }
 
@@ -194,10 +213,56 @@ __device__ __forceinline__ float2 meta_pair(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
-// The (row, query head) of a row r of a segment.
-__device__ __forceinline__ int64_t row_offset(int row0, int r, int h, int gqa, int64_t stride,
-                                              int D) {
-  return int64_t(row0 + r / gqa) * stride + int64_t(h * gqa + r % gqa) * D;
+// Offset of row r of the segment that begins at row0, of kv head h.
+__device__ __forceinline__ int64_t row_offset(const AttnParams& p, int row0, int r, int h,
+                                              int64_t stride, int D) {
+  const int i = p.by_gqa(r);
+  return int64_t(row0 + i) * stride + int64_t(h * p.gqa + (r - i * p.gqa)) * D;
+}
+
+// The segment that unit q belongs to, and q's place in it, for a warp that
+// asks with all its lanes: the block's threads have left the prefix sums of
+// their sequences' units in shared memory.
+template <int ROWS, int WARPS>
+__device__ __forceinline__ int find_segment(const AttnParams& p, const AttnControl<WARPS>& ctl,
+                                            int per_thread, int64_t q, int lane, Segment* out) {
+  int64_t sum = lane < WARPS ? ctl.warp_sum[lane] : 0;
+  const int64_t own = sum;
+#pragma unroll
+  for (int m = 1; m < 32; m *= 2) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, sum, m);
+    if (lane >= m) sum += v;
+  }
+  const int w = __ffs(__ballot_sync(0xffffffffu, sum > q)) - 1;
+  int64_t rem = q - __shfl_sync(0xffffffffu, sum - own, w);
+  const int64_t upto = ctl.upto[w * 32 + lane];
+  const int i = __ffs(__ballot_sync(0xffffffffu, upto > rem)) - 1;
+  const int64_t before = __shfl_up_sync(0xffffffffu, upto, 1);
+  if (i > 0) rem -= __shfl_sync(0xffffffffu, before, i);
+  Segment s;
+  s.b = (w * 32 + i) * per_thread;
+  Sequence seq = load_sequence(p.batch, s.b);
+  while (per_thread > 1) {
+    const int64_t n = sequence_units<ROWS>(p, seq);
+    if (rem < n) break;
+    rem -= n;
+    seq = load_sequence(p.batch, ++s.b);
+  }
+  s.row0 = seq.row0;
+  s.rows = seq.rows;
+  s.len = seq.len;
+  for (s.rb = 0;; ++s.rb) {
+    s.limit = block_limit<ROWS>(seq, s.rb, p);
+    s.units = limit_units(s.limit);
+    const int64_t n = int64_t(s.units) * p.cache.kv_heads;
+    if (rem < n) break;
+    rem -= n;
+  }
+  s.h = rem < (int64_t(1) << 31) ? int(uint32_t(rem) / uint32_t(s.units)) : int(rem / s.units);
+  const int unit = int(rem - int64_t(s.h) * s.units);
+  s.u0 = q - unit;
+  *out = s;
+  return unit;
 }
 
 template <int D, int G, int NT, int WARPS>
@@ -205,165 +270,146 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
   using C = AttnConfig<D, G, NT, WARPS>;
   constexpr int NC = C::kChunks, NG = C::kGroups, ROWS = C::kRows, NS = C::kStages;
   constexpr int kChunksPerGroup = G / 32;
+  static_assert(sizeof(AttnControl<WARPS>) <= C::kCtlBytes, "");
   extern __shared__ __align__(128) unsigned char smem[];
   auto* ctl = reinterpret_cast<AttnControl<WARPS>*>(smem + C::kOffCtl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int gqa = p.gqa;
-  unsigned char* ring = smem + warp * C::kRingBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBars) + warp * NS;
-  if (lane == 0) {
-    for (int s = 0; s < NS; ++s) mbar_init(&bars[s], 1);
-    fence_mbar_init();
-    ctl->head[warp].valid = 0;
-    ctl->tail[warp].valid = 0;
-  }
 
-  // ---- this CTA's and its warps' ranges of units.  Thread i counts the units
-  // of a contiguous range of sequences; the thread whose range holds a warp's
-  // first unit finds its sequence.
+  // ---- the units of the batch: thread i counts those of a contiguous range
+  // of sequences
   const int per_thread = (p.batch.seqs + C::kThreads - 1) / C::kThreads;
   const int b_begin = min(p.batch.seqs, tid * per_thread);
   const int b_end = min(p.batch.seqs, b_begin + per_thread);
-  int64_t own = 0;
-  for (int b = b_begin; b < b_end; ++b) own += sequence_units<ROWS>(p, b);
-  int64_t upto = own;  // inclusive prefix
+  int64_t upto = 0;
+  for (int b = b_begin; b < b_end; ++b)
+    upto += sequence_units<ROWS>(p, load_sequence(p.batch, b));
+  if (tid < WARPS * NS) {
+    mbar_init(&ctl->full[tid / NS][tid % NS], 1);
+    fence_mbar_init();
+  }
+  if (tid == 0) ctl->has_head = ctl->has_tail = 0u;
 #pragma unroll
   for (int m = 1; m < 32; m *= 2) {
     const int64_t v = __shfl_up_sync(0xffffffffu, upto, m);
     if (lane >= m) upto += v;
   }
+  ctl->upto[tid] = upto;
   if (lane == 31) ctl->warp_sum[warp] = upto;
   __syncthreads();
   int64_t total = 0;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    if (w < warp) upto += ctl->warp_sum[w];
-    total += ctl->warp_sum[w];
-  }
-  // one unit per warp at least, where the batch has fewer units than warps
-  const int64_t ctas = min(int64_t(gridDim.x), (total + WARPS - 1) / WARPS);
+  for (int w = 0; w < WARPS; ++w) total += ctl->warp_sum[w];
+
+  // ---- this CTA's range (one unit per warp at least, where the batch has
+  // fewer units than warps; the first `extra` CTAs have one more than the
+  // others), and its warps'
+  const int ctas = int(min(int64_t(gridDim.x), (total + WARPS - 1) / WARPS));
   const int cta = blockIdx.x;
   if (cta >= ctas) return;
-  const int64_t r0 = cta * total / ctas, r1 = (cta + 1) * total / ctas;
-  auto warp_begin = [&](int w) { return r0 + w * (r1 - r0) / WARPS; };
-  if (own > 0) {
-    for (int w = 0; w < WARPS; ++w) {
-      const int64_t q = warp_begin(w);
-      if (q < upto - own || q >= upto) continue;
-      int64_t rem = q - (upto - own);
-      int b = b_begin;
-      for (;; ++b) {
-        const int64_t n = sequence_units<ROWS>(p, b);
-        if (rem < n) break;
-        rem -= n;
-      }
-      ctl->start_b[w] = b;
-      ctl->start_rem[w] = rem;
-    }
-  }
-  __syncthreads();
-  const int64_t q0 = warp_begin(warp), q1 = warp_begin(warp + 1);
+  const bool narrow = total < (int64_t(1) << 31);
+  const int64_t per_cta = narrow ? int64_t(uint32_t(total) / uint32_t(ctas)) : total / ctas;
+  const int extra = int(total - per_cta * ctas);
+  const int64_t r0 = cta * per_cta + min(cta, extra);
+  const int n_cta = int(per_cta) + (cta < extra ? 1 : 0);
+  const int64_t r1 = r0 + n_cta;
+  const int per_warp = n_cta / WARPS, extra_warps = n_cta - per_warp * WARPS;
+  auto warp_begin = [&](int w) { return r0 + w * per_warp + min(w, extra_warps); };
 
-  if (q0 < q1) {
-    // ---- the first segment
-    Segment pf;  // of the next unit to copy
-    int pf_unit;
-    {
-      pf.b = ctl->start_b[warp];
-      int64_t rem = ctl->start_rem[warp];
-      const Sequence s = load_sequence(p.batch, pf.b);
-      pf.row0 = s.row0;
-      pf.rows = s.rows;
-      pf.len = s.len;
-      pf.rb = 0;
-      for (;; ++pf.rb) {
-        pf.units = block_units<ROWS>(s, pf.rb, gqa);
-        const int64_t n = int64_t(pf.units) * p.cache.kv_heads;
-        if (rem < n) break;
-        rem -= n;
-      }
-      pf.h = int(rem / pf.units);
-      pf_unit = int(rem % pf.units);
-      pf.u0 = q0 - pf_unit;
-    }
-    Segment cs = pf;  // of the unit being computed
-    int cs_unit = pf_unit;
+  const int64_t q0 = warp_begin(warp);
+  const int n_units = per_warp + (warp < extra_warps ? 1 : 0);
+  if (n_units > 0) {
+    const int64_t q1 = q0 + n_units;
+    unsigned char* const ring = smem + warp * C::kRingBytes;
+    Segment cs;  // of the unit being computed
+    int unit = find_segment<ROWS>(p, *ctl, per_thread, q0, lane, &cs);
 
-    const int sub_shift = min(p.cache.page_shift, 5);  // a copy stays inside one page
-    const int sub_tokens = 1 << sub_shift;
-    const uint32_t smem_ring = smem_addr(ring);
+    // ---- copies.  Lane 4 sub + kind copies the codes or metadata of one run
+    // of tokens inside a page; page numbers are read one unit ahead.
+    Segment pf = cs;  // of the next unit to copy
+    int pf_unit = unit, to_copy = n_units, pf_page = 0;
+    const int sub_shift = min(p.cache.page_shift, 5);
+    const int kind = lane & 3, sub = lane >> 2;
+    const uint32_t row_bytes = kind & 1 ? NG * 4 : D / 2;
+    const unsigned char* const copy_src =
+        kind == 0   ? p.cache.k_codes
+        : kind == 1 ? reinterpret_cast<const unsigned char*>(p.cache.k_meta)
+        : kind == 2 ? p.cache.v_codes
+                    : reinterpret_cast<const unsigned char*>(p.cache.v_meta);
+    unsigned char* const copy_dst = ring + (kind >> 1) * (C::kCodeBytes + C::kMetaBytes) +
+                                    (kind & 1) * C::kCodeBytes +
+                                    (sub << sub_shift) * int(row_bytes);
     const uint64_t policy = l2_policy_evict_first();
-    int64_t to_copy = q1 - q0;
-
-    // Starts the copies of the next unit into stage `s`: lane 4 sub + kind
-    // copies the codes or metadata of one run of tokens inside a page.
+    auto read_page = [&] {
+      const int pos = pf_unit * kUnit + (sub << sub_shift);
+      if (sub < (kUnit >> sub_shift) && pos < pf.limit)
+        pf_page = p.batch.page_table[int64_t(pf.b) * p.batch.table_stride +
+                                     (pos >> p.cache.page_shift)];
+    };
     auto copy_unit = [&](int s) {
-      const Sequence seq = {pf.row0, pf.rows, pf.len};
-      const int limit = block_limit<ROWS>(seq, pf.rb, gqa);
       const int tok0 = pf_unit * kUnit;
-      const int subs = min(kUnit >> sub_shift, (limit - tok0 + sub_tokens - 1) >> sub_shift);
-      const int kind = lane & 3, sub = lane >> 2;
-      const uint32_t row_bytes = kind & 1 ? NG * 4 : D / 2;
-      if (lane == 0) {
-        const uint32_t bytes =
-            uint32_t(max(subs, 0)) * uint32_t(sub_tokens) * uint32_t(2 * (NG * 4 + D / 2));
-        mbar_arrive_expect_tx(&bars[s], bytes);
-      }
+      const int subs = max(0, min(kUnit >> sub_shift,
+                                  (pf.limit - tok0 + (1 << sub_shift) - 1) >> sub_shift));
+      if (lane == 0)
+        mbar_arrive_expect_tx(&ctl->full[warp][s],
+                              uint32_t(subs) * uint32_t((2 * (NG * 4 + D / 2)) << sub_shift));
       __syncwarp();
       if (sub < subs) {
-        const int pos = tok0 + sub * sub_tokens;
-        int64_t page = load_page(p.batch, p.cache, pf.b, pos);
-        if (page < 0) page = 0;  // recorded; any page of the cache can be read
-        const int64_t token = ((page * p.cache.kv_heads + pf.h) << p.cache.page_shift) +
-                              (pos & ((1 << p.cache.page_shift) - 1));
-        const unsigned char* base =
-            kind == 0   ? p.cache.k_codes
-            : kind == 1 ? reinterpret_cast<const unsigned char*>(p.cache.k_meta)
-            : kind == 2 ? p.cache.v_codes
-                        : reinterpret_cast<const unsigned char*>(p.cache.v_meta);
-        const int off = (kind >> 1) * (C::kCodeBytes + C::kMetaBytes) +
-                        (kind & 1) * C::kCodeBytes + sub * sub_tokens * int(row_bytes);
-        bulk_load(ring + s * C::kStageBytes + off, base + token * row_bytes,
-                  uint32_t(sub_tokens) * row_bytes, &bars[s], policy);
+        if (uint32_t(pf_page) >= uint32_t(p.cache.pages)) {
+          record_status(kStatusInvalid);
+          pf_page = 0;  // any page of the cache can be read
+        }
+        const int64_t token =
+            ((int64_t(pf_page) * p.cache.kv_heads + pf.h) << p.cache.page_shift) +
+            ((tok0 + (sub << sub_shift)) & ((1 << p.cache.page_shift) - 1));
+        bulk_load(copy_dst + s * C::kStageBytes, copy_src + token * row_bytes,
+                  row_bytes << sub_shift, &ctl->full[warp][s], policy);
       }
-      --to_copy;
-      if (++pf_unit == pf.units && to_copy > 0) {
-        next_segment<ROWS>(p, pf);
-        pf_unit = 0;
+      if (--to_copy > 0) {
+        if (++pf_unit == pf.units) {
+          next_segment<ROWS>(p, pf);
+          pf_unit = 0;
+        }
+        read_page();
       }
     };
-
-    // ---- state of the present segment
-    float O[2 * NC][NT][4];   // m-tile i: dims 32(i/2) + 4g + 2(i%2) + {0, 1}; columns 2t, 2t + 1
-    uint32_t q[NT][2 * NC][2];
-    float sum_q[NT][NG][2], q_scale[NT][2], m[NT][2], l[NT][2], zc[NT][NG][2];
-    int limit[NT][2];
-    bool fresh = true, alive = true;
-
+    read_page();
     for (int s = 0; s < NS - 1; ++s)
       if (to_copy > 0) copy_unit(s);
 
-    const int64_t n = q1 - q0;
-    for (int64_t i = 0; i < n; ++i) {
-      const int st = int(i % NS);
-      // the stage freed by the previous unit
-      if (to_copy > 0) copy_unit(int((i + NS - 1) % NS));
+    // ---- state of the present segment
+    float O[2 * NC][NT][4];  // m-tile i: dims 32(i/2) + 4g + 2(i%2) + {0, 1}; columns 2t, 2t + 1
+    uint32_t q[NT][2 * NC][2];
+    float sum_q[NT][NG][2], q_scale[NT][2], m[NT][2], l[NT][2], zc[NT][NG][2];
+    int limit[NT][2], seen_by_all = 0;
+    bool fresh = true, alive = true;
 
+    // lane group g holds tokens pi(g) and pi(g) + 8 of each 16: with this
+    // order of the tokens the value loads below touch every bank group
+    const int tok_a = 2 * (g >> 1) + ((g & 1) ^ ((g >> 1) & 1));
+    // columns 2t, 2t + 1 (and + 8) of the value operand: tokens pi(2t), pi(2t + 1)
+    const int tok_v0 = 2 * t + (t & 1), tok_v1 = 2 * t + 1 - (t & 1);
+
+    int st = 0;
+    uint32_t parity = 0;
+    for (int left = n_units; left > 0; --left) {
+      // the stage freed by the previous unit
+      if (to_copy > 0) copy_unit(st == 0 ? NS - 1 : st - 1);
+      bool raise = fresh;
       if (fresh) {
         fresh = false;
+        seen_by_all = cs.len - cs.rows + p.by_gqa(cs.rb * ROWS) + 1;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           // ---- queries of column g, scaled to binary16
           const int r = cs.rb * ROWS + nt * 8 + g;
-          const bool have = r < cs.rows * gqa;
+          const bool have = r < cs.rows * p.gqa;
           uint4 raw[NC];
+          const __nv_bfloat16* row = p.Q + row_offset(p, cs.row0, r, cs.h, p.q_stride, D) + 8 * t;
 #pragma unroll
           for (int j = 0; j < NC; ++j) {
             raw[j] = make_uint4(0, 0, 0, 0);
-            if (have)
-              raw[j] = *reinterpret_cast<const uint4*>(
-                  p.Q + row_offset(cs.row0, r, cs.h, gqa, p.q_stride, D) + 32 * j + 8 * t);
+            if (have) raw[j] = *reinterpret_cast<const uint4*>(row + 32 * j);
           }
           float top = 0.f;
 #pragma unroll
@@ -414,7 +460,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
           for (int c = 0; c < 2; ++c) {
             q_scale[nt][c] = __shfl_sync(0xffffffffu, qs, (2 * t + c) * 4);
             const int rc = cs.rb * ROWS + nt * 8 + 2 * t + c;
-            limit[nt][c] = rc < cs.rows * gqa ? cs.len - cs.rows + rc / gqa + 1 : 0;
+            limit[nt][c] = rc < cs.rows * p.gqa ? cs.len - cs.rows + p.by_gqa(rc) + 1 : 0;
             m[nt][c] = -INFINITY;
             l[nt][c] = 0.f;
 #pragma unroll
@@ -427,26 +473,27 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
         }
       }
 
-      if (alive) alive = mbar_wait(&bars[st], uint32_t(i / NS) & 1u);
-      const uint32_t stage = smem_ring + st * C::kStageBytes;
-      const int tok0 = cs_unit * kUnit;
+      if (alive) alive = mbar_wait(&ctl->full[warp][st], parity);
+      const unsigned char* const stage = ring + st * C::kStageBytes;
+      const int tok0 = unit * kUnit;
       // tokens that every row of the block sees need no mask
-      const int seen_by_all = cs.len - cs.rows + (cs.rb * ROWS) / gqa + 1;
       const bool masked = tok0 + kUnit > seen_by_all;
 
-      // lane group g holds tokens pi(g) and pi(g) + 8 of each 16: with this
-      // order of the tokens the value loads below touch every bank group
-      const int tok_a = 2 * (g >> 1) + ((g & 1) ^ ((g >> 1) & 1));
+      // ---- scores (base 2) of the unit's two times 16 tokens
+      float x[2][NT][4];  // tokens a, a, b, b; columns 2t, 2t + 1
+      uint32_t vm[2][2][NG];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float x[NT][4];  // scores, then weights; tokens a, a, b, b
-        float vs[2][NG], vz[2][NG];
         const int ta = 16 * h + tok_a;
-        uint32_t wa[NC], wb[NC], ma[NG], mb[NG];
-        lds_words<NC>(stage + ta * (D / 2) + t * NC * 4, wa);
-        lds_words<NC>(stage + (ta + 8) * (D / 2) + t * NC * 4, wb);
-        lds_words<NG>(stage + C::kCodeBytes + ta * NG * 4, ma);
-        lds_words<NG>(stage + C::kCodeBytes + (ta + 8) * NG * 4, mb);
+        uint32_t wa[NC], wb[NC], km[2][NG];
+        load_words<NC>(stage + ta * (D / 2) + t * NC * 4, wa);
+        load_words<NC>(stage + (ta + 8) * (D / 2) + t * NC * 4, wb);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          load_words<NG>(stage + C::kCodeBytes + (ta + 8 * i) * NG * 4, km[i]);
+          load_words<NG>(stage + 2 * C::kCodeBytes + C::kMetaBytes + (ta + 8 * i) * NG * 4,
+                         vm[h][i]);
+        }
         float acc[NT][NG][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -467,68 +514,66 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
             mma_f16_16816(acc[nt][j / kChunksPerGroup], a1, q[nt][2 * j + 1]);
           }
         }
-        uint32_t va[NG], vb[NG];
-        lds_words<NG>(stage + 2 * C::kCodeBytes + C::kMetaBytes + ta * NG * 4, va);
-        lds_words<NG>(stage + 2 * C::kCodeBytes + C::kMetaBytes + (ta + 8) * NG * 4, vb);
         if (masked) {
           // what lies behind the sequence's end can be anything, NaN included
-          if (tok0 + ta >= cs.len)
 #pragma unroll
-            for (int k = 0; k < NG; ++k) ma[k] = va[k] = 0u;
-          if (tok0 + ta + 8 >= cs.len)
+          for (int i = 0; i < 2; ++i)
+            if (tok0 + ta + 8 * i >= cs.len)
 #pragma unroll
-            for (int k = 0; k < NG; ++k) mb[k] = vb[k] = 0u;
+              for (int k = 0; k < NG; ++k) km[i][k] = vm[h][i][k] = 0u;
         }
-        float lw[2] = {0.f, 0.f};  // the largest value scale of tokens a and b
 #pragma unroll
-        for (int k = 0; k < NG; ++k) {
-          const float2 fa = meta_pair(va[k]), fb = meta_pair(vb[k]);
-          vs[0][k] = fa.x, vz[0][k] = fa.y - 8.f;
-          vs[1][k] = fb.x, vz[1][k] = fb.y - 8.f;
-          lw[0] = fmaxf(lw[0], fa.x);
-          lw[1] = fmaxf(lw[1], fb.x);
-        }
-        lw[0] = log2_approx(lw[0]);
-        lw[1] = log2_approx(lw[1]);
+        for (int k = 0; k < NG; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 f = meta_pair(km[i][k]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const float y = fmaf(-f.y, sum_q[nt][k][c], acc[nt][k][2 * i + c]);
+                x[h][nt][2 * i + c] = k == 0 ? f.x * y : fmaf(f.x, y, x[h][nt][2 * i + c]);
+              }
+          }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) x[nt][c] = 0.f;
-#pragma unroll
-        for (int k = 0; k < NG; ++k) {
-          const float2 fa = meta_pair(ma[k]), fb = meta_pair(mb[k]);
+          for (int c = 0; c < 4; ++c) x[h][nt][c] *= q_scale[nt][c & 1];
+        if (masked) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float2 f = c < 2 ? fa : fb;
-              x[nt][c] = fmaf(f.x, fmaf(-f.y, sum_q[nt][k][c & 1], acc[nt][k][c]), x[nt][c]);
-            }
+            for (int c = 0; c < 4; ++c)
+              if (tok0 + ta + 8 * (c >> 1) >= limit[nt][c & 1]) x[h][nt][c] = -INFINITY;
         }
-        // scores in base 2, masked; the reference m rises only when a weight
-        // would pass 2^8
+      }
+
+      // ---- weights.  The reference m is raised where a segment begins and
+      // when a weight passes 2^15, so that the largest becomes 2^7, and the
+      // unit's weights are formed again.
+      uint32_t w16[2][2][NG][NT];  // pairs (columns 2t, 2t + 1) of tokens a and b
+      while (true) {
+        if (raise) {
+          float lw[2][2];  // log2 of the largest value scale of a token
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            x[nt][c] *= q_scale[nt][c & 1];
-            if (masked && tok0 + ta + 8 * (c >> 1) >= limit[nt][c & 1]) x[nt][c] = -INFINITY;
-          }
-        bool rise = false;
+            for (int i = 0; i < 2; ++i) {
+              float top = meta_pair(vm[h][i][0]).x;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) rise |= x[nt][c] + lw[c >> 1] > m[nt][c & 1] + 8.f;
-        if (__any_sync(0xffffffffu, rise)) {
+              for (int k = 1; k < NG; ++k) top = fmaxf(top, meta_pair(vm[h][i][k]).x);
+              lw[h][i] = log2_approx(top);
+            }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float top = fmaxf(x[nt][c] + lw[0], x[nt][c + 2] + lw[1]);
+              float top = fmaxf(fmaxf(x[0][nt][c] + lw[0][0], x[0][nt][c + 2] + lw[0][1]),
+                                fmaxf(x[1][nt][c] + lw[1][0], x[1][nt][c + 2] + lw[1][1]));
 #pragma unroll
               for (int d = 4; d < 32; d *= 2)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-              const float next = fmaxf(m[nt][c], top);
+              const float next = fmaxf(m[nt][c], top - 7.f);
               const float f = next == -INFINITY ? 1.f : exp2_approx(m[nt][c] - next);
               m[nt][c] = next;
               l[nt][c] *= f;
@@ -541,39 +586,80 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
               }
             }
         }
+        float l_next[NT][2], zc_next[NT][NG][2];
+        uint32_t most[NT];  // the largest weights (none is negative) of two columns
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float ref = m[nt][c & 1] == -INFINITY ? 0.f : m[nt][c & 1];
-            x[nt][c] = exp2_approx(x[nt][c] - ref);
-            l[nt][c & 1] += x[nt][c];
+          for (int c = 0; c < 2; ++c) {
+            most[nt] = 0u;
+            l_next[nt][c] = l[nt][c];
+#pragma unroll
+            for (int k = 0; k < NG; ++k) zc_next[nt][k][c] = zc[nt][k][c];
           }
-        // ---- values of these 16 tokens
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float e[2];
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                e[c] = exp2_approx(x[h][nt][2 * i + c] -
+                                   (m[nt][c] == -INFINITY ? 0.f : m[nt][c]));
+                l_next[nt][c] += e[c];
+              }
+#pragma unroll
+              for (int k = 0; k < NG; ++k) {
+                const float2 f = meta_pair(vm[h][i][k]);
+                const float w0 = e[0] * f.x, w1 = e[1] * f.x;
+                zc_next[nt][k][0] = fmaf(w0, f.y - 8.f, zc_next[nt][k][0]);
+                zc_next[nt][k][1] = fmaf(w1, f.y - 8.f, zc_next[nt][k][1]);
+                w16[h][i][k][nt] = pack_half2(w0, w1);
+                most[nt] = __vmaxu2(most[nt], w16[h][i][k][nt]);
+              }
+            }
+        // 0x7800 is 2^15; a NaN (above infinity, 0x7c00) raises nothing
+        bool over = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t hi = most[nt] >> 16, lo = most[nt] & 0xffffu;
+          over |= (hi > 0x7800u && hi <= 0x7c00u) || (lo > 0x7800u && lo <= 0x7c00u);
+        }
+        raise = !raise && over;
+        if (!__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              l[nt][c] = l_next[nt][c];
+#pragma unroll
+              for (int k = 0; k < NG; ++k) zc[nt][k][c] = zc_next[nt][k][c];
+            }
+          break;
+        }
+        raise = true;
+      }
+
+      // ---- values
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
         uint32_t b[NG][NT][2];
 #pragma unroll
         for (int k = 0; k < NG; ++k)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float w[4];
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              w[c] = x[nt][c] * vs[c >> 1][k];
-              zc[nt][k][c & 1] = fmaf(w[c], vz[c >> 1][k], zc[nt][k][c & 1]);
-            }
-            b[k][nt][0] = transpose8x8(pack_half2(w[0], w[1]));
-            b[k][nt][1] = transpose8x8(pack_half2(w[2], w[3]));
-          }
-        // columns k = 2t, 2t + 1, 2t + 8, 2t + 9 of the operand are tokens
-        // pi(2t), pi(2t + 1) and those + 8
-        const int t0 = 16 * h + 2 * t + (t & 1), t1 = 16 * h + 2 * t + 1 - (t & 1);
+            for (int i = 0; i < 2; ++i) b[k][nt][i] = transpose8x8(w16[h][i][k][nt]);
         constexpr int VW = NC / 2;  // words of a lane and token
-        const uint32_t vbase = stage + C::kCodeBytes + C::kMetaBytes + g * NC * 2;
+        const unsigned char* const vbase = stage + C::kCodeBytes + C::kMetaBytes +
+                                           16 * h * (D / 2) + g * NC * 2;
         uint32_t x0[VW], x1[VW], x2[VW], x3[VW];
-        lds_words<VW>(vbase + t0 * (D / 2), x0);
-        lds_words<VW>(vbase + t1 * (D / 2), x1);
-        lds_words<VW>(vbase + (t0 + 8) * (D / 2), x2);
-        lds_words<VW>(vbase + (t1 + 8) * (D / 2), x3);
+        load_words<VW>(vbase + tok_v0 * (D / 2), x0);
+        load_words<VW>(vbase + tok_v1 * (D / 2), x1);
+        load_words<VW>(vbase + (tok_v0 + 8) * (D / 2), x2);
+        load_words<VW>(vbase + (tok_v1 + 8) * (D / 2), x3);
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
           const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
@@ -590,16 +676,16 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
         }
       }
       __syncwarp();  // the stage may be refilled
+      if (++st == NS) {
+        st = 0;
+        parity ^= 1u;
+      }
 
       // ---- end of the segment, or of this warp's part of it
-      const bool last = i + 1 == n;
-      if (cs_unit + 1 == cs.units || last) {
+      if (unit + 1 == cs.units || left == 1) {
         const int64_t u1 = cs.u0 + cs.units;
-        const bool from_before = cs.u0 < q0, goes_on = u1 > q1;
-        const bool whole = !from_before && !goes_on;
-        float* piece = from_before ? reinterpret_cast<float*>(smem + C::kOffHead) +
-                                         warp * C::kPieceFloats
-                                   : reinterpret_cast<float*>(ring);
+        const bool from_before = cs.u0 < q0;
+        const bool whole = !from_before && u1 <= q1;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -611,161 +697,188 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
               for (int k = 0; k < NG; ++k)
                 zc[nt][k][c] += __shfl_xor_sync(0xffffffffu, zc[nt][k][c], d);
             }
-            const int rl = nt * 8 + 2 * t + c, r = cs.rb * ROWS + rl;
-            const float inv = l[nt][c] == 0.f ? 0.f : 1.f / l[nt][c];
 #pragma unroll
-            for (int j = 0; j < NC; ++j) {
-              const float z = zc[nt][j / kChunksPerGroup][c];
-              const float4 o = make_float4(O[2 * j][nt][c] - z, O[2 * j][nt][c + 2] - z,
-                                           O[2 * j + 1][nt][c] - z, O[2 * j + 1][nt][c + 2] - z);
-              if (!whole) {
-                *reinterpret_cast<float4*>(piece + rl * D + 32 * j + 4 * g) = o;
-              } else if (r < cs.rows * gqa) {
-                const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-                const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-                *reinterpret_cast<uint2*>(
-                    p.O + row_offset(cs.row0, r, cs.h, gqa, p.o_stride, D) + 32 * j + 4 * g) =
-                    make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                               *reinterpret_cast<const uint32_t*>(&hi));
-              }
-            }
-            if (!whole && g == 0) {
-              piece[ROWS * D + rl] = m[nt][c];
-              piece[ROWS * D + ROWS + rl] = l[nt][c];
+            for (int k = 0; k < 2 * NC; ++k) {
+              O[k][nt][c] -= zc[nt][k / 2 / kChunksPerGroup][c];
+              O[k][nt][c + 2] -= zc[nt][k / 2 / kChunksPerGroup][c];
             }
           }
-        if (!whole && lane == 0) {
-          PieceInfo& info = from_before ? ctl->head[warp] : ctl->tail[warp];
-          info = {1, cs.b, cs.rb, cs.h, cs.row0, cs.rows, cs.u0, u1};
+        if (whole) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int r = cs.rb * ROWS + nt * 8 + 2 * t + c;
+              if (r >= cs.rows * p.gqa) continue;
+              const float inv = l[nt][c] == 0.f ? 0.f : 1.f / l[nt][c];
+              __nv_bfloat16* row = p.O + row_offset(p, cs.row0, r, cs.h, p.o_stride, D) + 4 * g;
+#pragma unroll
+              for (int j = 0; j < NC; ++j)
+                *reinterpret_cast<uint2*>(row + 32 * j) = make_uint2(
+                    pack_bf162(O[2 * j][nt][c] * inv, O[2 * j][nt][c + 2] * inv),
+                    pack_bf162(O[2 * j + 1][nt][c] * inv, O[2 * j + 1][nt][c + 2] * inv));
+            }
+        } else {
+          float* piece = reinterpret_cast<float*>(
+              from_before ? smem + C::kOffHead + warp * C::kPieceBytes : ring);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int rl = nt * 8 + 2 * t + c;
+#pragma unroll
+              for (int j = 0; j < NC; ++j)
+                *reinterpret_cast<float4*>(piece + rl * D + 32 * j + 4 * g) =
+                    make_float4(O[2 * j][nt][c], O[2 * j][nt][c + 2], O[2 * j + 1][nt][c],
+                                O[2 * j + 1][nt][c + 2]);
+              if (g == 0) {
+                piece[ROWS * D + rl] = m[nt][c];
+                piece[ROWS * D + ROWS + rl] = l[nt][c];
+              }
+            }
+          if (lane == 0) {
+            (from_before ? ctl->head : ctl->tail)[warp] = {cs.rb,   cs.h,  cs.row0,
+                                                           cs.rows, cs.u0, u1};
+            atomicOr(from_before ? &ctl->has_head : &ctl->has_tail, 1u << warp);
+          }
         }
-        if (!last) {
+        if (left > 1) {
           next_segment<ROWS>(p, cs);
-          cs_unit = 0;
+          unit = 0;
           fresh = true;
         }
       } else {
-        ++cs_unit;
+        ++unit;
       }
     }
   }
 
   // ---- pieces of segments that span warps.  Chain 0 is the segment that
   // began before this CTA; chain w + 1 the one that begins in warp w and goes
-  // on.  A warp adds one row of one chain at a time, in warp order.
+  // on.  A warp adds one row of one chain at a time, in warp order; where the
+  // segment spans CTAs the row's sums go to the workspace, and the warp that
+  // is the last of all CTAs' to bring that row adds them, in CTA order.
   __syncthreads();
   constexpr int VF = D / 32;  // floats of a lane
-  auto head_piece = [&](int w) {
-    return reinterpret_cast<const float*>(smem + C::kOffHead) + w * C::kPieceFloats;
-  };
-  auto tail_piece = [&](int w) {
-    return reinterpret_cast<const float*>(smem + w * C::kRingBytes);
-  };
-  auto slot = [&](int64_t i) { return p.partial + i * C::kPieceFloats; };
-  auto store_row = [&](const PieceInfo& s, int rl, const float (&o)[VF], float l) {
-    const int r = s.rb * ROWS + rl;
-    if (r >= s.rows * gqa) return;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint32_t w[VF / 2];
-#pragma unroll
-    for (int k = 0; k < VF / 2; ++k) {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
-      w[k] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-    uint32_t* to = reinterpret_cast<uint32_t*>(
-        p.O + row_offset(s.row0, r, s.h, gqa, p.o_stride, D) + lane * VF);
-#pragma unroll
-    for (int k = 0; k < VF / 2; ++k) to[k] = w[k];
-  };
-  int first = 0;  // the first warp with units
-  while (first < WARPS - 1 && warp_begin(first + 1) == r0) ++first;
-  for (int task = warp; task < (WARPS + 1) * ROWS; task += WARPS) {
-    const int chain = task / ROWS, rl = task % ROWS;
-    const PieceInfo& s = chain == 0 ? ctl->head[first] : ctl->tail[chain - 1];
-    if (!s.valid || s.rb * ROWS + rl >= s.rows * gqa) continue;
-    float top = -INFINITY;
-    auto each = [&](auto&& f) {
-      if (chain != 0) f(tail_piece(chain - 1));
-      for (int w = chain == 0 ? first : chain; w < WARPS; ++w) {
-        const int64_t at = warp_begin(w);
-        if (at >= s.u1) break;
-        if (at < warp_begin(w + 1)) f(head_piece(w));
-      }
-    };
-    each([&](const float* f) { top = fmaxf(top, f[ROWS * D + rl]); });
-    float o[VF], l = 0.f;
-#pragma unroll
-    for (int k = 0; k < VF; ++k) o[k] = 0.f;
-    each([&](const float* f) {
-      const float m = f[ROWS * D + rl];
-      const float weight = m == -INFINITY ? 0.f : exp2_approx(m - top);
-      l = fmaf(weight, f[ROWS * D + ROWS + rl], l);
-#pragma unroll
-      for (int k = 0; k < VF; ++k) o[k] = fmaf(weight, f[rl * D + lane * VF + k], o[k]);
-    });
-    if (s.u0 >= r0 && s.u1 <= r1) {
-      store_row(s, rl, o, l);
-    } else {
-      float* to = slot(2 * cta + (s.u0 < r0 ? 0 : 1));
-#pragma unroll
-      for (int k = 0; k < VF; ++k) to[rl * D + lane * VF + k] = o[k];
-      if (lane == 0) {
-        to[ROWS * D + rl] = top;
-        to[ROWS * D + ROWS + rl] = l;
-      }
-    }
-  }
-
-  // ---- segments that span CTAs: the last to arrive adds their partial sums
-  auto cta_of = [&](int64_t u) { return int(((u + 1) * ctas - 1) / total); };
-  int open = -1;  // the warp whose tail goes on into the next CTA
-  for (int w = 0; w < WARPS; ++w)
-    if (ctl->tail[w].valid && ctl->tail[w].u1 > r1) open = w;
-  const bool spans[2] = {ctl->head[first].valid != 0 && ctl->head[first].u0 < r0, open >= 0};
-  if (!spans[0] && !spans[1]) return;
-  __syncthreads();
-  if (tid == 0) {
-    __threadfence();
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      ctl->last[k] = 0;
-      if (!spans[k]) continue;
-      const PieceInfo& s = k == 0 ? ctl->head[first] : ctl->tail[open];
-      const int c0 = cta_of(s.u0), c1 = cta_of(s.u1 - 1);
-      const unsigned before = atomicAdd(&p.arrived[c0], 1u);
-      if (before == unsigned(c1 - c0)) {
-        p.arrived[c0] = 0u;  // every CTA of the segment has arrived
-        ctl->last[k] = 1;
-      }
-    }
-    __threadfence();
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (!spans[k] || !ctl->last[k]) continue;
-    const PieceInfo& s = k == 0 ? ctl->head[first] : ctl->tail[open];
-    const int c0 = cta_of(s.u0), c1 = cta_of(s.u1 - 1);
-    for (int rl = warp; rl < ROWS; rl += WARPS) {
-      if (s.rb * ROWS + rl >= s.rows * gqa) break;
-      float top = -INFINITY;
-      for (int c = c0 + lane; c <= c1; c += 32)
-        top = fmaxf(top, __ldcg(slot(2 * c + (c == c0 ? 1 : 0)) + ROWS * D + rl));
+  const unsigned has_head = ctl->has_head, has_tail = ctl->has_tail;
+  const int first = has_head ? __ffs(has_head) - 1 : 0;
+  // the segment that began before this CTA is the first warp's with units
+  const bool from_before = has_head != 0u && ctl->head[first].u0 < r0;
+  int task = 0;
+  for (unsigned todo = (has_tail << 1) | (from_before ? 1u : 0u); todo != 0u; todo &= todo - 1u) {
+    const int chain = __ffs(todo) - 1;
+    const PieceInfo s = chain == 0 ? ctl->head[first] : ctl->tail[chain - 1];
+    const int rows = min(ROWS, s.rows * p.gqa - s.rb * ROWS);
+    // lane w holds the statistics of warp w's piece
+    const bool is_tail = lane == chain - 1;
+    const bool mine = is_tail || (lane < WARPS && lane >= max(chain, first) &&
+                                  ((has_head >> lane) & 1u) != 0u && ctl->head[lane].u0 == s.u0);
+    const unsigned char* piece = is_tail ? smem + lane * C::kRingBytes
+                                         : smem + C::kOffHead + lane * C::kPieceBytes;
+    const unsigned pieces = __ballot_sync(0xffffffffu, mine);
+    for (int rl = 0; rl < rows; ++rl, ++task) {
+      if (task % WARPS != warp) continue;
+      const float* stats = reinterpret_cast<const float*>(piece) + ROWS * D + rl;
+      const float own_m = mine ? stats[0] : -INFINITY;
+      float top = own_m;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      float o[VF], l = 0.f;
+      const float weight = own_m == -INFINITY ? 0.f : exp2_approx(own_m - top);
+      float l = mine ? weight * stats[ROWS] : 0.f;
 #pragma unroll
-      for (int j = 0; j < VF; ++j) o[j] = 0.f;
+      for (int d = 1; d < 32; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
+      float o[VF];
+#pragma unroll
+      for (int k = 0; k < VF; ++k) o[k] = 0.f;
 #pragma unroll 4
-      for (int c = c0; c <= c1; ++c) {
-        const float* f = slot(2 * c + (c == c0 ? 1 : 0));
-        const float m = __ldcg(f + ROWS * D + rl);
-        const float weight = m == -INFINITY ? 0.f : exp2_approx(m - top);
-        l = fmaf(weight, __ldcg(f + ROWS * D + ROWS + rl), l);
+      for (int w = 0; w < WARPS; ++w) {
+        const float f = __shfl_sync(0xffffffffu, weight, w);
+        if (!((pieces >> w) & 1u)) continue;
+        uint32_t v[VF];
+        load_words<VF>((w == chain - 1 ? smem + w * C::kRingBytes
+                                       : smem + C::kOffHead + w * C::kPieceBytes) +
+                           (rl * D + lane * VF) * 4,
+                       v);
 #pragma unroll
-        for (int j = 0; j < VF; ++j)
-          o[j] = fmaf(weight, __ldcg(f + rl * D + lane * VF + j), o[j]);
+        for (int k = 0; k < VF; ++k) o[k] = fmaf(f, __uint_as_float(v[k]), o[k]);
       }
-      store_row(s, rl, o, l);
+      if (s.u0 < r0 || s.u1 > r1) {
+        auto slot = [&](int c, bool begins) {
+          return p.partial + (2 * int64_t(c) + (begins ? 1 : 0)) * C::kPieceFloats;
+        };
+        float* to = slot(cta, s.u0 >= r0);
+#pragma unroll
+        for (int k = 0; k < VF; ++k) __stcg(to + rl * D + lane * VF + k, o[k]);
+        if (lane == 0) {
+          __stcg(to + ROWS * D + rl, top);
+          __stcg(to + ROWS * D + ROWS + rl, l);
+        }
+        // the CTAs of the segment's first and last unit
+        const int64_t wide = extra * (per_cta + 1);  // units of the CTAs with one more
+        auto cta_of = [&](int64_t u) {
+          const int64_t a = u < wide ? u : u - wide, n = u < wide ? per_cta + 1 : per_cta;
+          return (u < wide ? 0 : extra) + (narrow ? int(uint32_t(a) / uint32_t(n)) : int(a / n));
+        };
+        const int c0 = s.u0 >= r0 ? cta : cta_of(s.u0);
+        const int c1 = s.u1 <= r1 ? cta : cta_of(s.u1 - 1);
+        __syncwarp();
+        unsigned before = 0u;
+        if (lane == 0) {
+          __threadfence();
+          before = atomicAdd(&p.arrived[c0 * kMaxRows + rl], 1u);
+          __threadfence();
+        }
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before != unsigned(c1 - c0)) continue;
+        // every CTA of the segment has brought its row
+        if (lane == 0) p.arrived[c0 * kMaxRows + rl] = 0u;
+        constexpr int kAtOnce = 8;
+        top = -INFINITY;
+        l = 0.f;
+#pragma unroll
+        for (int k = 0; k < VF; ++k) o[k] = 0.f;
+        for (int base = c0; base <= c1; base += kAtOnce) {
+          float v[kAtOnce][VF];
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            const float* from = slot(min(base + i, c1), base + i == c0) + rl * D + lane * VF;
+#pragma unroll
+            for (int k = 0; k < VF / 2; ++k) {
+              const float2 f = __ldcg(reinterpret_cast<const float2*>(from) + k);
+              v[i][2 * k] = f.x, v[i][2 * k + 1] = f.y;
+            }
+          }
+          const int c = base + lane;
+          const bool there = lane < kAtOnce && c <= c1;
+          const float* from = slot(min(c, c1), c == c0) + ROWS * D + rl;
+          const float m_c = there ? __ldcg(from) : -INFINITY;
+          const float l_c = there ? __ldcg(from + ROWS) : 0.f;
+          float next = fmaxf(top, m_c);
+#pragma unroll
+          for (int d = 1; d < 32; d *= 2)
+            next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, d));
+          const float keep = top == -INFINITY ? 0.f : exp2_approx(top - next);
+          const float w_c = m_c == -INFINITY ? 0.f : exp2_approx(m_c - next);
+          float add = w_c * l_c;
+#pragma unroll
+          for (int d = 1; d < kAtOnce; d *= 2) add += __shfl_xor_sync(0xffffffffu, add, d);
+          l = fmaf(l, keep, __shfl_sync(0xffffffffu, add, 0));
+#pragma unroll
+          for (int k = 0; k < VF; ++k) o[k] *= keep;
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            const float f = __shfl_sync(0xffffffffu, w_c, i);
+#pragma unroll
+            for (int k = 0; k < VF; ++k) o[k] = fmaf(f, v[i][k], o[k]);
+          }
+          top = next;
+        }
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint32_t* to = reinterpret_cast<uint32_t*>(
+          p.O + row_offset(p, s.row0, s.rb * ROWS + rl, s.h, p.o_stride, D) + lane * VF);
+#pragma unroll
+      for (int k = 0; k < VF / 2; ++k) to[k] = pack_bf162(o[2 * k] * inv, o[2 * k + 1] * inv);
     }
   }
 }
