@@ -68,10 +68,11 @@ def sequence_values(codes, meta, table_row, n, page, kind):
     return c.astype(np.float64), m[..., 0], m[..., 1]
 
 
-def attention(q: np.ndarray, k, v, n: int, scale: float):
+def attention(q: np.ndarray, k, v, n: int, scale: float, few: bool = True):
     """One sequence: q [T, Hq, D] float64, k and v as ``sequence_values``
     gives them.  Returns the output [T, Hq, D] and the bound on the error of a
-    computation that rounds its weights to binary16 (see below)."""
+    computation that rounds its weights (``few``), or its weights, keys and
+    values (not ``few``), to binary16."""
     (kc, ks, kz), (vc, vs, vz) = k, v
     t, hq, d = q.shape
     h, ng = ks.shape[1], ks.shape[2]
@@ -94,14 +95,22 @@ def attention(q: np.ndarray, k, v, n: int, scale: float):
             # the magnitudes added up (tensor cores truncate)
             mags = (ks[:seen, a] * 16 * np.abs(q[i, j]).reshape(ng, g).sum(-1)).sum(-1).max()
             e = 16 * 2.0 ** -23 * abs(scale) * mags + 2.0 ** -21
-            # weights: half a step of binary16 (2^-11) each, times |u - 8| <=
-            # 8; those below binary16's normal range are off by 2^-25 where the
-            # largest is at least 1; score errors move every weight (twice:
-            # numerator and sum)
-            w8 = np.repeat((p[:, None] * vs[:seen, a]).sum(0) * 8, g)
-            tiny = seen * 8 * 2.0 ** -25 * vs[:seen, a].max()
-            wabs = p @ (np.repeat(vs[:seen, a], g, -1) * 16)
-            bound[i, j] = 2.0 ** -11 * w8 + tiny + 2 * e * wabs
+            if few:
+                # weights: half a step of binary16 (2^-11) each, times |u - 8|
+                # <= 8; those below binary16's normal range are off by 2^-25
+                # where the largest is at least 1; score errors move every
+                # weight (twice: numerator and sum)
+                w8 = np.repeat((p[:, None] * vs[:seen, a]).sum(0) * 8, g)
+                tiny = seen * 8 * 2.0 ** -25 * vs[:seen, a].max()
+                wabs = p @ (np.repeat(vs[:seen, a], g, -1) * 16)
+                bound[i, j] = 2.0 ** -11 * w8 + tiny + 2 * e * wabs
+            else:
+                # half a step of each key moves the scores, of each weight and
+                # value the sum
+                e += abs(scale) * 2.0 ** -11 * (np.abs(kh[:seen, a]) @ np.abs(q[i, j])).max()
+                wabs = p @ np.abs(vh[:seen, a])
+                tiny = seen * 2.0 ** -25 * np.abs(vh[:seen, a]).max()
+                bound[i, j] = 2.0 ** -10 * 1.01 * wabs + tiny + 2 * np.expm1(e) * wabs
     return out, bound
 
 

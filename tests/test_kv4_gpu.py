@@ -72,7 +72,9 @@ def reference(q, cache, lens, rows, table, scale):
         k = ref.sequence_values(kc, km, table[b], n, cache.page_size, "k")
         v = ref.sequence_values(vc, vm, table[b], n, cache.page_size, "v")
         x = q[at:at + t].float().cpu().numpy().astype(np.float64)
-        o, e = ref.attention(x, k, v, n, scale)
+        # more than 16 rows times heads of a group go to the tensor-memory kernel
+        few = t * (x.shape[1] // cache.kv_heads) <= 16
+        o, e = ref.attention(x, k, v, n, scale, few)
         out.append(o)
         bound.append(e)
         at += t
@@ -228,6 +230,59 @@ def test_page_sizes(page):
     ([20, 7], [20, 90]), ([70], [131])])
 def test_several_rows(d, group, rows, lens):
     run_attention(d, group, 32, 2, 2, lens, rows, seed=sum(rows))
+
+
+@pytest.mark.parametrize("d,group", FORMATS)
+@pytest.mark.parametrize("gqa,rows,lens", [
+    (1, [17], [17]), (4, [5], [300]), (4, [33], [40]), (1, [128], [128]), (1, [129], [131]),
+    (2, [128], [1000]), (4, [100, 1, 64], [100, 1, 260]), (7, [40, 0, 3, 90], [700, 5, 3, 20]),
+    (16, [2, 2], [130, 128])])
+def test_many_rows(d, group, gqa, rows, lens):
+    run_attention(d, group, 16, 2, gqa, lens, rows, seed=sum(rows) + gqa)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+def test_many_rows_page_sizes(page):
+    run_attention(128, 64, page, 1, 4, [page + 200, 600], [60, 100], seed=page)
+
+
+@pytest.mark.parametrize("kind", ["large", "tiny", "zero", "mixed", "negative", "no scale"])
+def test_many_rows_query_ranges(kind):
+    q = ref.keys(3, 40, 8, 128, 1.0).float()
+    if kind == "large":
+        q *= 40
+    elif kind == "tiny":
+        q *= 2.0 ** -120
+    elif kind == "zero":
+        q *= 0
+    elif kind == "mixed":
+        q *= torch.exp2(torch.arange(128) % 20 - 12.0)
+    run_attention(128, 32, 32, 2, 4, [350], [40], seed=4, q=q.to(torch.bfloat16),
+                  scale={"negative": -0.3, "no scale": 0.0}.get(kind))
+
+
+@pytest.mark.parametrize("what,strength", [("v", 2.0 ** -13), ("v", 2.0 ** -20), ("v", 2.0 ** 10),
+                                           ("v", 60000.0), ("k", 60000.0), ("both", 60000.0)])
+def test_many_rows_value_ranges(what, strength):
+    """Scales that differ from token to token, and values at the end of
+    binary16's range, whose codes can stand for more than its largest."""
+    d, group, heads, n, page, t = 128, 32, 2, 400, 32, 30
+    table, pages = ref.random_batch(5, [n], page)
+    cache = new_cache(pages, heads, d, page, group)
+    spread = torch.exp2(torch.randint(-8, 1, (n, 1, 1),
+                                      generator=torch.Generator().manual_seed(3)).float())
+    k, v = ref.keys(1, n, heads, d), ref.keys(2, n, heads, d, 1.0)
+    if what != "k":
+        v = v.float().clamp(-1, 1) * spread * strength
+    if what != "v":
+        k = k.float().clamp(-1, 1) * spread * strength
+    wq().kv4_write(k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16).cuda(), cache, ints([n]),
+                   ints(table))
+    q = ref.keys(9, t, 8, d, 1.0).float()
+    q = (q / strength if what != "v" else q).to(torch.bfloat16).cuda()
+    got = wq().kv4_attention(q, cache, ints([n]), ints(table))
+    o, bound = reference(q, cache, [n], [t], table, d ** -0.5)
+    ref.check(got, o, bound)
 
 
 @pytest.mark.parametrize("d,group,heads,gqa,lens", [

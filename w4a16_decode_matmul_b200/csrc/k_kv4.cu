@@ -6,8 +6,14 @@
 #include "kv4_host.h"
 #include "kv4.cuh"
 #include "kv4_attn.cuh"
+#include "kv4_prefill.cuh"
 
 namespace wqh {
+
+// k_kv4_prefill.cu
+cudaError_t run_kv4_prefill(int head_dim, int group, const wq::kv4::PrefillParams& p,
+                            cudaStream_t s);
+
 namespace {
 
 namespace kv4 = wq::kv4;
@@ -151,7 +157,19 @@ cudaError_t run_kv4_attention(const void* Q, int64_t q_stride, int q_heads,
   p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
                                        round_up(kCounterBytes, 256));
   const int64_t max_rows = batch.row_starts ? batch.max_rows : batch.rows / batch.seqs;
-  const int max_columns = int(std::min<int64_t>(max_rows * p.gqa, 1 << 20));
+  // Sequences with up to 16 rows (times heads) stream the cache through the
+  // warp-level kernel; with more, the tensor-memory kernel reads it once per
+  // 256 rows.  A ragged batch may hold both.
+  constexpr int kFew = kv4::kMaxRows;
+  const int64_t bound = max_rows > 0 ? max_rows : batch.rows;
+  p.max_columns = 1 << 30;
+  if (bound * p.gqa > kFew) {
+    kv4::PrefillParams pp = {p, kFew + 1};
+    const cudaError_t e = run_kv4_prefill(cache.head_dim, cache.group, pp, s);
+    if (e != cudaSuccess || !batch.row_starts) return e;
+    p.max_columns = kFew;
+  }
+  const int max_columns = int(std::min<int64_t>(bound * p.gqa, kFew));
   return dispatch_kv4<AttnOp>(cache.head_dim, cache.group, p, max_columns, s, dev.sms);
 }
 

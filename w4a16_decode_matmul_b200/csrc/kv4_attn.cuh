@@ -63,6 +63,7 @@ struct AttnParams {
   __nv_bfloat16* O;  // [rows][q_heads][D], rows o_stride elements apart
   int64_t o_stride;
   int gqa;            // query heads per kv head
+  int max_columns;    // sequences with more rows times gqa are another kernel's
   FastDiv by_gqa;
   float scale_log2;   // softmax scale times log2 e
   unsigned* arrived;  // [kMaxCtas][kMaxRows] zero counters
@@ -119,6 +120,13 @@ struct AttnControl {
   PieceInfo head[WARPS], tail[WARPS];
 };
 
+// Sequence b with its rows, none if it is another kernel's.
+__device__ __forceinline__ Sequence attn_sequence(const AttnParams& p, int b) {
+  Sequence s = load_sequence(p.batch, b);
+  if (s.rows * p.gqa > p.max_columns) s.rows = 0;
+  return s;
+}
+
 // Tokens that some row of block rb sees.
 template <int ROWS>
 __device__ __forceinline__ int block_limit(const Sequence& s, int rb, const AttnParams& p) {
@@ -155,7 +163,7 @@ __device__ __forceinline__ void next_segment(const AttnParams& p, Segment& s) {
   if (++s.rb >= row_blocks<ROWS>(q, p.gqa)) {
     s.rb = 0;
     do {
-      q = load_sequence(p.batch, ++s.b);
+      q = attn_sequence(p, ++s.b);
     } while (q.rows == 0);
     s.row0 = q.row0;
     s.rows = q.rows;
@@ -241,12 +249,12 @@ __device__ __forceinline__ int find_segment(const AttnParams& p, const AttnContr
   if (i > 0) rem -= __shfl_sync(0xffffffffu, before, i);
   Segment s;
   s.b = (w * 32 + i) * per_thread;
-  Sequence seq = load_sequence(p.batch, s.b);
+  Sequence seq = attn_sequence(p, s.b);
   while (per_thread > 1) {
     const int64_t n = sequence_units<ROWS>(p, seq);
     if (rem < n) break;
     rem -= n;
-    seq = load_sequence(p.batch, ++s.b);
+    seq = attn_sequence(p, ++s.b);
   }
   s.row0 = seq.row0;
   s.rows = seq.rows;
@@ -283,7 +291,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
   const int b_end = min(p.batch.seqs, b_begin + per_thread);
   int64_t upto = 0;
   for (int b = b_begin; b < b_end; ++b)
-    upto += sequence_units<ROWS>(p, load_sequence(p.batch, b));
+    upto += sequence_units<ROWS>(p, attn_sequence(p, b));
   if (tid < WARPS * NS) {
     mbar_init(&ctl->full[tid / NS][tid % NS], 1);
     fence_mbar_init();

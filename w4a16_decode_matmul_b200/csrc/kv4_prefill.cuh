@@ -1,0 +1,590 @@
+// kv4_prefill.cuh -- attention of many query rows per sequence over the 4-bit
+// cache (chunks, whole prompts) on the fifth generation tensor cores.
+//
+// One CTA computes up to 256 rows (query tokens times the heads that share a
+// kv head) of one sequence and kv head, as two tiles of 128 rows that take
+// turns on the tensor cores, over all the tokens they see, 128 at a time:
+//   warps 0-3, 4-7  softmax of tile 0 and 1: a thread owns a row (a lane of
+//                   tensor memory), so row maxima and sums need no exchange;
+//   warps 8-11      dequantize: a token's codes from global memory (one tile
+//                   ahead in registers) to binary16 values s (u - z) in shared
+//                   memory, 128-byte swizzled, two stages each of keys and
+//                   values;
+//   warp 12         one thread issues tcgen05.mma: S_i = Q_i K^T (both operands
+//                   in shared memory) and O_i += P_i V (P_i in tensor memory,
+//                   written over S_i by the softmax), 512 columns in all:
+//                   S_0, S_1, O_0, O_1.
+// Keys and values share one image in shared memory, [token][64 dims] rows of
+// 128 bytes: it is the K-major operand of the first product (k = dims) and the
+// MN-major operand of the second (n = dims).  The eight dims of a 16-byte
+// chunk keep the order of the codes' unpack (0, 4, 1, 5, 2, 6, 3, 7): the
+// query tile is stored in the same order and the output put back at the end.
+//
+// Roundings.  Queries: scaled by a power of two per row to [2^14, 2^15) and
+// rounded to binary16 (exact for every bfloat16 within 2^-21 of the row's
+// largest).  Keys and values: s (u - z) rounded once to binary16 (2^-11 half
+// step; exact where it is subnormal, since s is a multiple of 2^-24).  A tile
+// with a scale above 4366, the only ones whose values can pass 65504, is
+// halved, and the softmax doubles it back.  Weights: 2^(S - m) rounded to
+// binary16; the reference m is raised only when a row's largest weight would
+// pass 2^14, then so that it becomes 2^7 (and the row's output is rescaled).
+// Products, sums and statistics in binary32.
+//
+// What bounds it.  Per 256 rows x 128 tokens (D = 128): tensor cores 2,048
+// cycles, exponentials (16 a cycle) 2,048, issue slots about as many.
+#pragma once
+
+#include "gemm2.cuh"
+#include "kv4_attn.cuh"
+
+namespace wq {
+namespace kv4 {
+
+using gemm::fence_async_shared;
+using gemm::tc_commit;
+using gemm::tc_fence_after;
+using gemm::tc_fence_before;
+using gemm::tmem_ld32;
+using gemm::tmem_wait_ld;
+using gemm::tmem_wait_st;
+using gemm2::tc_mma_ts;
+using gemm2::tmem_st16;
+
+constexpr int kTile = 128;       // rows of a tile, tokens of a step
+constexpr int kBlockRows = 256;  // rows of a CTA
+constexpr int kPrefillThreads = 13 * 32;
+constexpr int kWideScale = 4366;  // 15 * 4366 is the last multiple below 65504
+
+struct PrefillParams {
+  AttnParams a;
+  int min_columns;  // sequences with fewer rows times heads are left alone
+};
+
+template <int D>
+struct PrefillConfig {
+  static constexpr int kHalves = D / 64;                    // 64-dim blocks of a row
+  static constexpr int kBlockBytes = kTile * 128;           // one block of a tile
+  static constexpr int kTileBytes = kHalves * kBlockBytes;
+  static constexpr int kOffQ = 1024;
+  static constexpr int kOffK = kOffQ + 2 * kTileBytes;      // 2 stages
+  static constexpr int kOffV = kOffK + 2 * kTileBytes;      // 2 stages
+  // with the alignment's slack; more than half an SM's, since a second CTA
+  // would wait for tensor memory
+  static constexpr int kUsed = kOffV + 2 * kTileBytes + 1024;
+  static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
+};
+
+struct PrefillControl {
+  uint64_t q_full[2];
+  uint64_t k_full[2], k_free[2], v_full[2], v_free[2];  // stages
+  uint64_t s_full[2], p_full[2], o_done[2];              // tiles
+  uint64_t mma_done;
+  int wide[4];  // of the last steps: values are halved
+  uint32_t tmem;
+  int abort;
+};
+
+// Shared-memory operand in the 128-byte swizzled layout: lbo is the distance
+// of 64-element blocks of a MN-major operand (unused when K-major), 1024 the
+// distance of 8-row groups.
+__device__ __forceinline__ uint64_t swizzled_desc(uint32_t addr, uint32_t lbo) {
+  return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) |
+         (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// binary16 operands, binary32 accumulator, M = 128; B K-major or MN-major.
+__host__ __device__ constexpr uint32_t instr_desc_f16(int n, bool b_mn) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) |
+         (uint32_t(kTile >> 4) << 24);
+}
+
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :
+      : "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Whether the predicate holds for any of the `threads` threads of a barrier.
+__device__ __forceinline__ bool named_barrier_or(uint32_t id, uint32_t threads, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.u32 a, %1, 0;\n\t"
+      "barrier.cta.red.or.pred b, %2, %3, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "r"(uint32_t(p)), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
+// The rows of a block of 256: the blocks of sequence b begin at index
+// row_starts[b] gqa / 256 + b, which leaves each sequence at least as many
+// indices as it has blocks.
+struct Block {
+  int b;
+  Sequence s;
+  int row;       // first row (query token times heads) of the block
+  int columns;   // rows of the sequence
+};
+
+__device__ __forceinline__ bool find_block(const PrefillParams& p, int index, int lane,
+                                           Block* out) {
+  const Batch& batch = p.a.batch;
+  auto first_block = [&](int b) {
+    const int start = batch.row_starts != nullptr
+                          ? min(max(batch.row_starts[b], 0), batch.rows)
+                          : b * batch.rows_per_seq;
+    return start * p.a.gqa / kBlockRows + b;
+  };
+  int lo = 0, n = batch.seqs;  // the largest b with first_block(b) <= index
+  while (n > 1) {
+    const int step = (n + 32) / 33;
+    const int at = lo + (lane + 1) * step;
+    const bool below = at < lo + n && first_block(at) <= index;
+    const int skip = __popc(__ballot_sync(0xffffffffu, below));
+    lo += skip * step;
+    n = min(step, n - skip * step);
+  }
+  out->b = lo;
+  out->s = load_sequence(batch, lo);
+  out->columns = out->s.rows * p.a.gqa;
+  const int rb = index - first_block(lo);
+  out->row = rb * kBlockRows;
+  return rb >= 0 && out->row < out->columns && out->columns >= p.min_columns;
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const PrefillParams p) {
+  using C = PrefillConfig<D>;
+  constexpr int NC = D / 32, NG = D / G;
+  extern __shared__ unsigned char raw_smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // the later rows of a sequence see more tokens: they come first
+  Block block;
+  const int heads = p.a.cache.kv_heads;
+  const int head = (int(gridDim.x) - 1 - int(blockIdx.x)) % heads;
+  if (!find_block(p, (int(gridDim.x) - 1 - int(blockIdx.x)) / heads, lane, &block)) return;
+  const Sequence& seq = block.s;
+  const int rows = min(kBlockRows, block.columns - block.row);
+  const int tiles = rows > kTile ? 2 : 1;
+  // tokens the block's last row sees
+  const int limit = seq.len - seq.rows + p.a.by_gqa(block.row + rows - 1) + 1;
+  const int steps = (max(limit, 0) + kTile - 1) / kTile;
+
+  unsigned char* const smem =
+      raw_smem + ((1024u - (smem_addr(raw_smem) & 1023u)) & 1023u);  // swizzle atoms
+  auto* ctl = reinterpret_cast<PrefillControl*>(smem);
+  static_assert(sizeof(PrefillControl) <= C::kOffQ, "");
+  volatile int* const abort_flag = &ctl->abort;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->q_full[i], 4);
+      mbar_init(&ctl->k_full[i], 4);
+      mbar_init(&ctl->v_full[i], 4);
+      mbar_init(&ctl->k_free[i], 1);
+      mbar_init(&ctl->v_free[i], 1);
+      mbar_init(&ctl->s_full[i], 1);
+      mbar_init(&ctl->p_full[i], 4);
+      mbar_init(&ctl->o_done[i], 1);
+    }
+    mbar_init(&ctl->mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&ctl->tmem)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&ctl->tmem);
+
+  // Waits for a phase; false once any role's wait has run out of time.
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_test_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (!mbar_wait(bar, parity)) {
+      *abort_flag = 1;
+      return false;
+    }
+    return true;
+  };
+
+  if (warp == 12) {
+    // ---- matrix products
+    if (lane == 0) {
+      constexpr uint32_t kDescQK = instr_desc_f16(kTile, false);
+      constexpr uint32_t kDescPV = instr_desc_f16(D, true);
+      const uint32_t sq = smem_addr(smem + C::kOffQ), sk = smem_addr(smem + C::kOffK),
+                     sv = smem_addr(smem + C::kOffV);
+      bool ok = true;
+      for (int i = 0; i < tiles && ok; ++i) ok = wait(&ctl->q_full[i], 0);
+      auto scores = [&](int i, int stage) {
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (ks >> 2) * C::kBlockBytes + (ks & 3) * 32;
+          tc_mma_ss(tmem + i * kTile, swizzled_desc(sq + i * C::kTileBytes + off, 16),
+                    swizzled_desc(sk + stage * C::kTileBytes + off, 16), kDescQK, ks > 0);
+        }
+        tc_commit(&ctl->s_full[i]);
+      };
+      // S_i of step j + 1 follows O_i of step j: it writes over P_i
+      if (ok && steps > 0 && (ok = wait(&ctl->k_full[0], 0))) {
+        for (int i = 0; i < tiles; ++i) scores(i, 0);
+        tc_commit(&ctl->k_free[0]);
+      }
+      for (int j = 0; j < steps && ok; ++j) {
+        const int stage = j & 1, next = stage ^ 1;
+        const bool more = j + 1 < steps;
+        for (int i = 0; i < tiles && ok; ++i) {
+          ok = wait(&ctl->p_full[i], uint32_t(j) & 1u) &&
+               (i > 0 || wait(&ctl->v_full[stage], uint32_t(j >> 1) & 1u));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks)
+            tc_mma_ts(tmem + 2 * kTile + i * kTile, tmem + i * kTile + ks * 8,
+                      swizzled_desc(sv + stage * C::kTileBytes + ks * 2048, C::kBlockBytes),
+                      kDescPV, j > 0 || ks > 0);
+          tc_commit(&ctl->o_done[i]);
+          if (i == tiles - 1) tc_commit(&ctl->v_free[stage]);
+          if (more) {
+            if (i == 0) ok = wait(&ctl->k_full[next], uint32_t((j + 1) >> 1) & 1u);
+            if (!ok) break;
+            scores(i, next);
+            if (i == tiles - 1) tc_commit(&ctl->k_free[next]);
+          }
+        }
+      }
+      // all of this CTA's products are done before tensor memory is freed
+      tc_commit(&ctl->mma_done);
+      mbar_wait(&ctl->mma_done, 0);
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    // ---- keys and values.  Thread (token, t): words t of every chunk of the
+    // rows of four tokens of each tile; neighbouring lanes take tokens 4 apart,
+    // so that 8 lanes write 8 different bank groups.
+    const int t = lane & 3, o = lane >> 2, w = warp - 8;
+    const int tok = 8 * w + 4 * (o & 1) + (o >> 1);  // and + 32, 64, 96
+    const int* const table =
+        p.a.batch.page_table + int64_t(block.b) * p.a.batch.table_stride;
+    const Cache& cache = p.a.cache;
+    uint32_t kc[4][NC], vc[4][NC], km[4][NG], vm[4][NG];
+    int page[4];
+    int64_t at[4];  // row of the cache, or -1 behind the last token
+    auto read_pages = [&](int j) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int pos = j * kTile + 32 * u + tok;
+        page[u] = pos < limit ? table[pos >> cache.page_shift] : -1;
+      }
+    };
+    auto read_keys = [&](int j) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int pos = j * kTile + 32 * u + tok;
+        at[u] = -1;
+#pragma unroll
+        for (int k = 0; k < NC; ++k) kc[u][k] = 0u;
+#pragma unroll
+        for (int k = 0; k < NG; ++k) km[u][k] = 0u;
+        if (pos >= limit) continue;
+        if (uint32_t(page[u]) >= uint32_t(cache.pages)) {
+          record_status(kStatusInvalid);
+          page[u] = 0;  // any page of the cache can be read
+        }
+        at[u] = ((int64_t(page[u]) * heads + head) << cache.page_shift) +
+                (pos & ((1 << cache.page_shift) - 1));
+        load_words<NC>(cache.k_codes + at[u] * (D / 2) + t * NC * 4, kc[u]);
+        load_words<NG>(reinterpret_cast<const unsigned char*>(cache.k_meta + at[u] * NG), km[u]);
+      }
+    };
+    auto read_values = [&] {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+#pragma unroll
+        for (int k = 0; k < NC; ++k) vc[u][k] = 0u;
+#pragma unroll
+        for (int k = 0; k < NG; ++k) vm[u][k] = 0u;
+        if (at[u] < 0) continue;
+        load_words<NC>(cache.v_codes + at[u] * (D / 2) + t * NC * 4, vc[u]);
+        load_words<NG>(reinterpret_cast<const unsigned char*>(cache.v_meta + at[u] * NG), vm[u]);
+      }
+    };
+    // eight codes -> eight values in the unpack's order, 16 bytes
+    auto expand = [&](uint32_t word, uint32_t meta, bool wide) {
+      const uint32_t z2 = __byte_perm(meta, meta, 0x3232);
+      uint32_t s2 = __byte_perm(meta, meta, 0x1010);
+      if (wide) s2 = hmul2(s2, 0x38003800u);  // 1/2
+      const uint32_t lo = hadd2(z2, 0x64006400u);   // 1024 + z
+      const uint32_t hi = hsub2(0xD400D400u, z2);   // -(64 + z)
+      const uint32_t w8 = word >> 8;
+      uint4 r;
+      r.x = hmul2(hsub2(lop3_and_or(word, 0x000F000Fu, 0x64006400u), lo), s2);
+      r.y = hmul2(hfma2(lop3_and_or(word, 0x00F000F0u, 0x64006400u), 0x2C002C00u, hi), s2);
+      r.z = hmul2(hsub2(lop3_and_or(w8, 0x000F000Fu, 0x64006400u), lo), s2);
+      r.w = hmul2(hfma2(lop3_and_or(w8, 0x00F000F0u, 0x64006400u), 0x2C002C00u, hi), s2);
+      return r;
+    };
+    auto place = [&](unsigned char* tile, int u, int j) {
+      const int row = 32 * u + tok, chunk = 4 * j + t;
+      return reinterpret_cast<uint4*>(tile + (chunk >> 3) * C::kBlockBytes + row * 128 +
+                                      (((chunk & 7) ^ (row & 7)) << 4));
+    };
+    if (steps > 0) {
+      read_pages(0);
+      read_keys(0);
+      read_values();
+      if (steps > 1) read_pages(1);
+    }
+    bool ok = true;
+    for (int j = 0; j < steps; ++j) {
+      const int stage = j & 1;
+      const uint32_t parity = (uint32_t(j >> 1) & 1u) ^ 1u;
+      bool wide = false;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int k = 0; k < NG; ++k)
+          wide |= meta_pair(km[u][k]).x > float(kWideScale) ||
+                  meta_pair(vm[u][k]).x > float(kWideScale);
+      wide = named_barrier_or(1, 128, wide);
+      // after a wait that gave up, the loop only keeps the barrier's count
+      ok = ok && __all_sync(0xffffffffu, wait(&ctl->k_free[stage], parity));
+      if (!ok) continue;
+      unsigned char* const ktile = smem + C::kOffK + stage * C::kTileBytes;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+          *place(ktile, u, k) = expand(kc[u][k], km[u][k * 32 / G], wide);
+      if (tid == 256) *reinterpret_cast<volatile int*>(&ctl->wide[j & 3]) = wide ? 1 : 0;
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->k_full[stage]);
+      if (j + 1 < steps) read_keys(j + 1);
+
+      ok = __all_sync(0xffffffffu, wait(&ctl->v_free[stage], parity));
+      if (!ok) continue;
+      unsigned char* const vtile = smem + C::kOffV + stage * C::kTileBytes;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+          const uint32_t word = __byte_perm(vc[u][k / 2], vc[u][NC / 2 + k / 2],
+                                            (k & 1) ? 0x7632 : 0x5410);
+          *place(vtile, u, k) = expand(word, vm[u][k * 32 / G], wide);
+        }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->v_full[stage]);
+      if (j + 1 < steps) {
+        read_values();
+        if (j + 2 < steps) read_pages(j + 2);
+      }
+    }
+  } else if ((warp >> 2) < tiles) {
+    // ---- softmax: this thread's row
+    const int i = warp >> 2, local = (warp & 3) * 32 + lane;
+    const int r = block.row + i * kTile + local;
+    const bool have = i * kTile + local < rows;
+    const uint32_t s_tmem = tmem + i * kTile + (uint32_t((warp & 3) * 32) << 16);
+    const uint32_t o_tmem = s_tmem + 2 * kTile;
+    float c;  // base 2 scale of the row's scores, not negative
+    {
+      uint4 raw[D / 8];
+      const __nv_bfloat16* row = p.a.Q + row_offset(p.a, seq.row0, r, head, p.a.q_stride, D);
+      float top = 0.f;
+#pragma unroll
+      for (int e = 0; e < D / 8; ++e) {
+        raw[e] = make_uint4(0, 0, 0, 0);
+        if (have) raw[e] = *reinterpret_cast<const uint4*>(row + 8 * e);
+      }
+#pragma unroll
+      for (int e = 0; e < D / 8; ++e) {
+        const uint32_t w[4] = {raw[e].x, raw[e].y, raw[e].z, raw[e].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = bf16x2_to_float2(w[k]);
+          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      const int exponent = int(__float_as_uint(top) >> 23);  // biased
+      const int up = top > 0.f ? min(141 - exponent, 126) : 0;
+      // the sign of the softmax scale goes to the queries
+      const float mult = copysignf(__uint_as_float(uint32_t(up + 127) << 23), p.a.scale_log2);
+      c = fabsf(p.a.scale_log2) * __uint_as_float(uint32_t(127 - up) << 23);
+      unsigned char* const tile = smem + C::kOffQ + i * C::kTileBytes + local * 128;
+#pragma unroll
+      for (int e = 0; e < D / 8; ++e) {
+        const float2 a = bf16x2_to_float2(raw[e].x), b = bf16x2_to_float2(raw[e].y),
+                     d = bf16x2_to_float2(raw[e].z), f = bf16x2_to_float2(raw[e].w);
+        *reinterpret_cast<uint4*>(tile + (e >> 3) * C::kBlockBytes +
+                                  (((e & 7) ^ (local & 7)) << 4)) =
+            make_uint4(pack_half2(a.x * mult, d.x * mult), pack_half2(a.y * mult, d.y * mult),
+                       pack_half2(b.x * mult, f.x * mult), pack_half2(b.y * mult, f.y * mult));
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->q_full[i]);
+    }
+    const int my_limit = have ? seq.len - seq.rows + p.a.by_gqa(r) + 1 : 0;
+    const int least = __reduce_min_sync(0xffffffffu, my_limit);
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < steps; ++j) {
+      ok = __all_sync(0xffffffffu, wait(&ctl->s_full[i], uint32_t(j) & 1u));
+      if (!ok) break;
+      tc_fence_after();
+      const bool wide = *reinterpret_cast<volatile int*>(&ctl->wide[j & 3]) != 0;
+      const float cj = wide ? 2.f * c : c;
+      const int first = j * kTile, seen = my_limit - first;  // columns below `seen` count
+      const bool masked = first + kTile > least;
+      float v[32];
+      float top = -INFINITY;
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) {
+        tmem_ld32(s_tmem + 32 * ch, v);
+        tmem_wait_ld();
+        if (masked) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (32 * ch + k >= seen) v[k] = -INFINITY;
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) top = fmaxf(top, v[k]);
+      }
+      // the reference rises only when a weight would pass 2^14
+      const float highest = top == -INFINITY ? -INFINITY : top * cj;
+      const bool raise = highest > m + 14.f;
+      if (__any_sync(0xffffffffu, raise)) {
+        const float next = raise ? highest - 7.f : m;
+        const float f = raise ? exp2_approx(m - next) : 1.f;
+        m = next;
+        l *= f;
+        if (j > 0) {
+          ok = __all_sync(0xffffffffu, wait(&ctl->o_done[i], uint32_t(j - 1) & 1u));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int ch = 0; ch < D / 32; ++ch) {
+            tmem_ld32(o_tmem + 32 * ch, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] *= f;
+            gemm::tmem_st32(o_tmem + 32 * ch, v);
+          }
+          tmem_wait_st();
+        }
+      }
+      // a halved tile of values takes doubled weights
+      const float ref = (m == -INFINITY ? 0.f : m) - (wide ? 1.f : 0.f);
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) {
+        tmem_ld32(s_tmem + 32 * ch, v);
+        tmem_wait_ld();
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          float2 e = fma2(make_float2(v[2 * k], v[2 * k + 1]), make_float2(cj, cj),
+                          make_float2(-ref, -ref));
+          e.x = exp2_approx(e.x);
+          e.y = exp2_approx(e.y);
+          if (masked) {
+            if (32 * ch + 2 * k >= seen) e.x = 0.f;
+            if (32 * ch + 2 * k + 1 >= seen) e.y = 0.f;
+          }
+          sum = add2(sum, e);
+          w[k] = pack_half2(e.x, e.y);
+        }
+        tmem_st16(s_tmem + 16 * ch, w);
+      }
+      l += wide ? 0.5f * (sum.x + sum.y) : sum.x + sum.y;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->p_full[i]);
+    }
+    if (ok && steps > 0)
+      ok = __all_sync(0xffffffffu, wait(&ctl->o_done[i], uint32_t(steps - 1) & 1u));
+    if (ok) {
+      tc_fence_after();
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      __nv_bfloat16* row = p.a.O + row_offset(p.a, seq.row0, r, head, p.a.o_stride, D);
+#pragma unroll
+      for (int ch = 0; ch < D / 32; ++ch) {
+        float v[32];
+        if (steps > 0) {
+          tmem_ld32(o_tmem + 32 * ch, v);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x[8];  // dims in order: the tile holds 0, 4, 1, 5, 2, 6, 3, 7
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            x[(k >> 1) + 4 * (k & 1)] = l == 0.f ? 0.f : v[8 * e + k] * inv;
+          if (have)
+            *reinterpret_cast<uint4*>(row + 32 * ch + 8 * e) =
+                make_uint4(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]),
+                           pack_bf162(x[4], x[5]), pack_bf162(x[6], x[7]));
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+  }
+}
+
+}  // namespace kv4
+}  // namespace wq
