@@ -54,24 +54,26 @@ cudaError_t dispatch_kv4(int head_dim, int group, const Args&... args) {
   return cudaErrorInvalidValue;
 }
 
-// Warps per row (each takes up to kRowIterations * 32 pieces of 8 elements),
+// Warps per row (each takes up to kRowIterations * 32 pieces of 16 elements),
 // and the CTAs that all rows make.
 int row_chunks(const wq_kv4_cache& c) {
-  const int pieces = c.kv_heads * (c.head_dim / 8), per_warp = kv4::kRowIterations * 32;
-  return (pieces + per_warp - 1) / per_warp;
+  const int64_t pieces = int64_t(c.kv_heads) * (c.head_dim / 16);
+  const int per_warp = kv4::kRowIterations * 32;
+  return int((pieces + per_warp - 1) / per_warp);
 }
 
-int64_t row_ctas(const wq_kv4_cache& c, int rows) {
-  return (int64_t(rows) * row_chunks(c) + kv4::kRowWarps - 1) / kv4::kRowWarps;
+int64_t row_warps(const wq_kv4_cache& c, int rows) { return int64_t(rows) * row_chunks(c); }
+
+unsigned row_ctas(const wq_kv4_cache& c, int rows) {
+  return unsigned((row_warps(c, rows) + kv4::kRowWarps - 1) / kv4::kRowWarps);
 }
 
 template <int D, int G>
 struct WriteOp {
   static cudaError_t run(const void* K, int64_t ks, const void* V, int64_t vs,
                          const wq_kv4_cache& c, const wq_kv4_batch& b, cudaStream_t s) {
-    const int64_t ctas = row_ctas(c, b.rows);
-    if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-    kv4::write_kernel<D, G><<<unsigned(ctas), kv4::kRowWarps * 32, 0, s>>>(
+    if (row_warps(c, b.rows) >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    kv4::write_kernel<D, G><<<row_ctas(c, b.rows), kv4::kRowWarps * 32, 0, s>>>(
         static_cast<const __nv_bfloat16*>(K), ks, static_cast<const __nv_bfloat16*>(V), vs,
         device_cache(c), device_batch(b, c.page_size), row_chunks(c));
     return cudaGetLastError();
@@ -82,22 +84,21 @@ template <int D, int G>
 struct ReadOp {
   static cudaError_t run(const wq_kv4_cache& c, const wq_kv4_batch& b, void* K, void* V,
                          cudaStream_t s) {
-    const int64_t ctas = row_ctas(c, b.rows);
-    if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-    kv4::read_kernel<D, G><<<unsigned(ctas), kv4::kRowWarps * 32, 0, s>>>(
+    if (row_warps(c, b.rows) >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    kv4::read_kernel<D, G><<<row_ctas(c, b.rows), kv4::kRowWarps * 32, 0, s>>>(
         device_cache(c), device_batch(b, c.page_size), static_cast<__nv_bfloat16*>(K),
         static_cast<__nv_bfloat16*>(V), row_chunks(c));
     return cudaGetLastError();
   }
 };
 
-template <int D, int G, int NT, int WARPS>
+template <int D, int G, int NT, int WARPS, int TILES>
 cudaError_t launch_attn(const kv4::AttnParams& p, cudaStream_t s, int sms) {
   using C = kv4::AttnConfig<D, G, NT, WARPS>;
   constexpr size_t smem = C::kOffCtl + C::kCtlBytes;
   static_assert(smem <= 232448, "shared memory of one CTA");
   static int configured[kMaxDevices] = {};
-  auto kernel = kv4::attn_kernel<D, G, NT, WARPS>;
+  auto kernel = kv4::attn_kernel<D, G, NT, WARPS, TILES>;
   const cudaError_t e = configure_smem(kernel, configured, smem);
   if (e != cudaSuccess) return e;
   kernel<<<unsigned(std::min(sms, kv4::kMaxCtas)), C::kThreads, smem, s>>>(p);
@@ -107,8 +108,9 @@ cudaError_t launch_attn(const kv4::AttnParams& p, cudaStream_t s, int sms) {
 template <int D, int G>
 struct AttnOp {
   static cudaError_t run(const kv4::AttnParams& p, int max_columns, cudaStream_t s, int sms) {
-    if (max_columns <= 8) return launch_attn<D, G, 1, 12>(p, s, sms);
-    return launch_attn<D, G, 2, 8>(p, s, sms);
+    constexpr bool kFourGroups = D / G == 4;
+    if (max_columns <= 8) return launch_attn<D, G, 1, 12, kFourGroups ? 1 : 2>(p, s, sms);
+    return launch_attn<D, G, 2, D == 64 ? 12 : 8, 1>(p, s, sms);
   }
 };
 

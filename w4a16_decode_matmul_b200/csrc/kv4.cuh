@@ -22,6 +22,7 @@
 
 #include "common.cuh"
 #include "quantize.cuh"
+#include "unpack.cuh"
 
 namespace wq {
 namespace kv4 {
@@ -138,161 +139,306 @@ __device__ __forceinline__ float2 bf16x2_to_float2(uint32_t v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
-// A bfloat16 as the binary16 value the format quantizes.
-__device__ __forceinline__ float to_format(float x) {
-  return __half2float(__float2half_rn(fminf(fmaxf(x, -65504.f), 65504.f)));
+// Two bfloat16 as the binary16 values the format quantizes (saturating).
+__device__ __forceinline__ uint32_t to_format(uint32_t v) {
+  const float2 f = bf16x2_to_float2(v);
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
+  return r;
 }
 
-// Eight values of a group that LANES adjacent lanes share -> the word of
-// their codes, scale and zero.  The scale is exact: __fadd_ru and __fdiv_ru
-// round up in binary32 and __float2half_ru to binary16; 15 c has 15
-// significant bits for a binary16 c, so no c lies between (hi - lo)/15 and
-// its binary32 round-ups, and the result is the smallest binary16 that is not
-// below the exact quotient.
+__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ float2 half2_to_float2(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+// Smallest binary16 that is not below r / 15, for the range r >= 0 of a group
+// rounded up to binary32: 15 c has 15 significant bits for a binary16 c, so
+// rounding r up crosses no 15 c, and the comparisons below are exact.  The
+// first guess is within one step.
+__device__ __forceinline__ float range_scale(float r) {
+  const unsigned short guess = __half_as_ushort(__float2half_ru(r * (1.f / 15.f)));
+  const float here = __half2float(__ushort_as_half(guess));
+  const float below = __half2float(__ushort_as_half((unsigned short)(guess - 1)));
+  const float above = __half2float(__ushort_as_half((unsigned short)(guess + 1)));
+  return 15.f * below >= r ? below : 15.f * here >= r ? here : above;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// Sixteen values of a group that LANES adjacent lanes share -> the two words
+// of their codes, scale and zero.
+//
+// The codes are round-half-even of the exact quotients x / s.  With inv within
+// 2^-23 of 1/s (relative), x inv is within 15 * 2^-22 < 2^-18 of x / s, so
+// rounding it decides every code whose x inv is farther than 2^-16 from a
+// half-integer; a lane with a nearer one decides its codes by the exact rule.
+// Outside that window no code needs a clamp: (hi - lo) / s <= 15, and
+// rint(hi/s) + rint(-lo/s) can be 16 only when both quotients are
+// half-integers.
 template <int LANES>
-__device__ __forceinline__ uint32_t quantize8(const uint4& raw, float* scale, float* zero) {
-  float x[8];
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  float lo = 0.f, hi = 0.f;
+__device__ __forceinline__ uint2 quantize16(const uint4 (&raw)[2], float* scale, float* zero) {
+  uint32_t h[8];
+  uint32_t hi = 0u, lo = 0u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = bf16x2_to_float2(w[i]);
-    x[2 * i] = to_format(f.x);
-    x[2 * i + 1] = to_format(f.y);
-    lo = fminf(lo, fminf(x[2 * i], x[2 * i + 1]));
-    hi = fmaxf(hi, fmaxf(x[2 * i], x[2 * i + 1]));
+  for (int i = 0; i < 2; ++i) {
+    h[4 * i] = to_format(raw[i].x);
+    h[4 * i + 1] = to_format(raw[i].y);
+    h[4 * i + 2] = to_format(raw[i].z);
+    h[4 * i + 3] = to_format(raw[i].w);
   }
-#pragma unroll
-  for (int m = 1; m < LANES; m *= 2) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
-  }
-  const float s =
-      hi > lo ? __half2float(__float2half_ru(__fdiv_ru(__fadd_ru(hi, -lo), 15.f))) : 1.f;
-  const float z = fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f) + 0.f;  // never -0
-  const float inv = __frcp_rn(s);
-  uint32_t word = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float q = fminf(fmaxf(rint_quotient(x[i], s, inv) + z, 0.f), 15.f);
-    word |= uint32_t(int(q)) << (4 * i);
+    hi = hmax2(hi, h[i]);
+    lo = hmin2(lo, h[i]);
+  }
+  // (hi, -lo) in one word
+  hi = hmax2(hi, __byte_perm(hi, hi, 0x1032));
+  lo = hmin2(lo, __byte_perm(lo, lo, 0x1032));
+  uint32_t ends = __byte_perm(hi, lo ^ 0x80008000u, 0x5410);
+#pragma unroll
+  for (int m = 1; m < LANES; m *= 2) ends = hmax2(ends, __shfl_xor_sync(0xffffffffu, ends, m));
+  const float2 end = half2_to_float2(ends);
+  const float range = __fadd_ru(end.x, end.y);
+  const float s = range > 0.f ? range_scale(range) : 1.f;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  const float z = fminf(rint_quotient(end.y, s, inv), 15.f);
+  // 1.5 * 2^23 + z: the sum below lands on the integers, its low bits the code
+  const float shift = 12582912.f + z;
+  uint32_t u[16];
+  float off = 0.f;  // the largest distance from the rounded value
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 x = half2_to_float2(h[i]);
+    const float2 a = fma2(x, make_float2(inv, inv), make_float2(shift, shift));
+    // shift - a is minus the rounded quotient, exactly
+    const float2 r = fma2(a, make_float2(-1.f, -1.f), make_float2(shift, shift));
+    const float2 e = fma2(x, make_float2(inv, inv), r);
+    off = fmaxf(off, fmaxf(fabsf(e.x), fabsf(e.y)));
+    u[2 * i] = __float_as_uint(a.x);
+    u[2 * i + 1] = __float_as_uint(a.y);
+  }
+  uint32_t word[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t bytes[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      bytes[k] = (u[8 * i + 2 * k] & 15u) | ((u[8 * i + 2 * k + 1] << 4) & 0xf0u);
+    word[i] = __byte_perm(__byte_perm(bytes[0], bytes[1], 0x0040),
+                          __byte_perm(bytes[2], bytes[3], 0x0040), 0x5410);
+  }
+  if (off > 0.5f - 0x1p-16f) {
+    word[0] = word[1] = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 x = half2_to_float2(h[i]);
+      const float a = fminf(fmaxf(rint_quotient(x.x, s, inv) + z, 0.f), 15.f);
+      const float b = fminf(fmaxf(rint_quotient(x.y, s, inv) + z, 0.f), 15.f);
+      word[i >> 2] |= (uint32_t(int(a)) | (uint32_t(int(b)) << 4)) << (8 * (i & 3));
+    }
   }
   *scale = s;
-  *zero = z;
-  return word;
+  *zero = z + 0.f;  // never -0
+  return make_uint2(word[0], word[1]);
 }
 
-constexpr int kRowWarps = 8;       // warps of a CTA of the two row kernels
-constexpr int kRowIterations = 4;  // 16-byte pieces of keys and values per lane
-
-// Rows into the cache, values as kv4.cuh's header defines them.  A warp takes
-// up to 128 pieces of 8 elements of one row (four heads of 64 ... ), all of
-// its loads first.  HBM bound: 4 D bytes read and D + 8 D/G written per row
-// and head.
-template <int D, int G>
-__global__ void __launch_bounds__(kRowWarps * 32)
-    write_kernel(const __nv_bfloat16* __restrict__ K, int64_t k_stride,
-                 const __nv_bfloat16* __restrict__ V, int64_t v_stride, Cache cache, Batch batch,
-                 int chunks) {
-  constexpr int NC = D / 32, NG = D / G, kPieces = D / 8;
-  const int lane = threadIdx.x & 31;
-  const int64_t item = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  if (item >= int64_t(batch.rows) * chunks) return;
-  const int r = int(item / chunks), chunk = int(item % chunks);
-  const int pieces = cache.kv_heads * kPieces;
-  uint4 k[kRowIterations], v[kRowIterations];
-#pragma unroll
-  for (int it = 0; it < kRowIterations; ++it) {
-    const int e = (chunk * kRowIterations + it) * 32 + lane;
-    if (e < pieces) {
-      k[it] = ldg_stream128(K + int64_t(r) * k_stride + int64_t(e) * 8);
-      v[it] = ldg_stream128(V + int64_t(r) * v_stride + int64_t(e) * 8);
-    } else {
-      k[it] = v[it] = make_uint4(0, 0, 0, 0);
-    }
-  }
-  const Place at = find_place(batch, cache, r, lane);
-  if (at.page < 0) return;  // the whole warp: one row
-#pragma unroll
-  for (int it = 0; it < kRowIterations; ++it) {
-    const int e = (chunk * kRowIterations + it) * 32 + lane;
-    if (e - lane >= pieces) break;
-    float ks, kz, vs, vz;
-    const uint32_t kw = quantize8<G / 8>(k[it], &ks, &kz);
-    const uint32_t vw = quantize8<G / 8>(v[it], &vs, &vz);
-    // value halfwords of chunks j (even) and j + 1 are neighbours in memory:
-    // lanes of the two chunks swap one halfword each and store one word each
-    const int l = e % kPieces, j = l / 4, t = l % 4;
-    const uint32_t give = (j & 1) ? (vw & 0xffffu) : (vw >> 16);
-    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 4);
-    if (e >= pieces) continue;
-    const int64_t token =
-        ((at.page * cache.kv_heads + e / kPieces) << cache.page_shift) + at.slot;
-    reinterpret_cast<uint32_t*>(cache.k_codes + token * (D / 2))[t * NC + j] = kw;
-    const uint32_t pair = (j & 1) ? (got | (vw & 0xffff0000u)) : ((vw & 0xffffu) | (got << 16));
-    reinterpret_cast<uint32_t*>(cache.v_codes + token * (D / 2))[((2 * t + (j & 1)) * NC + j) / 2] =
-        pair;
-    if (l % (G / 8) == 0) {
-      cache.k_meta[token * NG + l / (G / 8)] = __floats2half2_rn(ks, kz);
-      cache.v_meta[token * NG + l / (G / 8)] = __floats2half2_rn(vs, vz);
-    }
-  }
+// Halfwords of value codes: a lane holds those of g0 .. g0 + 3 of one chunk
+// (two words); the lane two further or back holds the neighbouring chunk's.
+// What is adjacent in memory is the pair of chunks of one g: after the swap
+// the lane of the even chunk has the pairs of g0 and g0 + 1, the other those of
+// g0 + 2 and g0 + 3.  The same swap undoes itself.
+__device__ __forceinline__ uint2 swap_chunks(uint2 w, bool odd) {
+  // words as pairs (g, g + 1) of one chunk <-> pairs (even, odd chunk) of one g
+  const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w.x : w.y, 2);
+  const uint32_t even = odd ? got : w.x, other = odd ? w.y : got;
+  return make_uint2(__byte_perm(even, other, 0x5410), __byte_perm(even, other, 0x7632));
 }
 
-// Eight codes -> eight bfloat16 values s (u - z): the product is exact in
-// binary32 (11 + 4 bits) and rounded once.
+__device__ __forceinline__ uint2 unswap_chunks(uint2 w, bool odd) {
+  // w.x = (even, odd) of g, w.y of g + 1
+  const uint32_t even = __byte_perm(w.x, w.y, 0x5410), other = __byte_perm(w.x, w.y, 0x7632);
+  const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? even : other, 2);
+  return odd ? make_uint2(got, other) : make_uint2(even, got);
+}
+
+// Eight codes -> eight bfloat16 values s (u - z): u - z is exact in binary16,
+// the product in binary32 (11 + 4 bits), and it is rounded once.
 __device__ __forceinline__ uint4 values8(uint32_t word, __half2 meta) {
-  const float2 m = __half22float2(meta);
+  const float s = __low2float(meta);
+  const __half2 zero = __high2half2(meta);
+  uint32_t u[4];  // (0, 4), (1, 5), (2, 6), (3, 7)
+  unpack_u4_h<0>(word, u);
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = half2_to_float2(hsub2(u[i], *reinterpret_cast<const uint32_t*>(&zero)));
+    x[i] = s * f.x;
+    x[i + 4] = s * f.y;
+  }
   uint32_t out[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = m.x * (float((word >> (8 * i)) & 15u) - m.y);
-    const float b = m.x * (float((word >> (8 * i + 4)) & 15u) - m.y);
-    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
     out[i] = *reinterpret_cast<const uint32_t*>(&p);
   }
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
+constexpr int kRowWarps = 8;       // warps of a CTA of the two row kernels
+constexpr int kRowIterations = 2;  // pieces of 16 keys and 16 values per lane
+
+// The place of a lane in the rows: it takes elements 16 lambda .. of every
+// (32 / lanes of a head)-th head.
+template <int D, int G>
+struct RowLane {
+  static constexpr int kLanes = D / 16;          // of a head
+  static constexpr int kHeads = 32 / kLanes;     // of an iteration
+  static constexpr int NC = D / 32, NG = D / G;
+  int head, elem, chunk, t, group;
+  bool odd, owns_meta;
+  __device__ RowLane(int lane, int chunk_of_row) {
+    const int lambda = lane % kLanes;
+    head = chunk_of_row * kRowIterations * kHeads + lane / kLanes;
+    elem = 16 * lambda;
+    chunk = lambda >> 1;
+    t = 2 * (lambda & 1);
+    group = elem / G;
+    odd = chunk & 1;
+    owns_meta = elem % G == 0;
+  }
+  // word of key word t of this chunk; words of the value pairs after the swap
+  __device__ int key_word(int i) const { return (t + i) * NC + chunk; }
+  __device__ int value_word(int i) const {
+    return ((2 * t + (odd ? 2 : 0) + i) * NC + (chunk & ~1)) / 2;
+  }
+};
+
+// Rows into the cache, values as kv4.cuh's header defines them.  A warp takes
+// up to 1,024 keys and values of one row, all of its loads first.  HBM bytes:
+// 4 D read and D + 8 D/G written per row and head.
+template <int D, int G>
+__global__ void __launch_bounds__(kRowWarps * 32, 4)
+    write_kernel(const __nv_bfloat16* __restrict__ K, int64_t k_stride,
+                 const __nv_bfloat16* __restrict__ V, int64_t v_stride, Cache cache, Batch batch,
+                 int chunks) {
+  using L = RowLane<D, G>;
+  const int lane = threadIdx.x & 31;
+  const int item = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  if (item >= batch.rows * chunks) return;
+  const int r = item / chunks;
+  const L my(lane, item - r * chunks);
+  uint4 k[kRowIterations][2], v[kRowIterations][2];
+  const uint4* from_k =
+      reinterpret_cast<const uint4*>(K + int64_t(r) * k_stride + my.head * D + my.elem);
+  const uint4* from_v =
+      reinterpret_cast<const uint4*>(V + int64_t(r) * v_stride + my.head * D + my.elem);
+#pragma unroll
+  for (int it = 0; it < kRowIterations; ++it)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      k[it][i] = v[it][i] = make_uint4(0, 0, 0, 0);
+      if (my.head + it * L::kHeads < cache.kv_heads) {
+        k[it][i] = __ldg(from_k + it * (L::kHeads * D / 8) + i);
+        v[it][i] = __ldg(from_v + it * (L::kHeads * D / 8) + i);
+      }
+    }
+  const Place at = find_place(batch, cache, r, lane);
+  if (at.page < 0) return;  // the whole warp: one row
+  int64_t token = ((at.page * cache.kv_heads + my.head) << cache.page_shift) + at.slot;
+#pragma unroll
+  for (int it = 0; it < kRowIterations; ++it) {
+    float ks, kz, vs, vz;
+    const uint2 kw = quantize16<G / 16>(k[it], &ks, &kz);
+    const uint2 vw = swap_chunks(quantize16<G / 16>(v[it], &vs, &vz), my.odd);
+    if (my.head + it * L::kHeads < cache.kv_heads) {
+      uint32_t* const to_k = reinterpret_cast<uint32_t*>(cache.k_codes + token * (D / 2));
+      uint32_t* const to_v = reinterpret_cast<uint32_t*>(cache.v_codes + token * (D / 2));
+      to_k[my.key_word(0)] = kw.x;
+      to_k[my.key_word(1)] = kw.y;
+      to_v[my.value_word(0)] = vw.x;
+      to_v[my.value_word(1)] = vw.y;
+      if (my.owns_meta) {
+        cache.k_meta[token * L::NG + my.group] = __floats2half2_rn(ks, kz);
+        cache.v_meta[token * L::NG + my.group] = __floats2half2_rn(vs, vz);
+      }
+    }
+    token += int64_t(L::kHeads) << cache.page_shift;
+  }
+}
+
 // The values of cached rows, bfloat16 [rows][kv_heads][D].  Rows of a
 // sequence that hold no token get zeros; rows of no sequence are left alone.
 template <int D, int G>
-__global__ void __launch_bounds__(kRowWarps * 32)
+__global__ void __launch_bounds__(kRowWarps * 32, 4)
     read_kernel(Cache cache, Batch batch, __nv_bfloat16* __restrict__ K,
                 __nv_bfloat16* __restrict__ V, int chunks) {
-  constexpr int NC = D / 32, NG = D / G, kPieces = D / 8;
+  using L = RowLane<D, G>;
   const int lane = threadIdx.x & 31;
-  const int64_t item = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  if (item >= int64_t(batch.rows) * chunks) return;
-  const int r = int(item / chunks), chunk = int(item % chunks);
-  const int pieces = cache.kv_heads * kPieces;
+  const int item = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  if (item >= batch.rows * chunks) return;
+  const int r = item / chunks;
+  const L my(lane, item - r * chunks);
   const Place at = find_place(batch, cache, r, lane);
   if (at.page < 0 && !at.empty) return;
-  uint32_t kw[kRowIterations], vw[kRowIterations];
+  uint2 kw[kRowIterations], vw[kRowIterations];
   __half2 km[kRowIterations], vm[kRowIterations];
+  int64_t token = ((at.page * cache.kv_heads + my.head) << cache.page_shift) + at.slot;
 #pragma unroll
   for (int it = 0; it < kRowIterations; ++it) {
-    const int e = (chunk * kRowIterations + it) * 32 + lane;
-    kw[it] = vw[it] = 0;
+    kw[it] = vw[it] = make_uint2(0, 0);
     km[it] = vm[it] = __half2half2(__ushort_as_half(0));
-    if (e < pieces && !at.empty) {
-      const int l = e % kPieces, j = l / 4, t = l % 4;
-      const int64_t token =
-          ((at.page * cache.kv_heads + e / kPieces) << cache.page_shift) + at.slot;
-      kw[it] = reinterpret_cast<const uint32_t*>(cache.k_codes + token * (D / 2))[t * NC + j];
-      const uint16_t* vrow = reinterpret_cast<const uint16_t*>(cache.v_codes + token * (D / 2));
-      vw[it] = uint32_t(vrow[2 * t * NC + j]) | (uint32_t(vrow[(2 * t + 1) * NC + j]) << 16);
-      km[it] = cache.k_meta[token * NG + l / (G / 8)];
-      vm[it] = cache.v_meta[token * NG + l / (G / 8)];
+    if (my.head + it * L::kHeads < cache.kv_heads && !at.empty) {
+      const uint32_t* const k = reinterpret_cast<const uint32_t*>(cache.k_codes + token * (D / 2));
+      const uint32_t* const v = reinterpret_cast<const uint32_t*>(cache.v_codes + token * (D / 2));
+      kw[it] = make_uint2(k[my.key_word(0)], k[my.key_word(1)]);
+      vw[it] = make_uint2(v[my.value_word(0)], v[my.value_word(1)]);
+      km[it] = cache.k_meta[token * L::NG + my.group];
+      vm[it] = cache.v_meta[token * L::NG + my.group];
     }
+    token += int64_t(L::kHeads) << cache.page_shift;
   }
+  const int64_t first = (int64_t(r) * cache.kv_heads + my.head) * D + my.elem;
 #pragma unroll
   for (int it = 0; it < kRowIterations; ++it) {
-    const int e = (chunk * kRowIterations + it) * 32 + lane;
-    if (e < pieces) {
-      const int64_t to = (int64_t(r) * pieces + e) * 8;
-      *reinterpret_cast<uint4*>(K + to) = values8(kw[it], km[it]);
-      *reinterpret_cast<uint4*>(V + to) = values8(vw[it], vm[it]);
+    const uint2 w = unswap_chunks(vw[it], my.odd);
+    if (my.head + it * L::kHeads < cache.kv_heads) {
+      uint4* const to_k = reinterpret_cast<uint4*>(K + first + it * (L::kHeads * D));
+      uint4* const to_v = reinterpret_cast<uint4*>(V + first + it * (L::kHeads * D));
+      to_k[0] = values8(kw[it].x, km[it]);
+      to_k[1] = values8(kw[it].y, km[it]);
+      to_v[0] = values8(w.x, vm[it]);
+      to_v[1] = values8(w.y, vm[it]);
     }
   }
 }

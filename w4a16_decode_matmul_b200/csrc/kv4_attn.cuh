@@ -228,6 +228,10 @@ __device__ __forceinline__ int64_t row_offset(const AttnParams& p, int row0, int
   return int64_t(row0 + i) * stride + int64_t(h * p.gqa + (r - i * p.gqa)) * D;
 }
 
+// The reference of a row that has seen no token yet: finite, so that no
+// difference of two is NaN, and below any score that binary32 tells apart.
+constexpr float kNoReference = -1e30f;
+
 // The segment that unit q belongs to, and q's place in it, for a warp that
 // asks with all its lanes: the block's threads have left the prefix sums of
 // their sequences' units in shared memory.
@@ -273,7 +277,7 @@ __device__ __forceinline__ int find_segment(const AttnParams& p, const AttnContr
   return unit;
 }
 
-template <int D, int G, int NT, int WARPS>
+template <int D, int G, int NT, int WARPS, int TILES>
 __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p) {
   using C = AttnConfig<D, G, NT, WARPS>;
   constexpr int NC = C::kChunks, NG = C::kGroups, ROWS = C::kRows, NS = C::kStages;
@@ -433,7 +437,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
           const int exponent = int(__float_as_uint(top) >> 23);  // biased
           const int up = top > 0.f ? min(141 - exponent, 126) : 0;
-          const float mult = __uint_as_float(uint32_t(up + 127) << 23);
+          // the sign of the softmax scale goes to the queries
+          const float mult =
+              copysignf(__uint_as_float(uint32_t(up + 127) << 23), p.scale_log2);
           float sums[NG];
 #pragma unroll
           for (int k = 0; k < NG; ++k) sums[k] = 0.f;
@@ -463,13 +469,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
             for (int c = 0; c < 2; ++c)
               sum_q[nt][k][c] = __shfl_sync(0xffffffffu, sums[k], (2 * t + c) * 4);
           }
-          const float qs = p.scale_log2 * __uint_as_float(uint32_t(127 - up) << 23);
+          const float qs = fabsf(p.scale_log2) * __uint_as_float(uint32_t(127 - up) << 23);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             q_scale[nt][c] = __shfl_sync(0xffffffffu, qs, (2 * t + c) * 4);
             const int rc = cs.rb * ROWS + nt * 8 + 2 * t + c;
             limit[nt][c] = rc < cs.rows * p.gqa ? cs.len - cs.rows + p.by_gqa(rc) + 1 : 0;
-            m[nt][c] = -INFINITY;
+            m[nt][c] = kNoReference;
             l[nt][c] = 0.f;
 #pragma unroll
             for (int k = 0; k < NG; ++k) zc[nt][k][c] = 0.f;
@@ -487,12 +493,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
       // tokens that every row of the block sees need no mask
       const bool masked = tok0 + kUnit > seen_by_all;
 
-      // ---- scores (base 2) of the unit's two times 16 tokens
-      float x[2][NT][4];  // tokens a, a, b, b; columns 2t, 2t + 1
-      uint32_t vm[2][2][NG];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int ta = 16 * h + tok_a;
+      for (int h0 = 0; h0 < 2; h0 += TILES) {
+      // ---- scores (base 2) of TILES times 16 tokens
+      float x[TILES][NT][4];  // tokens a, a, b, b; columns 2t, 2t + 1
+      uint32_t vm[TILES][2][NG];
+#pragma unroll
+      for (int h = 0; h < TILES; ++h) {
+        const int ta = 16 * (h0 + h) + tok_a;
         uint32_t wa[NC], wb[NC], km[2][NG];
         load_words<NC>(stage + ta * (D / 2) + t * NC * 4, wa);
         load_words<NC>(stage + (ta + 8) * (D / 2) + t * NC * 4, wb);
@@ -508,7 +516,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
 #pragma unroll
           for (int k = 0; k < NG; ++k)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[nt][k][c] = 8.f * sum_q[nt][k][c & 1];
+            for (int c = 0; c < 4; ++c) acc[nt][k][c] = 0.f;
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
           uint32_t ua[4], ub[4];
@@ -539,32 +547,35 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const float y = fmaf(-f.y, sum_q[nt][k][c], acc[nt][k][2 * i + c]);
+                const float y = fmaf(8.f - f.y, sum_q[nt][k][c], acc[nt][k][2 * i + c]);
                 x[h][nt][2 * i + c] = k == 0 ? f.x * y : fmaf(f.x, y, x[h][nt][2 * i + c]);
               }
           }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[h][nt][c] *= q_scale[nt][c & 1];
         if (masked) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              if (tok0 + ta + 8 * (c >> 1) >= limit[nt][c & 1]) x[h][nt][c] = -INFINITY;
+              x[h][nt][c] = tok0 + ta + 8 * (c >> 1) >= limit[nt][c & 1]
+                                ? -INFINITY
+                                : x[h][nt][c] * q_scale[nt][c & 1];
         }
       }
 
       // ---- weights.  The reference m is raised where a segment begins and
       // when a weight passes 2^15, so that the largest becomes 2^7, and the
       // unit's weights are formed again.
-      uint32_t w16[2][2][NG][NT];  // pairs (columns 2t, 2t + 1) of tokens a and b
+      float scale[NT][2];  // of the scores (masked ones have it already)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) scale[nt][c] = masked ? 1.f : q_scale[nt][c];
+      uint32_t w16[TILES][2][NG][NT];  // pairs (columns 2t, 2t + 1) of tokens a and b
       while (true) {
         if (raise) {
-          float lw[2][2];  // log2 of the largest value scale of a token
+          float lw[TILES][2];  // log2 of the largest value scale of a token
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < TILES; ++h)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               float top = meta_pair(vm[h][i][0]).x;
@@ -576,13 +587,16 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float top = fmaxf(fmaxf(x[0][nt][c] + lw[0][0], x[0][nt][c + 2] + lw[0][1]),
-                                fmaxf(x[1][nt][c] + lw[1][0], x[1][nt][c + 2] + lw[1][1]));
+              float top = -INFINITY;
+#pragma unroll
+              for (int h = 0; h < TILES; ++h)
+                top = fmaxf(top, fmaxf(fmaf(x[h][nt][c], scale[nt][c], lw[h][0]),
+                                       fmaf(x[h][nt][c + 2], scale[nt][c], lw[h][1])));
 #pragma unroll
               for (int d = 4; d < 32; d *= 2)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
               const float next = fmaxf(m[nt][c], top - 7.f);
-              const float f = next == -INFINITY ? 1.f : exp2_approx(m[nt][c] - next);
+              const float f = exp2_approx(m[nt][c] - next);
               m[nt][c] = next;
               l[nt][c] *= f;
 #pragma unroll
@@ -606,7 +620,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
             for (int k = 0; k < NG; ++k) zc_next[nt][k][c] = zc[nt][k][c];
           }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < TILES; ++h)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -614,8 +628,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
               float e[2];
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                e[c] = exp2_approx(x[h][nt][2 * i + c] -
-                                   (m[nt][c] == -INFINITY ? 0.f : m[nt][c]));
+                e[c] = exp2_approx(fmaf(x[h][nt][2 * i + c], scale[nt][c], -m[nt][c]));
                 l_next[nt][c] += e[c];
               }
 #pragma unroll
@@ -652,7 +665,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
 
       // ---- values
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < TILES; ++h) {
         uint32_t b[NG][NT][2];
 #pragma unroll
         for (int k = 0; k < NG; ++k)
@@ -662,7 +675,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
             for (int i = 0; i < 2; ++i) b[k][nt][i] = transpose8x8(w16[h][i][k][nt]);
         constexpr int VW = NC / 2;  // words of a lane and token
         const unsigned char* const vbase = stage + C::kCodeBytes + C::kMetaBytes +
-                                           16 * h * (D / 2) + g * NC * 2;
+                                           16 * (h0 + h) * (D / 2) + g * NC * 2;
         uint32_t x0[VW], x1[VW], x2[VW], x3[VW];
         load_words<VW>(vbase + tok_v0 * (D / 2), x0);
         load_words<VW>(vbase + tok_v1 * (D / 2), x1);
@@ -682,6 +695,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
             mma_f16_16816(O[2 * j + 1][nt], a1, b[j / kChunksPerGroup][nt]);
           }
         }
+      }
+        raise = false;
       }
       __syncwarp();  // the stage may be refilled
       if (++st == NS) {
@@ -787,11 +802,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
     for (int rl = 0; rl < rows; ++rl, ++task) {
       if (task % WARPS != warp) continue;
       const float* stats = reinterpret_cast<const float*>(piece) + ROWS * D + rl;
-      const float own_m = mine ? stats[0] : -INFINITY;
+      const float own_m = mine ? stats[0] : kNoReference;
       float top = own_m;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      const float weight = own_m == -INFINITY ? 0.f : exp2_approx(own_m - top);
+      const float weight = mine ? exp2_approx(own_m - top) : 0.f;
       float l = mine ? weight * stats[ROWS] : 0.f;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
@@ -841,7 +856,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
         // every CTA of the segment has brought its row
         if (lane == 0) p.arrived[c0 * kMaxRows + rl] = 0u;
         constexpr int kAtOnce = 8;
-        top = -INFINITY;
+        top = kNoReference;
         l = 0.f;
 #pragma unroll
         for (int k = 0; k < VF; ++k) o[k] = 0.f;
@@ -859,14 +874,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
           const int c = base + lane;
           const bool there = lane < kAtOnce && c <= c1;
           const float* from = slot(min(c, c1), c == c0) + ROWS * D + rl;
-          const float m_c = there ? __ldcg(from) : -INFINITY;
+          const float m_c = there ? __ldcg(from) : kNoReference;
           const float l_c = there ? __ldcg(from + ROWS) : 0.f;
           float next = fmaxf(top, m_c);
 #pragma unroll
           for (int d = 1; d < 32; d *= 2)
             next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, d));
-          const float keep = top == -INFINITY ? 0.f : exp2_approx(top - next);
-          const float w_c = m_c == -INFINITY ? 0.f : exp2_approx(m_c - next);
+          const float keep = exp2_approx(top - next);
+          const float w_c = there ? exp2_approx(m_c - next) : 0.f;
           float add = w_c * l_c;
 #pragma unroll
           for (int d = 1; d < kAtOnce; d *= 2) add += __shfl_xor_sync(0xffffffffu, add, d);
