@@ -498,37 +498,54 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
       // ---- scores (base 2) of TILES times 16 tokens
       float x[TILES][NT][4];  // tokens a, a, b, b; columns 2t, 2t + 1
       uint32_t vm[TILES][2][NG];
+      // the tiles' chains of products interleave; a single group's is cut in two
+      constexpr int ACC = NG == 1 ? 2 : NG;
+      float acc[TILES][NT][ACC][4];
+      uint32_t wa[TILES][NC], wb[TILES][NC], km[TILES][2][NG];
 #pragma unroll
       for (int h = 0; h < TILES; ++h) {
         const int ta = 16 * (h0 + h) + tok_a;
-        uint32_t wa[NC], wb[NC], km[2][NG];
-        load_words<NC>(stage + ta * (D / 2) + t * NC * 4, wa);
-        load_words<NC>(stage + (ta + 8) * (D / 2) + t * NC * 4, wb);
+        load_words<NC>(stage + ta * (D / 2) + t * NC * 4, wa[h]);
+        load_words<NC>(stage + (ta + 8) * (D / 2) + t * NC * 4, wb[h]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          load_words<NG>(stage + C::kCodeBytes + (ta + 8 * i) * NG * 4, km[i]);
+          load_words<NG>(stage + C::kCodeBytes + (ta + 8 * i) * NG * 4, km[h][i]);
           load_words<NG>(stage + 2 * C::kCodeBytes + C::kMetaBytes + (ta + 8 * i) * NG * 4,
                          vm[h][i]);
         }
-        float acc[NT][NG][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < NG; ++k)
+          for (int k = 0; k < ACC; ++k)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[nt][k][c] = 0.f;
+            for (int c = 0; c < 4; ++c) acc[h][nt][k][c] = 0.f;
+      }
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
+      for (int j = 0; j < NC; ++j) {
+        constexpr bool kCut = NG == 1;
+        const int k0 = kCut ? 0 : j / kChunksPerGroup, k1 = kCut ? 1 : k0;
+#pragma unroll
+        for (int h = 0; h < TILES; ++h) {
           uint32_t ua[4], ub[4];
-          unpack_u4_h<8>(wa[j], ua);
-          unpack_u4_h<8>(wb[j], ub);
+          unpack_u4_h<8>(wa[h][j], ua);
+          unpack_u4_h<8>(wb[h][j], ub);
           const uint32_t a0[4] = {ua[0], ub[0], ua[1], ub[1]};
           const uint32_t a1[4] = {ua[2], ub[2], ua[3], ub[3]};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma_f16_16816(acc[nt][j / kChunksPerGroup], a0, q[nt][2 * j]);
-            mma_f16_16816(acc[nt][j / kChunksPerGroup], a1, q[nt][2 * j + 1]);
+            mma_f16_16816(acc[h][nt][k0], a0, q[nt][2 * j]);
+            mma_f16_16816(acc[h][nt][k1], a1, q[nt][2 * j + 1]);
           }
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < TILES; ++h) {
+        const int ta = 16 * (h0 + h) + tok_a;
+        if (NG == 1) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[h][nt][0][c] += acc[h][nt][ACC - 1][c];
         }
         if (masked) {
           // what lies behind the sequence's end can be anything, NaN included
@@ -536,18 +553,18 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
           for (int i = 0; i < 2; ++i)
             if (tok0 + ta + 8 * i >= cs.len)
 #pragma unroll
-              for (int k = 0; k < NG; ++k) km[i][k] = vm[h][i][k] = 0u;
+              for (int k = 0; k < NG; ++k) km[h][i][k] = vm[h][i][k] = 0u;
         }
 #pragma unroll
         for (int k = 0; k < NG; ++k)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float2 f = meta_pair(km[i][k]);
+            const float2 f = meta_pair(km[h][i][k]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const float y = fmaf(8.f - f.y, sum_q[nt][k][c], acc[nt][k][2 * i + c]);
+                const float y = fmaf(8.f - f.y, sum_q[nt][k][c], acc[h][nt][k][2 * i + c]);
                 x[h][nt][2 * i + c] = k == 0 ? f.x * y : fmaf(f.x, y, x[h][nt][2 * i + c]);
               }
           }
