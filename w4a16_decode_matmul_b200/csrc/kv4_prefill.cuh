@@ -34,6 +34,8 @@
 // cycles, exponentials (16 a cycle) 2,048, issue slots about as many.
 #pragma once
 
+#include <type_traits>
+
 #include "gemm2.cuh"
 #include "kv4_attn.cuh"
 
@@ -455,77 +457,105 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
     }
     const int my_limit = have ? seq.len - seq.rows + p.a.by_gqa(r) + 1 : 0;
     const int least = __reduce_min_sync(0xffffffffu, my_limit);
-    float m = -INFINITY, l = 0.f;
+    float m = kNoReference, l = 0.f;
     bool ok = true;
+    // One step's weights, 32 tokens at a time, each chunk of scores loaded from
+    // tensor memory while the one before it is computed.  The packed weights
+    // go over scores that have been read.  A chunk with a weight above 2^14
+    // (never before the first chunk's) raises the row's reference and puts
+    // what the row has so far on it.
+    auto weights = [&](auto masked_tag, int j) {
+      constexpr bool kMasked = decltype(masked_tag)::value;
+      const bool wide = *reinterpret_cast<volatile int*>(&ctl->wide[j & 3]) != 0;
+      const float cj = wide ? 2.f * c : c;     // halved keys
+      const float shift = wide ? 1.f : 0.f;    // halved values take doubled weights
+      const uint32_t most_allowed = wide ? 0x7800u : 0x7400u;  // 2^15, 2^14
+      const int seen = my_limit - j * kTile;   // columns below `seen` count
+      float v[2][32];
+      float2 sum = make_float2(0.f, 0.f);
+      tmem_ld32(s_tmem, v[0]);
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) {
+        float(&x)[32] = v[ch & 1];
+        tmem_wait_ld();
+        if (ch < 3) tmem_ld32(s_tmem + 32 * (ch + 1), v[(ch + 1) & 1]);
+        uint32_t w[16];
+        float2 part;
+        auto form = [&] {
+          const float ref = shift - m;
+          part = make_float2(0.f, 0.f);
+          uint32_t most = 0u;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float2 e = fma2(make_float2(x[2 * k], x[2 * k + 1]), make_float2(cj, cj),
+                            make_float2(ref, ref));
+            e.x = exp2_approx(e.x);
+            e.y = exp2_approx(e.y);
+            if (kMasked) {
+              if (32 * ch + 2 * k >= seen) e.x = 0.f;
+              if (32 * ch + 2 * k + 1 >= seen) e.y = 0.f;
+            }
+            part = add2(part, e);
+            w[k] = pack_half2(e.x, e.y);
+            most = __vmaxu2(most, w[k]);
+          }
+          const uint32_t hi = most >> 16, lo = most & 0xffffu;
+          return (hi > most_allowed && hi <= 0x7c00u) || (lo > most_allowed && lo <= 0x7c00u);
+        };
+        const bool over = form();
+        if (__any_sync(0xffffffffu, over)) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (!kMasked || 32 * ch + k < seen) top = fmaxf(top, x[k]);
+          const float next = over ? top * cj - 7.f : m;
+          const float f = exp2_approx(m - next);
+          m = next;
+          l *= f;
+          sum.x *= f;
+          sum.y *= f;
+          if (j > 0) {
+            ok = __all_sync(0xffffffffu, wait(&ctl->o_done[i], uint32_t(j - 1) & 1u));
+            if (!ok) return;
+            tc_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < D / 16; ++k) {
+              float o[16];
+              gemm2::tmem_ld16(o_tmem + 16 * k, o);
+              tmem_wait_ld();
+              uint32_t r[16];
+#pragma unroll
+              for (int n = 0; n < 16; ++n) r[n] = __float_as_uint(o[n] * f);
+              tmem_st16(o_tmem + 16 * k, r);
+            }
+          }
+          const uint32_t f2 = pack_half2(f, f);
+#pragma unroll 1
+          for (int k = 0; k < ch; ++k) {
+            float o[16];
+            uint32_t r[16];
+            gemm2::tmem_ld16(s_tmem + 16 * k, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int n = 0; n < 16; ++n) r[n] = hmul2(__float_as_uint(o[n]), f2);
+            tmem_st16(s_tmem + 16 * k, r);
+          }
+          form();
+        }
+        sum = add2(sum, part);
+        tmem_st16(s_tmem + 16 * ch, w);
+      }
+      l += wide ? 0.5f * (sum.x + sum.y) : sum.x + sum.y;
+    };
     for (int j = 0; j < steps; ++j) {
       ok = __all_sync(0xffffffffu, wait(&ctl->s_full[i], uint32_t(j) & 1u));
       if (!ok) break;
       tc_fence_after();
-      const bool wide = *reinterpret_cast<volatile int*>(&ctl->wide[j & 3]) != 0;
-      const float cj = wide ? 2.f * c : c;
-      const int first = j * kTile, seen = my_limit - first;  // columns below `seen` count
-      const bool masked = first + kTile > least;
-      float v[32];
-      float top = -INFINITY;
-#pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        tmem_ld32(s_tmem + 32 * ch, v);
-        tmem_wait_ld();
-        if (masked) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (32 * ch + k >= seen) v[k] = -INFINITY;
-        }
-#pragma unroll
-        for (int k = 0; k < 32; ++k) top = fmaxf(top, v[k]);
-      }
-      // the reference rises only when a weight would pass 2^14
-      const float highest = top == -INFINITY ? -INFINITY : top * cj;
-      const bool raise = highest > m + 14.f;
-      if (__any_sync(0xffffffffu, raise)) {
-        const float next = raise ? highest - 7.f : m;
-        const float f = raise ? exp2_approx(m - next) : 1.f;
-        m = next;
-        l *= f;
-        if (j > 0) {
-          ok = __all_sync(0xffffffffu, wait(&ctl->o_done[i], uint32_t(j - 1) & 1u));
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int ch = 0; ch < D / 32; ++ch) {
-            tmem_ld32(o_tmem + 32 * ch, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] *= f;
-            gemm::tmem_st32(o_tmem + 32 * ch, v);
-          }
-          tmem_wait_st();
-        }
-      }
-      // a halved tile of values takes doubled weights
-      const float ref = (m == -INFINITY ? 0.f : m) - (wide ? 1.f : 0.f);
-      float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        tmem_ld32(s_tmem + 32 * ch, v);
-        tmem_wait_ld();
-        uint32_t w[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          float2 e = fma2(make_float2(v[2 * k], v[2 * k + 1]), make_float2(cj, cj),
-                          make_float2(-ref, -ref));
-          e.x = exp2_approx(e.x);
-          e.y = exp2_approx(e.y);
-          if (masked) {
-            if (32 * ch + 2 * k >= seen) e.x = 0.f;
-            if (32 * ch + 2 * k + 1 >= seen) e.y = 0.f;
-          }
-          sum = add2(sum, e);
-          w[k] = pack_half2(e.x, e.y);
-        }
-        tmem_st16(s_tmem + 16 * ch, w);
-      }
-      l += wide ? 0.5f * (sum.x + sum.y) : sum.x + sum.y;
+      if ((j + 1) * kTile > least)
+        weights(std::true_type{}, j);
+      else
+        weights(std::false_type{}, j);
+      if (!ok) break;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
