@@ -30,6 +30,10 @@ LOG = os.path.join(HERE, "ptxas.log")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMPILE_FLAGS = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-rdc=true",
                  "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
+# Units compiled as a whole program (no relocatable device code): register
+# reallocation between warpgroups is ignored in relocatable code.  They keep a
+# device status word of their own.
+WHOLE_PROGRAM = {"k_kv4_prefill.cu"}
 LINK_FLAGS = [*ARCH, "-rdc=true", "-shared", "-Xcompiler", "-fPIC"]
 
 _INCLUDE_RE = re.compile(r'^\s*#\s*include\s+"([^"]+)"', re.M)
@@ -90,7 +94,10 @@ def up_to_date() -> bool:
 def _compile(unit: str) -> tuple[str, int, str]:
     obj = _obj(unit)
     tmp = obj + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *COMPILE_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", unit, "-o", tmp]
+    flags = COMPILE_FLAGS
+    if os.path.basename(unit) in WHOLE_PROGRAM:
+        flags = [f for f in flags if f != "-rdc=true"]
+    cmd = [_nvcc(), *flags, "-I", INCLUDE, "-I", CSRC, "-c", unit, "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode == 0:
         os.replace(tmp, obj)

@@ -166,7 +166,8 @@ cudaError_t run_kv4_attention(const void* Q, int64_t q_stride, int q_heads,
   const int64_t bound = max_rows > 0 ? max_rows : batch.rows;
   p.max_columns = 1 << 30;
   if (bound * p.gqa > kFew) {
-    kv4::PrefillParams pp = {p, kFew + 1};
+    kv4::PrefillParams pp = {p, kFew + 1, status_address()};
+    if (pp.status == nullptr) return cudaErrorInitializationError;
     const cudaError_t e = run_kv4_prefill(cache.head_dim, cache.group, pp, s);
     if (e != cudaSuccess || !batch.row_starts) return e;
     p.max_columns = kFew;

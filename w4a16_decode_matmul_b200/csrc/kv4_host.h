@@ -17,4 +17,8 @@ cudaError_t run_kv4_attention(const void* Q, int64_t q_stride, int q_heads,
                               const DeviceInfo& dev);
 size_t kv4_workspace_bytes();
 
+// Address of the device status word on the current device (looked up once per
+// device); null on failure.
+unsigned int* status_address();
+
 }  // namespace wqh

@@ -54,12 +54,13 @@ using gemm2::tmem_st16;
 
 constexpr int kTile = 128;       // rows of a tile, tokens of a step
 constexpr int kBlockRows = 256;  // rows of a CTA
-constexpr int kPrefillThreads = 13 * 32;
+constexpr int kPrefillThreads = 16 * 32;  // four warpgroups; the last has one busy warp
 constexpr int kWideScale = 4366;  // 15 * 4366 is the last multiple below 65504
 
 struct PrefillParams {
   AttnParams a;
   int min_columns;  // sequences with fewer rows times heads are left alone
+  unsigned* status;  // the library's device status word
 };
 
 template <int D>
@@ -184,7 +185,15 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
   Block block;
   const int heads = p.a.cache.kv_heads;
   const int head = (int(gridDim.x) - 1 - int(blockIdx.x)) % heads;
-  if (!find_block(p, (int(gridDim.x) - 1 - int(blockIdx.x)) / heads, lane, &block)) return;
+  // what this unit's status word holds goes to the library's
+  auto report = [&] {
+    if (tid == 0 && *reinterpret_cast<volatile unsigned*>(&g_status) != 0u)
+      atomicCAS(p.status, 0u, atomicExch(&g_status, 0u));
+  };
+  if (!find_block(p, (int(gridDim.x) - 1 - int(blockIdx.x)) / heads, lane, &block)) {
+    report();
+    return;
+  }
   const Sequence& seq = block.s;
   const int rows = min(kBlockRows, block.columns - block.row);
   const int tiles = rows > kTile ? 2 : 1;
@@ -235,9 +244,12 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
     return true;
   };
 
-  if (warp == 12) {
+  // Registers: 512 threads at 128; the softmax holds a step's scores and
+  // weights.  2 * 128 * 184 + 128 * 104 + 128 * 40 = 65,536 = 512 * 128.
+  if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     // ---- matrix products
-    if (lane == 0) {
+    if (warp == 12 && lane == 0) {
       constexpr uint32_t kDescQK = instr_desc_f16(kTile, false);
       constexpr uint32_t kDescPV = instr_desc_f16(D, true);
       const uint32_t sq = smem_addr(smem + C::kOffQ), sk = smem_addr(smem + C::kOffK),
@@ -288,6 +300,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
     }
     __syncwarp();
   } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     // ---- keys and values.  Thread (token, t): words t of every chunk of the
     // rows of four tokens of each tile; neighbouring lanes take tokens 4 apart,
     // so that 8 lanes write 8 different bank groups.
@@ -410,8 +423,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
         if (j + 2 < steps) read_pages(j + 2);
       }
     }
-  } else if ((warp >> 2) < tiles) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // ---- softmax: this thread's row
+    if ((warp >> 2) < tiles) {
     const int i = warp >> 2, local = (warp & 3) * 32 + lane;
     const int r = block.row + i * kTile + local;
     const bool have = i * kTile + local < rows;
@@ -459,11 +474,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
     const int least = __reduce_min_sync(0xffffffffu, my_limit);
     float m = kNoReference, l = 0.f;
     bool ok = true;
-    // One step's weights, 32 tokens at a time, each chunk of scores loaded from
-    // tensor memory while the one before it is computed.  The packed weights
-    // go over scores that have been read.  A chunk with a weight above 2^14
-    // (never before the first chunk's) raises the row's reference and puts
-    // what the row has so far on it.
+    // One step's weights, formed with the row's present reference.  Where one
+    // passes 2^14 (always in the first step) the reference is raised, the output
+    // so far put on it, and the step's weights are formed again; they go over
+    // the scores in tensor memory only then.
     auto weights = [&](auto masked_tag, int j) {
       constexpr bool kMasked = decltype(masked_tag)::value;
       const bool wide = *reinterpret_cast<volatile int*>(&ctl->wide[j & 3]) != 0;
@@ -471,20 +485,19 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
       const float shift = wide ? 1.f : 0.f;    // halved values take doubled weights
       const uint32_t most_allowed = wide ? 0x7800u : 0x7400u;  // 2^15, 2^14
       const int seen = my_limit - j * kTile;   // columns below `seen` count
-      float v[2][32];
-      float2 sum = make_float2(0.f, 0.f);
-      tmem_ld32(s_tmem, v[0]);
+      uint32_t w[4][16];
+      float2 sum;
+      while (true) {
+        float v[2][32];  // each chunk is loaded while the one before it is computed
+        tmem_ld32(s_tmem, v[0]);
+        const float ref = shift - m;
+        uint32_t most = 0u;
+        sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        float(&x)[32] = v[ch & 1];
-        tmem_wait_ld();
-        if (ch < 3) tmem_ld32(s_tmem + 32 * (ch + 1), v[(ch + 1) & 1]);
-        uint32_t w[16];
-        float2 part;
-        auto form = [&] {
-          const float ref = shift - m;
-          part = make_float2(0.f, 0.f);
-          uint32_t most = 0u;
+        for (int ch = 0; ch < 4; ++ch) {
+          float(&x)[32] = v[ch & 1];
+          tmem_wait_ld();
+          if (ch < 3) tmem_ld32(s_tmem + 32 * (ch + 1), v[(ch + 1) & 1]);
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             float2 e = fma2(make_float2(x[2 * k], x[2 * k + 1]), make_float2(cj, cj),
@@ -495,56 +508,48 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
               if (32 * ch + 2 * k >= seen) e.x = 0.f;
               if (32 * ch + 2 * k + 1 >= seen) e.y = 0.f;
             }
-            part = add2(part, e);
-            w[k] = pack_half2(e.x, e.y);
-            most = __vmaxu2(most, w[k]);
+            sum = add2(sum, e);
+            w[ch][k] = pack_half2(e.x, e.y);
+            most = __vmaxu2(most, w[ch][k]);
           }
-          const uint32_t hi = most >> 16, lo = most & 0xffffu;
-          return (hi > most_allowed && hi <= 0x7c00u) || (lo > most_allowed && lo <= 0x7c00u);
-        };
-        const bool over = form();
-        if (__any_sync(0xffffffffu, over)) {
-          float top = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (!kMasked || 32 * ch + k < seen) top = fmaxf(top, x[k]);
-          const float next = over ? top * cj - 7.f : m;
-          const float f = exp2_approx(m - next);
-          m = next;
-          l *= f;
-          sum.x *= f;
-          sum.y *= f;
-          if (j > 0) {
-            ok = __all_sync(0xffffffffu, wait(&ctl->o_done[i], uint32_t(j - 1) & 1u));
-            if (!ok) return;
-            tc_fence_after();
-#pragma unroll 1
-            for (int k = 0; k < D / 16; ++k) {
-              float o[16];
-              gemm2::tmem_ld16(o_tmem + 16 * k, o);
-              tmem_wait_ld();
-              uint32_t r[16];
-#pragma unroll
-              for (int n = 0; n < 16; ++n) r[n] = __float_as_uint(o[n] * f);
-              tmem_st16(o_tmem + 16 * k, r);
-            }
-          }
-          const uint32_t f2 = pack_half2(f, f);
-#pragma unroll 1
-          for (int k = 0; k < ch; ++k) {
-            float o[16];
-            uint32_t r[16];
-            gemm2::tmem_ld16(s_tmem + 16 * k, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int n = 0; n < 16; ++n) r[n] = hmul2(__float_as_uint(o[n]), f2);
-            tmem_st16(s_tmem + 16 * k, r);
-          }
-          form();
         }
-        sum = add2(sum, part);
-        tmem_st16(s_tmem + 16 * ch, w);
+        // (a NaN, above infinity's 0x7c00, raises nothing)
+        const uint32_t hi = most >> 16, lo = most & 0xffffu;
+        const bool over = (hi > most_allowed && hi <= 0x7c00u) ||
+                          (lo > most_allowed && lo <= 0x7c00u);
+        if (!__any_sync(0xffffffffu, over)) break;
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int k = 0; k < kTile; k += 16) {
+          float x[16];
+          gemm2::tmem_ld16(s_tmem + k, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int n = 0; n < 16; ++n)
+            if (!kMasked || k + n < seen) top = fmaxf(top, x[n]);
+        }
+        const float next = over ? top * cj - 7.f : m;
+        const float f = exp2_approx(m - next);
+        m = next;
+        l *= f;
+        if (j > 0) {
+          ok = __all_sync(0xffffffffu, wait(&ctl->o_done[i], uint32_t(j - 1) & 1u));
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll 1
+          for (int k = 0; k < D / 16; ++k) {
+            float o[16];
+            gemm2::tmem_ld16(o_tmem + 16 * k, o);
+            tmem_wait_ld();
+            uint32_t r[16];
+#pragma unroll
+            for (int n = 0; n < 16; ++n) r[n] = __float_as_uint(o[n] * f);
+            tmem_st16(o_tmem + 16 * k, r);
+          }
+        }
       }
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) tmem_st16(s_tmem + 16 * ch, w[ch]);
       l += wide ? 0.5f * (sum.x + sum.y) : sum.x + sum.y;
     };
     for (int j = 0; j < steps; ++j) {
@@ -587,6 +592,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
         }
       }
     }
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -594,6 +600,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
   }
+  report();
 }
 
 }  // namespace kv4

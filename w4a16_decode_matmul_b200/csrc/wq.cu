@@ -60,6 +60,19 @@ bool device_info(DeviceInfo* out) {
   return true;
 }
 
+unsigned int* status_address() {
+  static unsigned int* found[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  if (found[dev] == nullptr) {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, wq::g_status) != cudaSuccess) return nullptr;
+    found[dev] = static_cast<unsigned int*>(p);
+  }
+  return found[dev];
+}
+
 bool encode_2d_ex(CUtensorMap* map, const void* base, CUtensorMapDataType type, int elem_bytes,
                   uint64_t cols, uint64_t rows, uint32_t box_cols, uint32_t box_rows,
                   CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion) {
