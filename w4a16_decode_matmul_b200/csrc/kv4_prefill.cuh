@@ -55,6 +55,7 @@ using gemm2::tmem_st16;
 constexpr int kTile = 128;       // rows of a tile, tokens of a step
 constexpr int kBlockRows = 256;  // rows of a CTA
 constexpr int kPrefillThreads = 16 * 32;  // four warpgroups; the last has one busy warp
+constexpr int kMmaWarp = 12;
 constexpr int kWideScale = 4366;  // 15 * 4366 is the last multiple below 65504
 
 struct PrefillParams {
@@ -122,6 +123,17 @@ __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+
+// One thread of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 // Whether the predicate holds for any of the `threads` threads of a barrier.
@@ -221,7 +233,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(&ctl->tmem)),
                  "r"(512u)
@@ -248,28 +260,35 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
   // weights.  2 * 128 * 184 + 128 * 104 + 128 * 40 = 65,536 = 512 * 128.
   if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    // ---- matrix products
-    if (warp == 12 && lane == 0) {
+    // ---- matrix products.  The whole warp runs the loop, so that descriptors
+    // stay in uniform registers; one elected thread issues.
+    if (warp == kMmaWarp) {
       constexpr uint32_t kDescQK = instr_desc_f16(kTile, false);
       constexpr uint32_t kDescPV = instr_desc_f16(D, true);
-      const uint32_t sq = smem_addr(smem + C::kOffQ), sk = smem_addr(smem + C::kOffK),
-                     sv = smem_addr(smem + C::kOffV);
+      const uint64_t q_desc = swizzled_desc(smem_addr(smem + C::kOffQ), 16),
+                     k_desc = swizzled_desc(smem_addr(smem + C::kOffK), 16),
+                     v_desc = swizzled_desc(smem_addr(smem + C::kOffV), C::kBlockBytes);
+      const bool leader = elect_one();
       bool ok = true;
       for (int i = 0; i < tiles && ok; ++i) ok = wait(&ctl->q_full[i], 0);
       auto scores = [&](int i, int stage) {
+        const uint64_t a = q_desc + uint32_t(i * (C::kTileBytes >> 4)),
+                       b = k_desc + uint32_t(stage * (C::kTileBytes >> 4));
         tc_fence_after();
+        if (leader) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * C::kBlockBytes + (ks & 3) * 32;
-          tc_mma_ss(tmem + i * kTile, swizzled_desc(sq + i * C::kTileBytes + off, 16),
-                    swizzled_desc(sk + stage * C::kTileBytes + off, 16), kDescQK, ks > 0);
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * C::kBlockBytes + (ks & 3) * 32) >> 4;
+            tc_mma_ss(tmem + i * kTile, a + off, b + off, kDescQK, ks > 0);
+          }
+          tc_commit(&ctl->s_full[i]);
         }
-        tc_commit(&ctl->s_full[i]);
+        __syncwarp();
       };
       // S_i of step j + 1 follows O_i of step j: it writes over P_i
       if (ok && steps > 0 && (ok = wait(&ctl->k_full[0], 0))) {
         for (int i = 0; i < tiles; ++i) scores(i, 0);
-        tc_commit(&ctl->k_free[0]);
+        if (leader) tc_commit(&ctl->k_free[0]);
       }
       for (int j = 0; j < steps && ok; ++j) {
         const int stage = j & 1, next = stage ^ 1;
@@ -278,27 +297,30 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
           ok = wait(&ctl->p_full[i], uint32_t(j) & 1u) &&
                (i > 0 || wait(&ctl->v_full[stage], uint32_t(j >> 1) & 1u));
           if (!ok) break;
+          const uint64_t b = v_desc + uint32_t(stage * (C::kTileBytes >> 4));
           tc_fence_after();
+          if (leader) {
 #pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-            tc_mma_ts(tmem + 2 * kTile + i * kTile, tmem + i * kTile + ks * 8,
-                      swizzled_desc(sv + stage * C::kTileBytes + ks * 2048, C::kBlockBytes),
-                      kDescPV, j > 0 || ks > 0);
-          tc_commit(&ctl->o_done[i]);
-          if (i == tiles - 1) tc_commit(&ctl->v_free[stage]);
+            for (int ks = 0; ks < kTile / 16; ++ks)
+              tc_mma_ts(tmem + 2 * kTile + i * kTile, tmem + i * kTile + ks * 8, b + ks * 128,
+                        kDescPV, j > 0 || ks > 0);
+            tc_commit(&ctl->o_done[i]);
+            if (i == tiles - 1) tc_commit(&ctl->v_free[stage]);
+          }
+          __syncwarp();
           if (more) {
             if (i == 0) ok = wait(&ctl->k_full[next], uint32_t((j + 1) >> 1) & 1u);
             if (!ok) break;
             scores(i, next);
-            if (i == tiles - 1) tc_commit(&ctl->k_free[next]);
+            if (i == tiles - 1 && leader) tc_commit(&ctl->k_free[next]);
           }
         }
       }
       // all of this CTA's products are done before tensor memory is freed
-      tc_commit(&ctl->mma_done);
+      if (leader) tc_commit(&ctl->mma_done);
+      __syncwarp();
       mbar_wait(&ctl->mma_done, 0);
     }
-    __syncwarp();
   } else if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     // ---- keys and values.  Thread (token, t): words t of every chunk of the
@@ -596,7 +618,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
   }
