@@ -72,9 +72,10 @@ def reference(q, cache, lens, rows, table, scale):
         k = ref.sequence_values(kc, km, table[b], n, cache.page_size, "k")
         v = ref.sequence_values(vc, vm, table[b], n, cache.page_size, "v")
         x = q[at:at + t].float().cpu().numpy().astype(np.float64)
-        # more than 16 rows times heads of a group go to the tensor-memory kernel
-        few = t * (x.shape[1] // cache.kv_heads) <= 16
-        o, e = ref.attention(x, k, v, n, scale, few)
+        # more than 16 rows times heads of a group: either kernel may be chosen
+        o, e = ref.attention(x, k, v, n, scale, True)
+        if t * (x.shape[1] // cache.kv_heads) > 16:
+            e = np.maximum(e, ref.attention(x, k, v, n, scale, False)[1])
         out.append(o)
         bound.append(e)
         at += t
@@ -241,6 +242,66 @@ def test_many_rows(d, group, gqa, rows, lens):
     run_attention(d, group, 16, 2, gqa, lens, rows, seed=sum(rows) + gqa)
 
 
+@pytest.mark.parametrize("d,group,heads,gqa,lens,rows", [
+    (128, 64, 1, 4, [5000], [40]),                 # one block over many CTAs
+    (64, 32, 2, 8, [1200, 129, 70], [20, 30, 70]), # blocks with one step, two and more
+    (128, 128, 1, 1, [3000], [300]),               # the last rows see most
+    (128, 32, 1, 32, [2000], [1])])
+def test_many_rows_split_over_ctas(d, group, heads, gqa, lens, rows):
+    run_attention(d, group, 64, heads, gqa, lens, rows, seed=len(lens) + gqa)
+
+
+def test_many_rows_repeated_and_captured_calls():
+    """The last split to arrive adds the parts: same bits every time, in a
+    graph and over other lengths too."""
+    lens, rows = [2600], [50]
+    got, cache, table, q = run_attention(128, 64, 64, 1, 4, lens, rows, seed=21)
+    ws, n, tb = wq().kv4_workspace(), ints(lens), ints(table)
+    out = torch.zeros_like(q)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        for _ in range(3):
+            wq().kv4_attention(q, cache, n, tb, out=out, workspace=ws)
+        stream.synchronize()
+        assert torch.equal(out, got)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            wq().kv4_attention(q, cache, n, tb, out=out, workspace=ws)
+    for length in (2600, 2600, 700, 30, 2600):
+        n.copy_(ints([length]))
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        o, e = reference(q, cache, [length], rows, table, 128 ** -0.5)
+        ref.check(out, o, e)
+    assert torch.equal(out, got) and not ws[:COUNTERS].any()
+
+
+def test_many_rows_bad_device_arrays():
+    d, group, heads, page = 64, 32, 2, 16
+    lens, rows = [300, 200], [40, 30]
+    table, pages = ref.random_batch(3, lens, page)
+    cache = new_cache(pages, heads, d, page, group)
+    fill(cache, lens, table)
+    before = images(cache)
+    q = ref.keys(1, 70, heads, d).cuda()
+    args = (q, cache, ints(lens), ints(table), ints(starts_of(rows)))
+    good = wq().kv4_attention(*args, max_rows=40)
+    assert wq().get_device_error() == 0
+    bad = table.copy()
+    bad[1, 0], bad[1, 5] = pages, -1
+    out = wq().kv4_attention(q, cache, ints(lens), ints(bad), ints(starts_of(rows)), max_rows=40)
+    assert wq().get_device_error() == 1
+    assert torch.equal(out[:40], good[:40])
+    wq().kv4_attention(q, cache, ints([300, 10 ** 6]), ints(table), ints(starts_of(rows)))
+    assert wq().get_device_error() == 1
+    wq().kv4_attention(q, cache, ints(lens), ints(table), ints([0, 40, 90]))
+    assert wq().get_device_error() == 1
+    assert torch.equal(wq().kv4_attention(*args, max_rows=40), good)
+    assert wq().get_device_error() == 0
+    assert_cache(cache, before)
+
+
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
 def test_many_rows_page_sizes(page):
     run_attention(128, 64, page, 1, 4, [page + 200, 600], [60, 100], seed=page)
@@ -294,6 +355,19 @@ def test_many_rows_value_ranges(what, strength):
 ])
 def test_split_over_ctas(d, group, heads, gqa, lens):
     run_attention(d, group, 64, heads, gqa, lens, [1] * len(lens), seed=len(lens))
+
+
+@pytest.mark.parametrize("rows", [1, 17, 40])
+def test_tokens_that_are_not_copied(rows):
+    """Several blocks of rows over a few tokens, after a call that left NaN
+    metadata in every SM's shared memory."""
+    d, group, heads, page, n = 128, 32, 2, 16, max(rows, 17)
+    noise = new_cache(4, heads, d, page, group)
+    ones = ints([64] * 200)
+    q = ref.keys(1, 200, heads, d).cuda()
+    wq().kv4_attention(q, noise, ones, ints(np.tile(np.arange(4), (200, 1))))
+    assert wq().get_device_error() == 0
+    run_attention(d, group, page, heads, 1, [n], [rows], seed=rows)
 
 
 def test_more_sequences_than_threads():

@@ -21,7 +21,8 @@ cudaError_t launch(const kv4::PrefillParams& p, cudaStream_t s) {
   const cudaError_t e = configure_smem(kernel, configured, C::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t blocks =
-      (int64_t(p.a.batch.rows) * p.a.gqa / kv4::kBlockRows + p.a.batch.seqs) * p.a.cache.kv_heads;
+      (int64_t(p.a.batch.rows) * p.a.gqa / kv4::kBlockRows + p.a.batch.seqs) *
+      p.a.cache.kv_heads * p.splits;
   if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
   kernel<<<unsigned(blocks), kv4::kPrefillThreads, C::kSmem, s>>>(p);
   return cudaGetLastError();

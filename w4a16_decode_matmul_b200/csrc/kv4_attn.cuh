@@ -548,10 +548,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
             for (int c = 0; c < 4; ++c) acc[h][nt][0][c] += acc[h][nt][ACC - 1][c];
         }
         if (masked) {
-          // what lies behind the sequence's end can be anything, NaN included
+          // tokens that no row of the block sees may not have been copied, and what
+          // lies behind the end of a sequence can be anything, NaN included
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            if (tok0 + ta + 8 * i >= cs.len)
+            if (tok0 + ta + 8 * i >= cs.limit)
 #pragma unroll
               for (int k = 0; k < NG; ++k) km[h][i][k] = vm[h][i][k] = 0u;
         }

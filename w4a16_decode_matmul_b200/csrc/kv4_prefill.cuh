@@ -30,6 +30,11 @@
 // pass 2^14, then so that it becomes 2^7 (and the row's output is rescaled).
 // Products, sums and statistics in binary32.
 //
+// Work split.  Where the blocks of 256 rows do not fill half of the SMs, each
+// block's tokens are divided among `splits` CTAs.  A softmax warp then leaves
+// its rows' sums in the workspace, and the warp that is the last of all splits'
+// to bring its 32 rows adds them in split order (no CTA waits for another).
+//
 // What bounds it.  Per 256 rows x 128 tokens (D = 128): tensor cores 2,048
 // cycles, exponentials (16 a cycle) 2,048, issue slots about as many.
 #pragma once
@@ -62,6 +67,8 @@ struct PrefillParams {
   AttnParams a;
   int min_columns;  // sequences with fewer rows times heads are left alone
   unsigned* status;  // the library's device status word
+  int splits;        // CTAs that share the tokens of a block (see below)
+  float* partial;    // with splits > 1: one slot for each CTA of the grid
 };
 
 template <int D>
@@ -196,13 +203,15 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
   // the later rows of a sequence see more tokens: they come first
   Block block;
   const int heads = p.a.cache.kv_heads;
-  const int head = (int(gridDim.x) - 1 - int(blockIdx.x)) % heads;
+  const int cta = int(gridDim.x) - 1 - int(blockIdx.x);
+  const int split = cta % p.splits, group = cta / p.splits;
+  const int head = group % heads;
   // what this unit's status word holds goes to the library's
   auto report = [&] {
     if (tid == 0 && *reinterpret_cast<volatile unsigned*>(&g_status) != 0u)
       atomicCAS(p.status, 0u, atomicExch(&g_status, 0u));
   };
-  if (!find_block(p, (int(gridDim.x) - 1 - int(blockIdx.x)) / heads, lane, &block)) {
+  if (!find_block(p, group / heads, lane, &block)) {
     report();
     return;
   }
@@ -211,7 +220,16 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
   const int tiles = rows > kTile ? 2 : 1;
   // tokens the block's last row sees
   const int limit = seq.len - seq.rows + p.a.by_gqa(block.row + rows - 1) + 1;
-  const int steps = (max(limit, 0) + kTile - 1) / kTile;
+  const int all_steps = (max(limit, 0) + kTile - 1) / kTile;
+  const int splits = max(1, min(p.splits, all_steps));
+  if (split >= splits) {
+    report();
+    return;
+  }
+  // this CTA's steps, and its first token
+  const int step0 = int(int64_t(split) * all_steps / splits);
+  const int steps = int(int64_t(split + 1) * all_steps / splits) - step0;
+  const int token0 = step0 * kTile;
 
   unsigned char* const smem =
       raw_smem + ((1024u - (smem_addr(raw_smem) & 1023u)) & 1023u);  // swizzle atoms
@@ -257,9 +275,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
   };
 
   // Registers: 512 threads at 128; the softmax holds a step's scores and
-  // weights.  2 * 128 * 184 + 128 * 104 + 128 * 40 = 65,536 = 512 * 128.
+  // weights.  2 * 128 * 176 + 128 * 104 + 128 * 56 = 65,536 = 512 * 128.
   if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     // ---- matrix products.  The whole warp runs the loop, so that descriptors
     // stay in uniform registers; one elected thread issues.
     if (warp == kMmaWarp) {
@@ -337,14 +355,14 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
     auto read_pages = [&](int j) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int pos = j * kTile + 32 * u + tok;
+        const int pos = token0 + j * kTile + 32 * u + tok;
         page[u] = pos < limit ? table[pos >> cache.page_shift] : -1;
       }
     };
     auto read_keys = [&](int j) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int pos = j * kTile + 32 * u + tok;
+        const int pos = token0 + j * kTile + 32 * u + tok;
         at[u] = -1;
 #pragma unroll
         for (int k = 0; k < NC; ++k) kc[u][k] = 0u;
@@ -446,7 +464,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     // ---- softmax: this thread's row
     if ((warp >> 2) < tiles) {
     const int i = warp >> 2, local = (warp & 3) * 32 + lane;
@@ -506,7 +524,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
       const float cj = wide ? 2.f * c : c;     // halved keys
       const float shift = wide ? 1.f : 0.f;    // halved values take doubled weights
       const uint32_t most_allowed = wide ? 0x7800u : 0x7400u;  // 2^15, 2^14
-      const int seen = my_limit - j * kTile;   // columns below `seen` count
+      const int seen = my_limit - token0 - j * kTile;  // columns below `seen` count
       uint32_t w[4][16];
       float2 sum;
       while (true) {
@@ -578,7 +596,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
       ok = __all_sync(0xffffffffu, wait(&ctl->s_full[i], uint32_t(j) & 1u));
       if (!ok) break;
       tc_fence_after();
-      if ((j + 1) * kTile > least)
+      if (token0 + (j + 1) * kTile > least)
         weights(std::true_type{}, j);
       else
         weights(std::false_type{}, j);
@@ -592,25 +610,92 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
       ok = __all_sync(0xffffffffu, wait(&ctl->o_done[i], uint32_t(steps - 1) & 1u));
     if (ok) {
       tc_fence_after();
-      const float inv = l == 0.f ? 0.f : 1.f / l;
       __nv_bfloat16* row = p.a.O + row_offset(p.a, seq.row0, r, head, p.a.o_stride, D);
-#pragma unroll
-      for (int ch = 0; ch < D / 32; ++ch) {
-        float v[32];
-        if (steps > 0) {
-          tmem_ld32(o_tmem + 32 * ch, v);
-          tmem_wait_ld();
-        }
+      // 32 dims of the row, in the tile's order 0, 4, 1, 5, 2, 6, 3, 7
+      auto store = [&](int ch, const float (&v)[32], float inv) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float x[8];  // dims in order: the tile holds 0, 4, 1, 5, 2, 6, 3, 7
+          float x[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            x[(k >> 1) + 4 * (k & 1)] = l == 0.f ? 0.f : v[8 * e + k] * inv;
+            x[(k >> 1) + 4 * (k & 1)] = inv == 0.f ? 0.f : v[8 * e + k] * inv;
           if (have)
             *reinterpret_cast<uint4*>(row + 32 * ch + 8 * e) =
                 make_uint4(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]),
                            pack_bf162(x[4], x[5]), pack_bf162(x[6], x[7]));
+        }
+      };
+      if (splits == 1) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int ch = 0; ch < D / 32; ++ch) {
+          float v[32];
+          if (steps > 0) {
+            tmem_ld32(o_tmem + 32 * ch, v);
+            tmem_wait_ld();
+          }
+          store(ch, v, inv);
+        }
+      } else {
+        // a slot: [D / 4][256 rows] of four sums, then m [256], l [256]
+        constexpr int kSlot = kBlockRows * (D + 2);
+        const int my_row = i * kTile + local;
+        auto sums = [&](int c) {
+          return reinterpret_cast<float4*>(p.partial + int64_t(group * p.splits + c) * kSlot) +
+                 my_row;
+        };
+        auto stats = [&](int c) {
+          return p.partial + int64_t(group * p.splits + c) * kSlot + kBlockRows * D + my_row;
+        };
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          float v[32];
+          tmem_ld32(o_tmem + 32 * ch, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            __stcg(sums(split) + (8 * ch + k) * kBlockRows,
+                   make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+        }
+        __stcg(stats(split), m);
+        __stcg(stats(split) + kBlockRows, l);
+        __syncwarp();
+        unsigned* const arrived = p.a.arrived + group * kMaxRows + warp;
+        unsigned before = 0u;
+        if (lane == 0) {
+          __threadfence();
+          before = atomicAdd(arrived, 1u);
+          __threadfence();
+        }
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before == unsigned(splits - 1)) {
+          if (lane == 0) *arrived = 0u;
+          float top = kNoReference;
+          for (int c = 0; c < splits; ++c) top = fmaxf(top, __ldcg(stats(c)));
+          float all = 0.f;
+#pragma unroll 4
+          for (int c = 0; c < splits; ++c)
+            all = fmaf(exp2_approx(__ldcg(stats(c)) - top), __ldcg(stats(c) + kBlockRows), all);
+          const float inv = all == 0.f ? 0.f : 1.f / all;
+#pragma unroll 1
+          for (int ch = 0; ch < D / 32; ++ch) {
+            float v[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = 0.f;
+#pragma unroll 2
+            for (int c = 0; c < splits; ++c) {
+              const float f = exp2_approx(__ldcg(stats(c)) - top);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float4 x = __ldcg(sums(c) + (8 * ch + k) * kBlockRows);
+                v[4 * k] = fmaf(f, x.x, v[4 * k]);
+                v[4 * k + 1] = fmaf(f, x.y, v[4 * k + 1]);
+                v[4 * k + 2] = fmaf(f, x.z, v[4 * k + 2]);
+                v[4 * k + 3] = fmaf(f, x.w, v[4 * k + 3]);
+              }
+            }
+            store(ch, v, inv);
+          }
         }
       }
     }
