@@ -116,7 +116,7 @@ struct AttnControl {
   uint64_t full[WARPS][4];
   int64_t warp_sum[WARPS];
   int64_t upto[WARPS * 32];     // inclusive prefix of a thread inside its warp
-  unsigned has_head, has_tail;  // a bit per warp
+  unsigned pieces[WARPS];       // 1: head, 2: tail of a warp
   PieceInfo head[WARPS], tail[WARPS];
 };
 
@@ -232,34 +232,13 @@ __device__ __forceinline__ int64_t row_offset(const AttnParams& p, int row0, int
 // difference of two is NaN, and below any score that binary32 tells apart.
 constexpr float kNoReference = -1e30f;
 
-// The segment that unit q belongs to, and q's place in it, for a warp that
-// asks with all its lanes: the block's threads have left the prefix sums of
-// their sequences' units in shared memory.
-template <int ROWS, int WARPS>
-__device__ __forceinline__ int find_segment(const AttnParams& p, const AttnControl<WARPS>& ctl,
-                                            int per_thread, int64_t q, int lane, Segment* out) {
-  int64_t sum = lane < WARPS ? ctl.warp_sum[lane] : 0;
-  const int64_t own = sum;
-#pragma unroll
-  for (int m = 1; m < 32; m *= 2) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, sum, m);
-    if (lane >= m) sum += v;
-  }
-  const int w = __ffs(__ballot_sync(0xffffffffu, sum > q)) - 1;
-  int64_t rem = q - __shfl_sync(0xffffffffu, sum - own, w);
-  const int64_t upto = ctl.upto[w * 32 + lane];
-  const int i = __ffs(__ballot_sync(0xffffffffu, upto > rem)) - 1;
-  const int64_t before = __shfl_up_sync(0xffffffffu, upto, 1);
-  if (i > 0) rem -= __shfl_sync(0xffffffffu, before, i);
+// The segment of unit q, which is `rem` units behind the first of sequence b,
+// and q's place in it.
+template <int ROWS>
+__device__ __forceinline__ int segment_at(const AttnParams& p, int b, const Sequence& seq,
+                                          int64_t rem, int64_t q, Segment* out) {
   Segment s;
-  s.b = (w * 32 + i) * per_thread;
-  Sequence seq = attn_sequence(p, s.b);
-  while (per_thread > 1) {
-    const int64_t n = sequence_units<ROWS>(p, seq);
-    if (rem < n) break;
-    rem -= n;
-    seq = attn_sequence(p, ++s.b);
-  }
+  s.b = b;
   s.row0 = seq.row0;
   s.rows = seq.rows;
   s.len = seq.len;
@@ -277,6 +256,35 @@ __device__ __forceinline__ int find_segment(const AttnParams& p, const AttnContr
   return unit;
 }
 
+// The same for a warp that asks with all its lanes: the block's threads have
+// left the prefix sums of their sequences' units in shared memory.
+template <int ROWS, int WARPS>
+__device__ __forceinline__ int find_segment(const AttnParams& p, const AttnControl<WARPS>& ctl,
+                                            int per_thread, int64_t q, int lane, Segment* out) {
+  int64_t sum = lane < WARPS ? ctl.warp_sum[lane] : 0;
+  const int64_t own = sum;
+#pragma unroll
+  for (int m = 1; m < 32; m *= 2) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, sum, m);
+    if (lane >= m) sum += v;
+  }
+  const int w = __ffs(__ballot_sync(0xffffffffu, sum > q)) - 1;
+  int64_t rem = q - __shfl_sync(0xffffffffu, sum - own, w);
+  const int64_t upto = ctl.upto[w * 32 + lane];
+  const int i = __ffs(__ballot_sync(0xffffffffu, upto > rem)) - 1;
+  const int64_t before = __shfl_up_sync(0xffffffffu, upto, 1);
+  if (i > 0) rem -= __shfl_sync(0xffffffffu, before, i);
+  int b = (w * 32 + i) * per_thread;
+  Sequence seq = attn_sequence(p, b);
+  while (per_thread > 1) {
+    const int64_t n = sequence_units<ROWS>(p, seq);
+    if (rem < n) break;
+    rem -= n;
+    seq = attn_sequence(p, ++b);
+  }
+  return segment_at<ROWS>(p, b, seq, rem, q, out);
+}
+
 template <int D, int G, int NT, int WARPS, int TILES>
 __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p) {
   using C = AttnConfig<D, G, NT, WARPS>;
@@ -288,30 +296,44 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
 
-  // ---- the units of the batch: thread i counts those of a contiguous range
-  // of sequences
-  const int per_thread = (p.batch.seqs + C::kThreads - 1) / C::kThreads;
-  const int b_begin = min(p.batch.seqs, tid * per_thread);
-  const int b_end = min(p.batch.seqs, b_begin + per_thread);
-  int64_t upto = 0;
-  for (int b = b_begin; b < b_end; ++b)
-    upto += sequence_units<ROWS>(p, attn_sequence(p, b));
-  if (tid < WARPS * NS) {
-    mbar_init(&ctl->full[tid / NS][tid % NS], 1);
+  if (lane == 0) {
+    for (int i = 0; i < NS; ++i) mbar_init(&ctl->full[warp][i], 1);
     fence_mbar_init();
+    ctl->pieces[warp] = 0u;
   }
-  if (tid == 0) ctl->has_head = ctl->has_tail = 0u;
+  __syncwarp();
+
+  // ---- the units of the batch.  Up to 32 sequences: every warp counts them
+  // by itself, lane b sequence b.  More: thread i counts those of a contiguous
+  // range of sequences, and the prefix sums meet in shared memory.
+  const bool few = p.batch.seqs <= 32;
+  const int per_thread = (p.batch.seqs + C::kThreads - 1) / C::kThreads;
+  Sequence mine = {0, 0, 0};
+  int64_t upto = 0, total = 0;
+  if (few) {
+    if (lane < p.batch.seqs) {
+      mine = attn_sequence(p, lane);
+      upto = sequence_units<ROWS>(p, mine);
+    }
+  } else {
+    const int b_begin = min(p.batch.seqs, tid * per_thread);
+    const int b_end = min(p.batch.seqs, b_begin + per_thread);
+    for (int b = b_begin; b < b_end; ++b) upto += sequence_units<ROWS>(p, attn_sequence(p, b));
+  }
 #pragma unroll
   for (int m = 1; m < 32; m *= 2) {
     const int64_t v = __shfl_up_sync(0xffffffffu, upto, m);
     if (lane >= m) upto += v;
   }
-  ctl->upto[tid] = upto;
-  if (lane == 31) ctl->warp_sum[warp] = upto;
-  __syncthreads();
-  int64_t total = 0;
+  if (few) {
+    total = __shfl_sync(0xffffffffu, upto, 31);
+  } else {
+    ctl->upto[tid] = upto;
+    if (lane == 31) ctl->warp_sum[warp] = upto;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) total += ctl->warp_sum[w];
+    for (int w = 0; w < WARPS; ++w) total += ctl->warp_sum[w];
+  }
 
   // ---- this CTA's range (one unit per warp at least, where the batch has
   // fewer units than warps; the first `extra` CTAs have one more than the
@@ -334,7 +356,18 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
     const int64_t q1 = q0 + n_units;
     unsigned char* const ring = smem + warp * C::kRingBytes;
     Segment cs;  // of the unit being computed
-    int unit = find_segment<ROWS>(p, *ctl, per_thread, q0, lane, &cs);
+    int unit;
+    if (few) {
+      const int i = __ffs(__ballot_sync(0xffffffffu, upto > q0)) - 1;
+      const int64_t before = __shfl_up_sync(0xffffffffu, upto, 1);
+      const int64_t skipped = __shfl_sync(0xffffffffu, before, i);
+      const Sequence seq = {__shfl_sync(0xffffffffu, mine.row0, i),
+                            __shfl_sync(0xffffffffu, mine.rows, i),
+                            __shfl_sync(0xffffffffu, mine.len, i)};
+      unit = segment_at<ROWS>(p, i, seq, i > 0 ? q0 - skipped : q0, q0, &cs);
+    } else {
+      unit = find_segment<ROWS>(p, *ctl, per_thread, q0, lane, &cs);
+    }
 
     // ---- copies.  Lane 4 sub + kind copies the codes or metadata of one run
     // of tokens inside a page; page numbers are read one unit ahead.
@@ -385,7 +418,21 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
         read_page();
       }
     };
+    // Queries of column g of a segment.  Where registers allow it they are
+    // loaded before the copies wait for their page numbers.
+    constexpr bool kAhead = NT == 1 && WARPS == 8;
+    uint4 raw[NC];
+    auto load_queries = [&](int nt) {
+      const int r = cs.rb * ROWS + nt * 8 + g;
+      const __nv_bfloat16* row = p.Q + row_offset(p, cs.row0, r, cs.h, p.q_stride, D) + 8 * t;
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        raw[j] = make_uint4(0, 0, 0, 0);
+        if (r < cs.rows * p.gqa) raw[j] = *reinterpret_cast<const uint4*>(row + 32 * j);
+      }
+    };
     read_page();
+    if (kAhead) load_queries(0);
     for (int s = 0; s < NS - 1; ++s)
       if (to_copy > 0) copy_unit(s);
 
@@ -414,15 +461,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           // ---- queries of column g, scaled to binary16
-          const int r = cs.rb * ROWS + nt * 8 + g;
-          const bool have = r < cs.rows * p.gqa;
-          uint4 raw[NC];
-          const __nv_bfloat16* row = p.Q + row_offset(p, cs.row0, r, cs.h, p.q_stride, D) + 8 * t;
-#pragma unroll
-          for (int j = 0; j < NC; ++j) {
-            raw[j] = make_uint4(0, 0, 0, 0);
-            if (have) raw[j] = *reinterpret_cast<const uint4*>(row + 32 * j);
-          }
+          if (!kAhead) load_queries(nt);
           float top = 0.f;
 #pragma unroll
           for (int j = 0; j < NC; ++j) {
@@ -780,13 +819,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
           if (lane == 0) {
             (from_before ? ctl->head : ctl->tail)[warp] = {cs.rb,   cs.h,  cs.row0,
                                                            cs.rows, cs.u0, u1};
-            atomicOr(from_before ? &ctl->has_head : &ctl->has_tail, 1u << warp);
+            ctl->pieces[warp] |= from_before ? 1u : 2u;
           }
         }
         if (left > 1) {
           next_segment<ROWS>(p, cs);
           unit = 0;
           fresh = true;
+          if (kAhead) load_queries(0);
         }
       } else {
         ++unit;
@@ -801,7 +841,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
   // is the last of all CTAs' to bring that row adds them, in CTA order.
   __syncthreads();
   constexpr int VF = D / 32;  // floats of a lane
-  const unsigned has_head = ctl->has_head, has_tail = ctl->has_tail;
+  const unsigned kinds = lane < WARPS ? ctl->pieces[lane] : 0u;
+  const unsigned has_head = __ballot_sync(0xffffffffu, kinds & 1u);
+  const unsigned has_tail = __ballot_sync(0xffffffffu, kinds & 2u);
   const int first = has_head ? __ffs(has_head) - 1 : 0;
   // the segment that began before this CTA is the first warp's with units
   const bool from_before = has_head != 0u && ctl->head[first].u0 < r0;
