@@ -33,6 +33,14 @@ def test_structs_match_the_header(tmp_path):
     assert got == want
 
 
+def test_packed_structs_match_the_declared_ones():
+    """What the binding passes is the bytes of the declared structs."""
+    values = (0x10, 0x20, 0x30, 0x40, 1 << 33, 64, 8, 128, 32)
+    assert wq._pack_kv4_cache(*values) == bytes(wq._KV4CacheStruct(*values))
+    values = (3, 7, 0x50, 0x60, 0x70, 9, 1 << 34, 5)
+    assert wq._pack_kv4_batch(*values) == bytes(wq._KV4BatchStruct(*values))
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_code_order(d):
     """Two codes a byte, even element low; key words and value halfwords of

@@ -24,8 +24,8 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
-import math
 import os
+import struct
 
 import torch
 
@@ -65,6 +65,12 @@ class _KV4BatchStruct(ctypes.Structure):
                 ("table_stride", ctypes.c_int64), ("max_rows", ctypes.c_int32)]
 
 
+# The same two structs as bytes (native alignment, trailing padding included):
+# packing is a few times cheaper than filling a ctypes structure.
+_pack_kv4_cache = struct.Struct("@PPPPqiiii").pack
+_pack_kv4_batch = struct.Struct("@iiPPPiqi0q").pack
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIBRARY_PATH):
         raise ImportError(
@@ -97,15 +103,13 @@ def _load() -> ctypes.CDLL:
     lib.wq_q4k_matmul.restype = i32
     lib.wq_q4k_matmul_ex.argtypes = [vp, i64, vp, i64, i64, vp, i32, ctypes.c_uint, vp]
     lib.wq_q4k_matmul_ex.restype = i32
-    cache, batch = ctypes.POINTER(_KV4CacheStruct), ctypes.POINTER(_KV4BatchStruct)
-    lib.wq_kv4_write.argtypes = [vp, i64, vp, i64, cache, batch, vp]
+    lib.wq_kv4_write.argtypes = [vp, i64, vp, i64, vp, vp, vp]
     lib.wq_kv4_write.restype = i32
-    lib.wq_kv4_read.argtypes = [cache, batch, vp, vp, vp]
+    lib.wq_kv4_read.argtypes = [vp, vp, vp, vp, vp]
     lib.wq_kv4_read.restype = i32
     lib.wq_kv4_attention_workspace_bytes.argtypes = []
     lib.wq_kv4_attention_workspace_bytes.restype = sz
-    lib.wq_kv4_attention.argtypes = [vp, i64, i32, cache, batch, ctypes.c_float, vp, i64, vp, sz,
-                                     vp]
+    lib.wq_kv4_attention.argtypes = [vp, i64, i32, vp, vp, ctypes.c_float, vp, i64, vp, sz, vp]
     lib.wq_kv4_attention.restype = i32
     lib.wq_get_device_error.argtypes = [vp]
     lib.wq_get_device_error.restype = i32
@@ -349,9 +353,9 @@ class KV4Cache:
         for m in (self.k_meta, self.v_meta):
             if m.dtype != torch.float16 or tuple(m.shape) != meta:
                 raise ValueError(f"metadata must be float16 {list(meta)}")
-        # the format as the C ABI takes it; the addresses are set at each call
-        object.__setattr__(self, "_c", _KV4CacheStruct(
-            0, 0, 0, 0, self.pages, self.page_size, self.kv_heads, self.head_dim, self.group))
+        # the sizes in the order of the C struct, the addresses being taken at each call
+        sizes = (self.pages, self.page_size, self.kv_heads, self.head_dim, self.group)
+        object.__setattr__(self, "_sizes", sizes)
 
     @property
     def pages(self) -> int:
@@ -374,11 +378,9 @@ class KV4Cache:
         return (self.k_codes.nbytes + self.k_meta.nbytes + self.v_codes.nbytes
                 + self.v_meta.nbytes)
 
-    def _struct(self) -> _KV4CacheStruct:
-        c = self._c
-        c.k_codes, c.k_meta = self.k_codes.data_ptr(), self.k_meta.data_ptr()
-        c.v_codes, c.v_meta = self.v_codes.data_ptr(), self.v_meta.data_ptr()
-        return c
+    def _struct(self) -> bytes:
+        return _pack_kv4_cache(self.k_codes.data_ptr(), self.k_meta.data_ptr(),
+                               self.v_codes.data_ptr(), self.v_meta.data_ptr(), *self._sizes)
 
 
 def kv4_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, group: int = 64,
@@ -397,57 +399,58 @@ def kv4_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, gro
     return KV4Cache(codes(), meta(), codes(), meta(), group)
 
 
-def _kv4_batch(cache: KV4Cache, rows: int, seq_lens, page_table, row_starts, max_rows):
+def _kv4_batch(index: int, rows: int, seq_lens, page_table, row_starts, max_rows) -> bytes:
     """The batch struct after the checks the C ABI cannot make (types, shapes
     and devices of the int32 arrays)."""
-    dev = cache.k_codes.device
-    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
+    if seq_lens.dtype is not torch.int32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
         raise ValueError("seq_lens must be a contiguous 1-D int32 tensor")
     seqs = seq_lens.shape[0]
-    if (page_table.dtype != torch.int32 or page_table.dim() != 2
-            or page_table.shape[0] != seqs):
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2:
         raise ValueError("page_table must be an int32 tensor [sequences, pages]")
-    width = page_table.shape[1]
+    entries, width = page_table.shape
     stride, step = page_table.stride()
+    if entries != seqs:
+        raise ValueError("page_table must have a row for each sequence")
     if width > 1 and step != 1:
         raise ValueError("rows of page_table must be contiguous")
-    if seq_lens.device != dev or page_table.device != dev:
+    if seq_lens.get_device() != index or page_table.get_device() != index:
         raise ValueError("seq_lens and page_table must be on the cache's device")
-    starts = None
+    starts = 0
     if row_starts is not None:
-        if (row_starts.dtype != torch.int32 or row_starts.shape != (seqs + 1,)
+        if (row_starts.dtype is not torch.int32 or row_starts.shape != (seqs + 1,)
                 or not row_starts.is_contiguous()):
             raise ValueError("row_starts must be a contiguous int32 tensor [sequences + 1]")
-        if row_starts.device != dev:
+        if row_starts.get_device() != index:
             raise ValueError("row_starts must be on the cache's device")
         starts = row_starts.data_ptr()
-    return _KV4BatchStruct(seqs, rows, starts, seq_lens.data_ptr(), page_table.data_ptr(), width,
+    return _pack_kv4_batch(seqs, rows, starts, seq_lens.data_ptr(), page_table.data_ptr(), width,
                            stride if seqs > 1 else width, max_rows or 0)
 
 
-def _kv4_rows(x: torch.Tensor, heads: int | None, cache: KV4Cache, what: str) -> int:
-    """The row stride in elements of a bfloat16 tensor [rows, heads, head_dim]
-    whose heads are contiguous (a slice of a fused projection's rows, say)."""
-    shape = x.shape
-    d = cache._c.head_dim
-    if x.dtype != torch.bfloat16 or len(shape) != 3 or shape[2] != d or (
-            heads is not None and shape[1] != heads):
+def _kv4_rows(x: torch.Tensor, heads: int | None, d: int, index: int, what: str) -> int:
+    """The row stride in elements of a bfloat16 tensor [rows, heads, d] whose
+    heads are contiguous (a slice of a fused projection's rows, say)."""
+    if x.dtype is not torch.bfloat16 or x.dim() != 3:
         raise ValueError(f"{what} must be bfloat16 [rows, {heads or 'heads'}, {d}]")
-    if x.device != cache.k_codes.device:
-        raise ValueError(f"{what} is on another device than the cache")
+    rows, h, size = x.shape
+    if size != d or (heads is not None and h != heads):
+        raise ValueError(f"{what} must be bfloat16 [rows, {heads or 'heads'}, {d}]")
+    if x.get_device() != index:
+        raise ValueError(f"{what} must be on the cache's device")
+    if x.is_contiguous():
+        return h * d
     row, head, step = x.stride()
-    if x.numel() and (step != 1 or (shape[1] > 1 and head != d)):
+    if step != 1 or (h > 1 and head != d):
         raise ValueError(f"the heads of a row of {what} must be contiguous")
-    return row if shape[0] > 1 else shape[1] * d
+    return row if rows > 1 else h * d
 
 
-def _on(device: torch.device, call, *args) -> int:
-    """call(*args, the device's current stream) with the device current."""
-    index = device.index
+def _on(index: int, call, *args) -> int:
+    """call(*args, the current stream of device `index`) with that device current."""
     stream = torch._C._cuda_getCurrentRawStream(index)
     if torch._C._cuda_getDevice() == index:
         return call(*args, stream)
-    with torch.cuda.device(device):
+    with torch.cuda.device(index):
         return call(*args, stream)
 
 
@@ -459,13 +462,18 @@ def kv4_write(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, seq_lens: torch
     seq_lens int32 [seqs] counts the tokens with the new rows included;
     page_table int32 [seqs, width]; row_starts int32 [seqs + 1] gives the rows
     of each sequence (None: rows/seqs each).  All on the GPU."""
-    ks = _kv4_rows(k, cache._c.kv_heads, cache, "k")
-    vs = _kv4_rows(v, cache._c.kv_heads, cache, "v")
-    if k.shape[0] != v.shape[0]:
+    _, _, heads, d, _ = cache._sizes
+    index = cache.k_codes.get_device()
+    ks = _kv4_rows(k, heads, d, index, "k")
+    vs = _kv4_rows(v, heads, d, index, "v")
+    rows = k.shape[0]
+    if rows != v.shape[0]:
         raise ValueError("k and v must have the same rows")
-    batch = _kv4_batch(cache, k.shape[0], seq_lens, page_table, row_starts, None)
-    _check(_on(cache.k_codes.device, lib.wq_kv4_write, k.data_ptr(), ks, v.data_ptr(), vs,
-               cache._struct(), batch), "wq_kv4_write")
+    batch = _kv4_batch(index, rows, seq_lens, page_table, row_starts, None)
+    status = _on(index, lib.wq_kv4_write, k.data_ptr(), ks, v.data_ptr(), vs, cache._struct(),
+                 batch)
+    if status:
+        raise WQError(status, "wq_kv4_write")
 
 
 def kv4_read(cache: KV4Cache, seq_lens: torch.Tensor, page_table: torch.Tensor,
@@ -475,23 +483,26 @@ def kv4_read(cache: KV4Cache, seq_lens: torch.Tensor, page_table: torch.Tensor,
     stand for, bfloat16 [rows, kv_heads, head_dim]; the arguments as for
     ``kv4_write``.  ``rows`` or ``out`` gives the number of rows; rows behind
     the last sequence are left as they were in ``out`` (zeros without it)."""
-    dev = cache.k_codes.device
+    _, _, heads, d, _ = cache._sizes
+    index = cache.k_codes.get_device()
     if out is None:
         if rows is None:
             raise ValueError("rows or out is required")
         make = torch.empty if row_starts is None else torch.zeros
-        out = tuple(make((rows, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16, device=dev)
+        out = tuple(make((rows, heads, d), dtype=torch.bfloat16, device=cache.k_codes.device)
                     for _ in range(2))
     k, v = out
-    for x, what in ((k, "out[0]"), (v, "out[1]")):
-        _kv4_rows(x, cache._c.kv_heads, cache, what)
-        if not x.is_contiguous():
-            raise ValueError(f"{what} must be contiguous")
-    if k.shape[0] != v.shape[0] or (rows is not None and rows != k.shape[0]):
+    _kv4_rows(k, heads, d, index, "out[0]")
+    _kv4_rows(v, heads, d, index, "out[1]")
+    if not (k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("the outputs must be contiguous")
+    n = k.shape[0]
+    if n != v.shape[0] or (rows is not None and rows != n):
         raise ValueError("the outputs must have the same rows")
-    batch = _kv4_batch(cache, k.shape[0], seq_lens, page_table, row_starts, None)
-    _check(_on(dev, lib.wq_kv4_read, cache._struct(), batch, k.data_ptr(), v.data_ptr()),
-           "wq_kv4_read")
+    batch = _kv4_batch(index, n, seq_lens, page_table, row_starts, None)
+    status = _on(index, lib.wq_kv4_read, cache._struct(), batch, k.data_ptr(), v.data_ptr())
+    if status:
+        raise WQError(status, "wq_kv4_read")
     return k, v
 
 
@@ -516,24 +527,28 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, seq_lens: torch.Tensor,
     caller keeps, for instance in a captured graph; without it each call makes
     its own.  Rows behind the last sequence are left as they were in ``out``
     (zeros without it)."""
-    qs = _kv4_rows(q, None, cache, "q")
-    dev = cache.k_codes.device
+    _, _, heads, d, _ = cache._sizes
+    index = cache.k_codes.get_device()
+    qs = _kv4_rows(q, None, d, index, "q")
+    rows, q_heads, _ = q.shape
+    if q_heads == 0 or q_heads % heads:
+        raise ValueError("q_heads must be a multiple of kv_heads")
     if out is None:
         make = torch.empty if row_starts is None else torch.zeros
-        out = make(q.shape, dtype=torch.bfloat16, device=dev)
-    os_ = _kv4_rows(out, q.shape[1], cache, "out")
-    if out.shape[0] != q.shape[0]:
+        out = make(q.shape, dtype=torch.bfloat16, device=q.device)
+    os_ = _kv4_rows(out, q_heads, d, index, "out")
+    if out.shape[0] != rows:
         raise ValueError("out must have the rows of q")
-    if q.shape[1] % cache._c.kv_heads or q.shape[1] == 0:
-        raise ValueError("q_heads must be a multiple of kv_heads")
     if workspace is None:
-        workspace = kv4_workspace(dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
+        workspace = kv4_workspace(q.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on the cache's device")
-    batch = _kv4_batch(cache, q.shape[0], seq_lens, page_table, row_starts, max_rows)
-    _check(_on(dev, lib.wq_kv4_attention, q.data_ptr(), qs, q.shape[1], cache._struct(), batch,
-               1.0 / math.sqrt(cache._c.head_dim) if scale is None else float(scale),
-               out.data_ptr(), os_, workspace.data_ptr(), workspace.nbytes), "wq_kv4_attention")
+    batch = _kv4_batch(index, rows, seq_lens, page_table, row_starts, max_rows)
+    status = _on(index, lib.wq_kv4_attention, q.data_ptr(), qs, q_heads, cache._struct(), batch,
+                 d ** -0.5 if scale is None else scale, out.data_ptr(), os_,
+                 workspace.data_ptr(), workspace.nbytes)
+    if status:
+        raise WQError(status, "wq_kv4_attention")
     return out
 
 
