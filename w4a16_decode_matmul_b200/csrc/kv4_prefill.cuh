@@ -24,7 +24,7 @@
 // rounded to binary16 (exact for every bfloat16 within 2^-21 of the row's
 // largest).  Keys and values: s (u - z) rounded once to binary16 (2^-11 half
 // step; exact where it is subnormal, since s is a multiple of 2^-24).  A tile
-// with a scale above 4366, the only ones whose values can pass 65504, is
+// with a scale of 4368 or more, the only ones whose values can pass 65504, is
 // halved, and the softmax doubles it back.  Weights: 2^(S - m) rounded to
 // binary16; the reference m is raised only when a row's largest weight would
 // pass 2^14, then so that it becomes 2^7 (and the row's output is rescaled).
@@ -60,8 +60,10 @@ using gemm2::tmem_st16;
 constexpr int kTile = 128;       // rows of a tile, tokens of a step
 constexpr int kBlockRows = 256;  // rows of a CTA
 constexpr int kPrefillThreads = 16 * 32;  // four warpgroups; the last has one busy warp
+// Scales from 4368 on (the binary16 after 4364) can stand for values past
+// 65504: 15 * 4364 = 65460.
+constexpr uint32_t kWideScaleBits = 0x6C44u;
 constexpr int kMmaWarp = 12;
-constexpr int kWideScale = 4366;  // 15 * 4366 is the last multiple below 65504
 
 struct PrefillParams {
   AttnParams a;
@@ -132,6 +134,13 @@ __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
   return r;
 }
 
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                       uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
 // One thread of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -155,6 +164,38 @@ __device__ __forceinline__ bool named_barrier_or(uint32_t id, uint32_t threads, 
       : "r"(uint32_t(p)), "r"(id), "r"(threads)
       : "memory");
   return r != 0;
+}
+
+// Codes of four tokens, 32 apart, to a tile's values s (u - z), halved if wide,
+// in the unpack's order; `put` are the places of the first token's chunks.
+template <int NC, int NG, bool VALUES>
+__device__ __forceinline__ void expand_tile(const uint32_t (&code)[4][NC],
+                                            const uint32_t (&meta)[4][NG],
+                                            const uint32_t (&put)[NC], uint32_t tile, bool wide) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    uint32_t s2 = 0, lo = 0, hi = 0;
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      if (k % (NC / NG) == 0) {
+        const uint32_t m = meta[u][k / (NC / NG)], z2 = __byte_perm(m, m, 0x3232);
+        s2 = __byte_perm(m, m, 0x1010);
+        if (wide) s2 = hmul2(s2, 0x38003800u);  // 1/2
+        lo = hadd2(z2, 0x64006400u);            // 1024 + z
+        hi = hsub2(0xD400D400u, z2);            // -(64 + z)
+      }
+      // a value word is made of the halfwords of two g (see kv4.cuh)
+      const uint32_t word = VALUES ? __byte_perm(code[u][k / 2], code[u][NC / 2 + k / 2],
+                                                 (k & 1) ? 0x7632 : 0x5410)
+                                   : code[u][k];
+      const uint32_t w8 = word >> 8;
+      sts128(tile + put[k] + 4096u * u,
+             hmul2(hsub2(lop3_and_or(word, 0x000F000Fu, 0x64006400u), lo), s2),
+             hmul2(hfma2(lop3_and_or(word, 0x00F000F0u, 0x64006400u), 0x2C002C00u, hi), s2),
+             hmul2(hsub2(lop3_and_or(w8, 0x000F000Fu, 0x64006400u), lo), s2),
+             hmul2(hfma2(lop3_and_or(w8, 0x00F000F0u, 0x64006400u), 0x2C002C00u, hi), s2));
+    }
+  }
 }
 
 // The rows of a block of 256: the blocks of sequence b begin at index
@@ -344,11 +385,22 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
     // ---- keys and values.  Thread (token, t): words t of every chunk of the
     // rows of four tokens of each tile; neighbouring lanes take tokens 4 apart,
     // so that 8 lanes write 8 different bank groups.
-    const int t = lane & 3, o = lane >> 2, w = warp - 8;
-    const int tok = 8 * w + 4 * (o & 1) + (o >> 1);  // and + 32, 64, 96
+    const int t = lane & 3, o = lane >> 2;
+    const int perm = 4 * (o & 1) + (o >> 1);
+    const int tok = 8 * (warp - 8) + perm;  // and + 32, 64, 96
     const int* const table =
         p.a.batch.page_table + int64_t(block.b) * p.a.batch.table_stride;
     const Cache& cache = p.a.cache;
+    const int page_mask = (1 << cache.page_shift) - 1;
+    // byte offset of chunk k of token `tok` in a tile; token tok + 32 u follows
+    // 4096 u bytes behind
+    uint32_t put[NC];
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      const int chunk = 4 * k + t;
+      put[k] =
+          uint32_t((chunk >> 3) * C::kBlockBytes + tok * 128 + (((chunk & 7) ^ perm) << 4));
+    }
     uint32_t kc[4][NC], vc[4][NC], km[4][NG], vm[4][NG];
     int page[4];
     int64_t at[4];  // row of the cache, or -1 behind the last token
@@ -373,8 +425,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
           record_status(kStatusInvalid);
           page[u] = 0;  // any page of the cache can be read
         }
-        at[u] = ((int64_t(page[u]) * heads + head) << cache.page_shift) +
-                (pos & ((1 << cache.page_shift) - 1));
+        at[u] = ((int64_t(page[u]) * heads + head) << cache.page_shift) + (pos & page_mask);
         load_words<NC>(cache.k_codes + at[u] * (D / 2) + t * NC * 4, kc[u]);
         load_words<NG>(reinterpret_cast<const unsigned char*>(cache.k_meta + at[u] * NG), km[u]);
       }
@@ -391,53 +442,27 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
         load_words<NG>(reinterpret_cast<const unsigned char*>(cache.v_meta + at[u] * NG), vm[u]);
       }
     };
-    // eight codes -> eight values in the unpack's order, 16 bytes
-    auto expand = [&](uint32_t word, uint32_t meta, bool wide) {
-      const uint32_t z2 = __byte_perm(meta, meta, 0x3232);
-      uint32_t s2 = __byte_perm(meta, meta, 0x1010);
-      if (wide) s2 = hmul2(s2, 0x38003800u);  // 1/2
-      const uint32_t lo = hadd2(z2, 0x64006400u);   // 1024 + z
-      const uint32_t hi = hsub2(0xD400D400u, z2);   // -(64 + z)
-      const uint32_t w8 = word >> 8;
-      uint4 r;
-      r.x = hmul2(hsub2(lop3_and_or(word, 0x000F000Fu, 0x64006400u), lo), s2);
-      r.y = hmul2(hfma2(lop3_and_or(word, 0x00F000F0u, 0x64006400u), 0x2C002C00u, hi), s2);
-      r.z = hmul2(hsub2(lop3_and_or(w8, 0x000F000Fu, 0x64006400u), lo), s2);
-      r.w = hmul2(hfma2(lop3_and_or(w8, 0x00F000F0u, 0x64006400u), 0x2C002C00u, hi), s2);
-      return r;
-    };
-    auto place = [&](unsigned char* tile, int u, int j) {
-      const int row = 32 * u + tok, chunk = 4 * j + t;
-      return reinterpret_cast<uint4*>(tile + (chunk >> 3) * C::kBlockBytes + row * 128 +
-                                      (((chunk & 7) ^ (row & 7)) << 4));
-    };
     if (steps > 0) {
       read_pages(0);
       read_keys(0);
       read_values();
       if (steps > 1) read_pages(1);
     }
+    const uint32_t k_tiles = smem_addr(smem + C::kOffK), v_tiles = smem_addr(smem + C::kOffV);
     bool ok = true;
     for (int j = 0; j < steps; ++j) {
       const int stage = j & 1;
       const uint32_t parity = (uint32_t(j >> 1) & 1u) ^ 1u;
-      bool wide = false;
+      uint32_t most = 0u;  // low half: the scales (positive); high: the zeros
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int k = 0; k < NG; ++k)
-          wide |= meta_pair(km[u][k]).x > float(kWideScale) ||
-                  meta_pair(vm[u][k]).x > float(kWideScale);
-      wide = named_barrier_or(1, 128, wide);
+        for (int k = 0; k < NG; ++k) most = __vmaxu2(most, __vmaxu2(km[u][k], vm[u][k]));
+      const bool wide = named_barrier_or(1, 128, (most & 0xffffu) >= kWideScaleBits);
       // after a wait that gave up, the loop only keeps the barrier's count
       ok = ok && __all_sync(0xffffffffu, wait(&ctl->k_free[stage], parity));
       if (!ok) continue;
-      unsigned char* const ktile = smem + C::kOffK + stage * C::kTileBytes;
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int k = 0; k < NC; ++k)
-          *place(ktile, u, k) = expand(kc[u][k], km[u][k * 32 / G], wide);
+      expand_tile<NC, NG, false>(kc, km, put, k_tiles + stage * C::kTileBytes, wide);
       if (tid == 256) *reinterpret_cast<volatile int*>(&ctl->wide[j & 3]) = wide ? 1 : 0;
       fence_async_shared();
       __syncwarp();
@@ -446,15 +471,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
 
       ok = __all_sync(0xffffffffu, wait(&ctl->v_free[stage], parity));
       if (!ok) continue;
-      unsigned char* const vtile = smem + C::kOffV + stage * C::kTileBytes;
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int k = 0; k < NC; ++k) {
-          const uint32_t word = __byte_perm(vc[u][k / 2], vc[u][NC / 2 + k / 2],
-                                            (k & 1) ? 0x7632 : 0x5410);
-          *place(vtile, u, k) = expand(word, vm[u][k * 32 / G], wide);
-        }
+      expand_tile<NC, NG, true>(vc, vm, put, v_tiles + stage * C::kTileBytes, wide);
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->v_full[stage]);
