@@ -246,7 +246,7 @@ wq_status wq_q4k_matmul_ex(const void *X, int64_t M, const void *blocks, int64_t
  *   x), hi = max(0, max x); s = smallest binary16 >= (hi - lo)/15 (1 if hi =
  *   lo); z = clamp(round(-lo/s), 0, 15); u = clamp(round(x/s) + z, 0, 15);
  *   every rounding half-to-even of the exact value.  It stands for s (u - z).
- * A value that is NaN or infinite makes the codes of its group unspecified.
+ * The code of a NaN is unspecified.
  *
  * A cache is a pool of pages of `page_size` tokens, in four device buffers
  * that the caller owns (16-byte aligned):

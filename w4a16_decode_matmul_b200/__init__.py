@@ -545,7 +545,7 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, seq_lens: torch.Tensor,
         raise ValueError("workspace must be contiguous and on the cache's device")
     batch = _kv4_batch(index, rows, seq_lens, page_table, row_starts, max_rows)
     status = _on(index, lib.wq_kv4_attention, q.data_ptr(), qs, q_heads, cache._struct(), batch,
-                 d ** -0.5 if scale is None else scale, out.data_ptr(), os_,
+                 d ** -0.5 if scale is None else float(scale), out.data_ptr(), os_,
                  workspace.data_ptr(), workspace.nbytes)
     if status:
         raise WQError(status, "wq_kv4_attention")
