@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
                 zc_next[nt][k][0] = fmaf(w0, f.y - 8.f, zc_next[nt][k][0]);
                 zc_next[nt][k][1] = fmaf(w1, f.y - 8.f, zc_next[nt][k][1]);
                 w16[h][i][k][nt] = pack_half2(w0, w1);
-                most[nt] = __vmaxu2(most[nt], w16[h][i][k][nt]);
+                most[nt] = hmax2(most[nt], w16[h][i][k][nt]);
               }
             }
         // 0x7800 is 2^15; a NaN (above infinity, 0x7c00) raises nothing
