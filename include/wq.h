@@ -317,7 +317,8 @@ wq_status wq_kv4_read(const wq_kv4_cache *cache, const wq_kv4_batch *batch, void
 /* Bytes of the attention workspace: a device buffer, 16-byte aligned, filled
  * with zeros before its first use and left ready by every call.  Calls that
  * may run at the same time (other streams, graphs replayed concurrently)
- * need different workspaces. */
+ * need different workspaces.  After a call that recorded WQ_ERR_TIMEOUT the
+ * workspace must be zero-filled again. */
 size_t wq_kv4_attention_workspace_bytes(void);
 
 /* Causal attention of the rows' queries over the cache:

@@ -488,6 +488,45 @@ def test_two_streams_with_a_workspace_each():
     assert all(torch.equal(o, got) for out in outs for o in out)
 
 
+def test_two_streams_with_many_rows_and_few():
+    """Both attention kernels at once, each stream with its own workspace."""
+    many = run_attention(64, 32, 32, 2, 4, [900], [60], seed=12)
+    few = run_attention(128, 64, 64, 2, 4, [3000], [1], seed=13)
+    torch.cuda.synchronize()
+    outs = []
+    for (got, cache, table, q), lens in ((many, [900]), (few, [3000])):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            ws, n, tb = wq().kv4_workspace(), ints(lens), ints(table)
+            outs.append((got, [wq().kv4_attention(q, cache, n, tb, workspace=ws)
+                               for _ in range(20)]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, got) for got, each in outs for o in each)
+
+
+def test_page_table_that_is_part_of_a_wider_one():
+    lens, rows = [70, 33, 90], [2, 1, 3]
+    got, cache, table, q = run_attention(64, 64, 16, 2, 2, lens, rows, seed=14)
+    wide = torch.full((3, table.shape[1] + 5), -1, dtype=torch.int32, device="cuda")
+    wide[:, 2:2 + table.shape[1]] = ints(table)
+    part = wide[:, 2:2 + table.shape[1]]
+    starts = ints(starts_of(rows))
+    assert torch.equal(wq().kv4_attention(q, cache, ints(lens), part, starts, max_rows=3), got)
+    a = wq().kv4_read(cache, ints(lens), part, ints(starts_of(lens)), rows=sum(lens))
+    b = wq().kv4_read(cache, ints(lens), ints(table), ints(starts_of(lens)), rows=sum(lens))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert wq().get_device_error() == 0
+
+
+def test_five_thousand_sequences():
+    lens = [1 + (11 * i) % 50 for i in range(5000)]
+    got, cache, table, q = run_attention(64, 32, 16, 1, 1, lens, [1] * 5000, seed=15)
+
+
+@pytest.mark.parametrize("gqa", [33, 70, 300])
+def test_very_wide_groups(gqa):
+    run_attention(128, 64, 16, 1, gqa, [40, 200], [1, 2], seed=gqa)
+
+
 def test_bad_device_arrays_are_recorded_and_stay_in_bounds():
     d, group, heads, page = 64, 32, 2, 16
     lens = [40, 40]
