@@ -67,6 +67,8 @@ class _KV4BatchStruct(ctypes.Structure):
 
 # The same two structs as bytes (native alignment, trailing padding included):
 # packing is a few times cheaper than filling a ctypes structure.
+_BF16, _I32 = torch.bfloat16, torch.int32
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 _pack_kv4_cache = struct.Struct("@PPPPqiiii").pack
 _pack_kv4_batch = struct.Struct("@iiPPPiqi0q").pack
 
@@ -402,35 +404,38 @@ def kv4_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, gro
 def _kv4_batch(index: int, rows: int, seq_lens, page_table, row_starts, max_rows) -> bytes:
     """The batch struct after the checks the C ABI cannot make (types, shapes
     and devices of the int32 arrays)."""
-    if seq_lens.dtype is not torch.int32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
+    if seq_lens.dtype is not _I32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
         raise ValueError("seq_lens must be a contiguous 1-D int32 tensor")
-    seqs = seq_lens.shape[0]
-    if page_table.dtype is not torch.int32 or page_table.dim() != 2:
+    if page_table.dtype is not _I32 or page_table.dim() != 2:
         raise ValueError("page_table must be an int32 tensor [sequences, pages]")
-    entries, width = page_table.shape
-    stride, step = page_table.stride()
-    if entries != seqs:
+    seqs, width = page_table.shape
+    if seq_lens.shape[0] != seqs:
         raise ValueError("page_table must have a row for each sequence")
-    if width > 1 and step != 1:
-        raise ValueError("rows of page_table must be contiguous")
+    stride = width
+    if not page_table.is_contiguous():
+        stride, step = page_table.stride()
+        if width > 1 and step != 1:
+            raise ValueError("rows of page_table must be contiguous")
+        if seqs <= 1:
+            stride = width
     if seq_lens.get_device() != index or page_table.get_device() != index:
         raise ValueError("seq_lens and page_table must be on the cache's device")
     starts = 0
     if row_starts is not None:
-        if (row_starts.dtype is not torch.int32 or row_starts.shape != (seqs + 1,)
+        if (row_starts.dtype is not _I32 or row_starts.shape != (seqs + 1,)
                 or not row_starts.is_contiguous()):
             raise ValueError("row_starts must be a contiguous int32 tensor [sequences + 1]")
         if row_starts.get_device() != index:
             raise ValueError("row_starts must be on the cache's device")
         starts = row_starts.data_ptr()
     return _pack_kv4_batch(seqs, rows, starts, seq_lens.data_ptr(), page_table.data_ptr(), width,
-                           stride if seqs > 1 else width, max_rows or 0)
+                           stride, max_rows or 0)
 
 
-def _kv4_rows(x: torch.Tensor, heads: int | None, d: int, index: int, what: str) -> int:
-    """The row stride in elements of a bfloat16 tensor [rows, heads, d] whose
-    heads are contiguous (a slice of a fused projection's rows, say)."""
-    if x.dtype is not torch.bfloat16 or x.dim() != 3:
+def _kv4_rows(x: torch.Tensor, heads: int | None, d: int, index: int, what: str):
+    """(rows, heads, row stride in elements) of a bfloat16 tensor [rows, heads,
+    d] whose heads are contiguous (a slice of a fused projection's rows, say)."""
+    if x.dtype is not _BF16 or x.dim() != 3:
         raise ValueError(f"{what} must be bfloat16 [rows, {heads or 'heads'}, {d}]")
     rows, h, size = x.shape
     if size != d or (heads is not None and h != heads):
@@ -438,20 +443,23 @@ def _kv4_rows(x: torch.Tensor, heads: int | None, d: int, index: int, what: str)
     if x.get_device() != index:
         raise ValueError(f"{what} must be on the cache's device")
     if x.is_contiguous():
-        return h * d
+        return rows, h, h * d
     row, head, step = x.stride()
     if step != 1 or (h > 1 and head != d):
         raise ValueError(f"the heads of a row of {what} must be contiguous")
-    return row if rows > 1 else h * d
+    return rows, h, row if rows > 1 else h * d
 
 
-def _on(index: int, call, *args) -> int:
-    """call(*args, the current stream of device `index`) with that device current."""
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if torch._C._cuda_getDevice() == index:
-        return call(*args, stream)
-    with torch.cuda.device(index):
-        return call(*args, stream)
+def _on(index: int, call, what: str, *args) -> None:
+    """call(*args, the current stream of device `index`) with that device
+    current; raises for a status other than WQ_OK."""
+    if _current_device() == index:
+        status = call(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = call(*args, _raw_stream(index))
+    if status:
+        raise WQError(status, what)
 
 
 def kv4_write(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, seq_lens: torch.Tensor,
@@ -464,16 +472,12 @@ def kv4_write(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, seq_lens: torch
     of each sequence (None: rows/seqs each).  All on the GPU."""
     _, _, heads, d, _ = cache._sizes
     index = cache.k_codes.get_device()
-    ks = _kv4_rows(k, heads, d, index, "k")
-    vs = _kv4_rows(v, heads, d, index, "v")
-    rows = k.shape[0]
-    if rows != v.shape[0]:
+    rows, _, ks = _kv4_rows(k, heads, d, index, "k")
+    v_rows, _, vs = _kv4_rows(v, heads, d, index, "v")
+    if rows != v_rows:
         raise ValueError("k and v must have the same rows")
-    batch = _kv4_batch(index, rows, seq_lens, page_table, row_starts, None)
-    status = _on(index, lib.wq_kv4_write, k.data_ptr(), ks, v.data_ptr(), vs, cache._struct(),
-                 batch)
-    if status:
-        raise WQError(status, "wq_kv4_write")
+    _on(index, lib.wq_kv4_write, "wq_kv4_write", k.data_ptr(), ks, v.data_ptr(), vs,
+        cache._struct(), _kv4_batch(index, rows, seq_lens, page_table, row_starts, None))
 
 
 def kv4_read(cache: KV4Cache, seq_lens: torch.Tensor, page_table: torch.Tensor,
@@ -492,17 +496,14 @@ def kv4_read(cache: KV4Cache, seq_lens: torch.Tensor, page_table: torch.Tensor,
         out = tuple(make((rows, heads, d), dtype=torch.bfloat16, device=cache.k_codes.device)
                     for _ in range(2))
     k, v = out
-    _kv4_rows(k, heads, d, index, "out[0]")
-    _kv4_rows(v, heads, d, index, "out[1]")
+    n, _, _ = _kv4_rows(k, heads, d, index, "out[0]")
+    v_rows, _, _ = _kv4_rows(v, heads, d, index, "out[1]")
     if not (k.is_contiguous() and v.is_contiguous()):
         raise ValueError("the outputs must be contiguous")
-    n = k.shape[0]
-    if n != v.shape[0] or (rows is not None and rows != n):
+    if n != v_rows or (rows is not None and rows != n):
         raise ValueError("the outputs must have the same rows")
-    batch = _kv4_batch(index, n, seq_lens, page_table, row_starts, None)
-    status = _on(index, lib.wq_kv4_read, cache._struct(), batch, k.data_ptr(), v.data_ptr())
-    if status:
-        raise WQError(status, "wq_kv4_read")
+    _on(index, lib.wq_kv4_read, "wq_kv4_read", cache._struct(),
+        _kv4_batch(index, n, seq_lens, page_table, row_starts, None), k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -529,26 +530,23 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, seq_lens: torch.Tensor,
     (zeros without it)."""
     _, _, heads, d, _ = cache._sizes
     index = cache.k_codes.get_device()
-    qs = _kv4_rows(q, None, d, index, "q")
-    rows, q_heads, _ = q.shape
+    rows, q_heads, qs = _kv4_rows(q, None, d, index, "q")
     if q_heads == 0 or q_heads % heads:
         raise ValueError("q_heads must be a multiple of kv_heads")
     if out is None:
         make = torch.empty if row_starts is None else torch.zeros
-        out = make(q.shape, dtype=torch.bfloat16, device=q.device)
-    os_ = _kv4_rows(out, q_heads, d, index, "out")
-    if out.shape[0] != rows:
+        out = make(q.shape, dtype=_BF16, device=q.device)
+    out_rows, _, os_ = _kv4_rows(out, q_heads, d, index, "out")
+    if out_rows != rows:
         raise ValueError("out must have the rows of q")
     if workspace is None:
         workspace = kv4_workspace(q.device)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on the cache's device")
-    batch = _kv4_batch(index, rows, seq_lens, page_table, row_starts, max_rows)
-    status = _on(index, lib.wq_kv4_attention, q.data_ptr(), qs, q_heads, cache._struct(), batch,
-                 d ** -0.5 if scale is None else float(scale), out.data_ptr(), os_,
-                 workspace.data_ptr(), workspace.nbytes)
-    if status:
-        raise WQError(status, "wq_kv4_attention")
+    _on(index, lib.wq_kv4_attention, "wq_kv4_attention", q.data_ptr(), qs, q_heads,
+        cache._struct(), _kv4_batch(index, rows, seq_lens, page_table, row_starts, max_rows),
+        d ** -0.5 if scale is None else float(scale), out.data_ptr(), os_, workspace.data_ptr(),
+        workspace.nbytes)
     return out
 
 
