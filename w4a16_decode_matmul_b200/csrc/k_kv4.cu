@@ -106,10 +106,15 @@ cudaError_t launch_attn(const kv4::AttnParams& p, cudaStream_t s, int sms) {
 }
 
 // Warps of a CTA and 16-token tiles per softmax step, by the registers that the
-// format needs.  A batch of up to four units of 32 tokens per warp takes fewer
-// warps (one sequence of 1,000 tokens, 8 kv heads: 10.1 us with 8 warps, 12.2
-// with 12; of 16,000: 16.7 and 16.5); a larger one is limited by how many
-// instructions are in flight.
+// format needs (12 warps leave 168 a thread, 8 warps 255).  Measured on B200:
+//   one block of 8 columns, four groups: one tile 67 us, two (spilling) 118;
+//     one or two groups: 58 either way;
+//   two blocks of columns, head dim 128: 8 warps 46 us, 12 (spilling) 72; head
+//     dim 64: 12 warps 34 us, 8 37.
+// A batch of up to four units of 32 tokens per warp takes 8 warps (one sequence
+// of 1,000 tokens, 8 kv heads: 10.1 us, with 12 warps 12.2; of 16,000: 16.7 and
+// 16.5); a larger one is limited by how many instructions are in flight (8
+// warps 63 us, 12 warps 55).
 template <int D, int G>
 struct AttnOp {
   static cudaError_t run(const kv4::AttnParams& p, int max_columns, cudaStream_t s, int sms) {
