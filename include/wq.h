@@ -329,8 +329,11 @@ size_t wq_kv4_attention_workspace_bytes(void);
  * [rows][q_heads][head_dim], heads contiguous, row strides in elements;
  * q_heads a multiple of kv_heads; scale finite.  A row that sees no token
  * gets zeros.  Products are of exact codes with binary16 operands (queries
- * scaled by a power of two per row, weights rounded within 2^-11), sums and
- * softmax in binary32.  Deterministic. */
+ * scaled by a power of two per row; a weight times its value scale within
+ * 2^-11, or 2^-25 of the largest weight times the largest value scale of the
+ * row's tokens where that is more), sums and softmax in binary32.
+ * The same call gives the same bits; within the roundings above, a row's may
+ * depend on the other rows of its call.  O may not overlap Q. */
 wq_status wq_kv4_attention(const void *Q, int64_t q_stride, int32_t q_heads,
                            const wq_kv4_cache *cache, const wq_kv4_batch *batch, float scale,
                            void *O, int64_t o_stride, void *workspace, size_t workspace_bytes,

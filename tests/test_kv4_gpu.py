@@ -408,6 +408,75 @@ def test_value_ranges(strength):
     ref.check(got, o, bound)
 
 
+@pytest.mark.parametrize("what,strength", [("v", 60000.0), ("k", 60000.0), ("both", 60000.0),
+                                           ("v", 2.0 ** -20)])
+@pytest.mark.parametrize("rows", [1, 3])
+def test_values_at_the_ends_of_binary16(what, strength, rows):
+    """Few rows over codes that can stand for more than binary16's largest
+    value, and over scales close to its smallest."""
+    d, group, heads, n, page = 128, 32, 2, 330, 32
+    table, pages = ref.random_batch(5, [n], page)
+    cache = new_cache(pages, heads, d, page, group)
+    spread = torch.exp2(torch.randint(-8, 1, (n, 1, 1),
+                                      generator=torch.Generator().manual_seed(7)).float())
+    k, v = ref.keys(1, n, heads, d), ref.keys(2, n, heads, d, 1.0)
+    if what != "k":
+        v = v.float().clamp(-1, 1) * spread * strength
+    if what != "v":
+        k = k.float().clamp(-1, 1) * spread * strength
+    wq().kv4_write(k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16).cuda(), cache, ints([n]),
+                   ints(table))
+    q = ref.keys(9, rows, 8, d, 1.0).float()
+    q = (q / strength if what != "v" else q).to(torch.bfloat16).cuda()
+    got = wq().kv4_attention(q, cache, ints([n]), ints(table))
+    o, bound = reference(q, cache, [n], [rows], table, d ** -0.5)
+    ref.check(got, o, bound)
+
+
+@pytest.mark.parametrize("d,group", FORMATS)
+def test_nan_and_infinite_rows_are_cached_as_finite_values(d, group):
+    """A NaN spoils its own row's codes at most: the metadata stays finite, so
+    rows that do not see the token and tokens beside it keep their values."""
+    heads, page, n = 2, 16, 40
+    table, pages = ref.random_batch(2, [n], page)
+    x = ref.keys(4, n, heads, d)
+    clean, cache = new_cache(pages, heads, d, page, group), new_cache(pages, heads, d, page, group)
+    wq().kv4_write(x.cuda(), x.cuda(), clean, ints([n]), ints(table))
+    bad = x.clone()
+    bad[-1, 0, 3], bad[-2, 1] = float("nan"), float("nan")
+    bad[-3, 0, 7], bad[-4, 1, 9] = float("inf"), float("-inf")
+    wq().kv4_write(bad.cuda(), bad.cuda(), cache, ints([n]), ints(table))
+    for got, want in zip(wq().kv4_read(cache, ints([n]), ints(table), rows=n),
+                         wq().kv4_read(clean, ints([n]), ints(table), rows=n)):
+        assert torch.isfinite(got).all()
+        assert torch.equal(got[:-4], want[:-4])
+    for rows in (8, 40):          # each kernel
+        q = ref.keys(6, rows, 8, d, 1.0).cuda()
+        got = wq().kv4_attention(q, cache, ints([n]), ints(table))
+        assert torch.isfinite(got).all()
+        # The exact values of rows before the four are those of the clean cache.
+        # Their bits need not be: rows that share a warp or a tile with one that
+        # sees a large scale form their weights again from another reference, and
+        # each way is within the bound.
+        o, bound = reference(q, clean, [n], [rows], table, d ** -0.5)
+        ref.check(got[:-4], o[:-4], bound[:-4])
+    assert wq().get_device_error() == 0
+
+
+def test_a_nan_query_among_many_rows_stays_in_its_row():
+    d, heads, gqa = 128, 2, 4
+    _, cache, table, q = run_attention(d, 64, 16, heads, gqa, [400], [70], seed=8)
+    o, bound = reference(q, cache, [400], [70], table, d ** -0.5)
+    for value in (float("nan"), float("inf")):
+        bad = q.clone()
+        bad[33, 5, 17] = value
+        again = wq().kv4_attention(bad, cache, ints([400]), ints(table))
+        keep = torch.ones(70, heads * gqa, dtype=torch.bool)
+        keep[33, 5] = False
+        ref.check(again[keep.cuda()], o[keep.numpy()], bound[keep.numpy()])
+        assert not torch.isfinite(again[33, 5]).any()
+
+
 def test_a_nan_query_stays_in_its_row():
     d, heads, gqa = 128, 2, 4
     got, cache, table, q = run_attention(d, 64, 16, heads, gqa, [90, 40], [2, 2], seed=8)
