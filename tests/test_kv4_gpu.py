@@ -151,6 +151,44 @@ def test_write_edge_values(d, group):
     assert_cache(cache, want)
 
 
+@pytest.mark.parametrize("d,group", FORMATS)
+@pytest.mark.parametrize("kind", ["spread", "steps", "large", "nan"])
+def test_write_ranges(d, group, kind):
+    """Rows of every magnitude, with elements far below their row's largest;
+    rows of a few distinct values, full of ties; values that saturate; a NaN,
+    which counts as zero for the others and has any code."""
+    n, heads = 96, 2
+    g = torch.Generator().manual_seed(d + group)
+    x = ref.keys(4, n, heads, d).float()
+    if kind == "spread":
+        x *= torch.exp2(-torch.randint(0, 18, (n, heads, d), generator=g).float())
+        x *= torch.exp2(8 - torch.arange(n) / 4).view(n, 1, 1)
+    elif kind == "steps":
+        x = torch.randint(-15, 16, (n, heads, d), generator=g).float()
+        x *= torch.exp2(-(torch.arange(n) // 4).float()).view(n, 1, 1)
+    elif kind == "large":
+        x *= torch.exp2(torch.randint(-4, 18, (n, heads, d), generator=g).float())
+    x = x.to(torch.bfloat16)
+    nan = torch.zeros(x.shape, dtype=torch.bool)
+    if kind == "nan":
+        nan = torch.rand(x.shape, generator=g) < 0.02
+    table, pages = ref.random_batch(1, [n], 16)
+    cache = new_cache(pages, heads, d, 16, group)
+    want = images(cache)
+    held, _ = ref.places([n], [n], table, 16)
+    expect_written(cache, x.masked_fill(nan, 0), held, "k", *want["k"])
+    expect_written(cache, -x.masked_fill(nan, 0), held, "v", *want["v"])
+    x = x.masked_fill(nan, float("nan"))
+    wq().kv4_write(x.cuda(), -x.cuda(), cache, ints([n]), ints(table))
+    got = images(cache)
+    for kind in "kv":
+        assert np.array_equal(got[kind][1], want[kind][1])
+        u, w = (ref.unpack(i[kind][0], kind) for i in (got, want))
+        for row, _, _, page, slot in held:
+            same = (u[page, :, slot] == w[page, :, slot]) | nan[row].numpy()
+            assert same.all(), (kind, row)
+
+
 def test_write_matches_the_weight_quantizer():
     """The cache's codes are those of wq_quantize for the same values."""
     n, heads, d, group = 64, 4, 128, 32

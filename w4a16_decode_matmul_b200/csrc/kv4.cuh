@@ -153,9 +153,15 @@ __device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t bmax2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t bmin2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -198,74 +204,63 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // Sixteen values of a group that LANES adjacent lanes share -> the two words
 // of their codes, scale and zero.
 //
-// The codes are round-half-even of the exact quotients x / s.  With inv within
-// 2^-23 of 1/s (relative), x inv is within 15 * 2^-22 < 2^-18 of x / s, so
-// rounding it decides every code whose x inv is farther than 2^-16 from a
-// half-integer; a lane with a nearer one decides its codes by the exact rule.
-// Outside that window no code needs a clamp: (hi - lo) / s <= 15, and
-// rint(hi/s) + rint(-lo/s) can be 16 only when both quotients are
+// The codes are round-half-even of the exact quotients x / s of the binary16
+// values x; the range is found on the bfloat16, whose order rounding keeps.
+// With inv within 2^-23 of 1/s (relative), x inv is within 15 * 2^-22 < 2^-18
+// of x / s, so rounding it decides every code whose x inv is farther than 2^-16
+// from a half-integer; a lane with a nearer one, or a NaN, decides its codes by
+// the exact rule.  Outside that window no code needs a clamp: (hi - lo) / s <=
+// 15, and rint(hi/s) + rint(-lo/s) can be 16 only when both quotients are
 // half-integers.
 template <int LANES>
 __device__ __forceinline__ uint2 quantize16(const uint4 (&raw)[2], float* scale, float* zero) {
-  uint32_t h[8];
+  const uint32_t b[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w,
+                         raw[1].x, raw[1].y, raw[1].z, raw[1].w};
   uint32_t hi = 0u, lo = 0u;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    h[4 * i] = to_format(raw[i].x);
-    h[4 * i + 1] = to_format(raw[i].y);
-    h[4 * i + 2] = to_format(raw[i].z);
-    h[4 * i + 3] = to_format(raw[i].w);
-  }
-#pragma unroll
   for (int i = 0; i < 8; ++i) {
-    hi = hmax2(hi, h[i]);
-    lo = hmin2(lo, h[i]);
+    hi = bmax2(hi, b[i]);
+    lo = bmin2(lo, b[i]);
   }
   // (hi, -lo) in one word
-  hi = hmax2(hi, __byte_perm(hi, hi, 0x1032));
-  lo = hmin2(lo, __byte_perm(lo, lo, 0x1032));
+  hi = bmax2(hi, __byte_perm(hi, hi, 0x1032));
+  lo = bmin2(lo, __byte_perm(lo, lo, 0x1032));
   uint32_t ends = __byte_perm(hi, lo ^ 0x80008000u, 0x5410);
 #pragma unroll
-  for (int m = 1; m < LANES; m *= 2) ends = hmax2(ends, __shfl_xor_sync(0xffffffffu, ends, m));
-  const float2 end = half2_to_float2(ends);
+  for (int m = 1; m < LANES; m *= 2) ends = bmax2(ends, __shfl_xor_sync(0xffffffffu, ends, m));
+  const float2 end = half2_to_float2(to_format(ends));
   const float range = __fadd_ru(end.x, end.y);
   const float s = range > 0.f ? range_scale(range) : 1.f;
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
   const float z = fminf(rint_quotient(end.y, s, inv), 15.f);
-  // 1.5 * 2^23 + z: the sum below lands on the integers, its low bits the code
+  // 1.5 * 2^23 + z: the sum below lands on the integers, its low byte the code
   const float shift = 12582912.f + z;
-  uint32_t u[16];
-  float off = 0.f;  // the largest distance from the rounded value
+  uint32_t u[8];    // low byte: the codes of a pair
+  float off = 0.f;  // the largest distance from the rounded value, or NaN
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float2 x = half2_to_float2(h[i]);
+    const float2 x = half2_to_float2(to_format(b[i]));
     const float2 a = fma2(x, make_float2(inv, inv), make_float2(shift, shift));
     // shift - a is minus the rounded quotient, exactly
     const float2 r = fma2(a, make_float2(-1.f, -1.f), make_float2(shift, shift));
     const float2 e = fma2(x, make_float2(inv, inv), r);
-    off = fmaxf(off, fmaxf(fabsf(e.x), fabsf(e.y)));
-    u[2 * i] = __float_as_uint(a.x);
-    u[2 * i + 1] = __float_as_uint(a.y);
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(off) : "f"(e.x), "f"(e.y), "f"(off));
+    u[i] = __float_as_uint(a.y) * 16u + __float_as_uint(a.x);
   }
   uint32_t word[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t bytes[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      bytes[k] = (u[8 * i + 2 * k] & 15u) | ((u[8 * i + 2 * k + 1] << 4) & 0xf0u);
-    word[i] = __byte_perm(__byte_perm(bytes[0], bytes[1], 0x0040),
-                          __byte_perm(bytes[2], bytes[3], 0x0040), 0x5410);
-  }
-  if (off > 0.5f - 0x1p-16f) {
+  for (int i = 0; i < 2; ++i)
+    word[i] = __byte_perm(__byte_perm(u[4 * i], u[4 * i + 1], 0x0040),
+                          __byte_perm(u[4 * i + 2], u[4 * i + 3], 0x0040), 0x5410);
+  if (!(off <= 0.5f - 0x1p-16f)) {
     word[0] = word[1] = 0u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float2 x = half2_to_float2(h[i]);
-      const float a = fminf(fmaxf(rint_quotient(x.x, s, inv) + z, 0.f), 15.f);
-      const float b = fminf(fmaxf(rint_quotient(x.y, s, inv) + z, 0.f), 15.f);
-      word[i >> 2] |= (uint32_t(int(a)) | (uint32_t(int(b)) << 4)) << (8 * (i & 3));
+      const float2 f = half2_to_float2(to_format(b[i]));
+      const float even = fminf(fmaxf(rint_quotient(f.x, s, inv) + z, 0.f), 15.f);
+      const float odd = fminf(fmaxf(rint_quotient(f.y, s, inv) + z, 0.f), 15.f);
+      word[i >> 2] |= (uint32_t(int(even)) | (uint32_t(int(odd)) << 4)) << (8 * (i & 3));
     }
   }
   *scale = s;
@@ -315,7 +310,11 @@ __device__ __forceinline__ uint4 values8(uint32_t word, __half2 meta) {
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-constexpr int kRowWarps = 8;       // warps of a CTA of the two row kernels
+// Warps of a CTA of the two row kernels: one, so that a row's place on the SM is
+// free as soon as the row is done (against 8, 4 and 2 a CTA at the same
+// registers, the sizes below: read 144,000 rows 79 us, 92, 86, 82; write 32,768
+// and read them back 85, 88, 88, 88).
+constexpr int kRowWarps = 1;
 constexpr int kRowIterations = 2;  // pieces of 16 keys and 16 values per lane
 
 // The place of a lane in the rows: it takes elements 16 lambda .. of every
@@ -349,12 +348,15 @@ struct RowLane {
 // 4 D read and D + 8 D/G written per row and head.
 //
 // Measured on B200: 32,768 rows of 8 heads of 128 (134 MB in, 36 MB out, groups
-// of 128) 58 us, 2.9 TB/s; bound by instructions (17 per value and lane, issue
-// 61 %, ALU 54 %).  With one value per instruction throughout and 8 values a
-// lane (twice the work per group) it was 115 us; with packed ranges but 8
-// values a lane 83.  Four CTAs per SM (64 registers) against three: 58 and 62.
+// of 128) 54 us, 3.2 TB/s.  Instructions (17 per value and lane, issue 59 %) and
+// the wait of each row for its page and its values share the time: quotients
+// formed from the bfloat16, several instructions a pair fewer, measured no
+// faster (written and read back 87.4 and 88.2 us).  With
+// one value per instruction throughout and 8 values a lane (twice the work per
+// group) it was 115 us; with packed ranges but 8 values a lane 83.  64 registers
+// (32 warps an SM) against 80: 57 and 62.
 template <int D, int G>
-__global__ void __launch_bounds__(kRowWarps * 32, 4)
+__global__ void __launch_bounds__(kRowWarps * 32, 32)
     write_kernel(const __nv_bfloat16* __restrict__ K, int64_t k_stride,
                  const __nv_bfloat16* __restrict__ V, int64_t v_stride, Cache cache, Batch batch,
                  int chunks) {
@@ -405,9 +407,9 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4)
 
 // The values of cached rows, bfloat16 [rows][kv_heads][D].  Rows of a
 // sequence that hold no token get zeros; rows of no sequence are left alone.
-// HBM bound, six bytes written for each read: 460 MB in 91 us (5.0 TB/s).
+// HBM bound, six bytes written for each read: 460 MB in 79 us (5.8 TB/s).
 template <int D, int G>
-__global__ void __launch_bounds__(kRowWarps * 32, 4)
+__global__ void __launch_bounds__(kRowWarps * 32, 32)
     read_kernel(Cache cache, Batch batch, __nv_bfloat16* __restrict__ K,
                 __nv_bfloat16* __restrict__ V, int chunks) {
   using L = RowLane<D, G>;
