@@ -242,8 +242,12 @@ __device__ __forceinline__ int64_t row_offset(const AttnParams& p, int row0, int
 }
 
 // The reference of a row that has seen no token yet: finite, so that no
-// difference of two is NaN, and below any score that binary32 tells apart.
-constexpr float kNoReference = -1e30f;
+// difference of two is NaN, and no larger than any finite score.
+constexpr float kNoReference = -0x1.fffffep127f;
+
+// Scores (base 2) from which a binary32 reference cannot be trusted to be
+// within a few units of the exact one: half a step is 1 here, 16 at 2^28.
+constexpr float kFarScore = 0x1p24f;
 
 // The segment of unit q, which is `rem` units behind the first of sequence b,
 // and q's place in it.

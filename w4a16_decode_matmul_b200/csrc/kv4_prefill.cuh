@@ -28,7 +28,7 @@
 // halved, and the softmax doubles it back.  Weights: 2^(S - m) rounded to
 // binary16; the reference m is raised only when the weights of a step would add
 // up to more than 2^15, then so that the largest becomes 2^7 (and the row's
-// output is rescaled).
+// output is rescaled), or 1 where scores reach 2^24.
 // Products, sums and statistics in binary32.
 //
 // Work split.  Where the blocks of 256 rows do not fill half of the SMs, each
@@ -543,58 +543,96 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
     const int least = __reduce_min_sync(0xffffffffu, my_limit);
     float m = kNoReference, l = 0.f;
     bool ok = true;
-    // One step's weights, formed with the row's present reference.  Where their
-    // sum passes 2^15 (always in the first step) the reference is raised so that
-    // the largest becomes 2^7 (and the sum 2^14 at most), the output so far is
-    // put on it, and the step's weights are formed again; they go over the
-    // scores in tensor memory only then.  (Following the largest packed weight
-    // instead of the sum cost 5 % of the kernel's time.)
-    auto weights = [&](auto masked_tag, int j) {
+    bool far = false;  // of the warp: a row's reference is kFarScore or more
+    // One step's weights, formed with the row's present reference; they go over
+    // the scores in tensor memory.  They do not, and the function returns true,
+    // where some row's sum passes 2^15 (*over for this thread's row) or the step is
+    // a halved one.  (Following the largest packed weight instead of the sum cost
+    // 5 % of the kernel's time; asking for `wide` before the scores are loaded 1 %.)
+    auto weights = [&](auto masked_tag, int seen, bool wide, bool* over) {
       constexpr bool kMasked = decltype(masked_tag)::value;
-      const bool wide = *reinterpret_cast<volatile int*>(&ctl->wide[j & 3]) != 0;
-      const float cj = wide ? 2.f * c : c;     // halved keys
-      const float shift = wide ? 1.f : 0.f;    // halved values take doubled weights
-      const int seen = my_limit - token0 - j * kTile;  // columns below `seen` count
       uint32_t w[4][16];
-      float2 sum;
-      while (true) {
-        float v[2][32];  // each chunk is loaded while the one before it is computed
-        tmem_ld32(s_tmem, v[0]);
-        const float ref = shift - m;
-        sum = make_float2(0.f, 0.f);
+      float v[2][32];  // each chunk is loaded while the one before it is computed
+      tmem_ld32(s_tmem, v[0]);
+      float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          float(&x)[32] = v[ch & 1];
-          tmem_wait_ld();
-          if (ch < 3) tmem_ld32(s_tmem + 32 * (ch + 1), v[(ch + 1) & 1]);
+      for (int ch = 0; ch < 4; ++ch) {
+        float(&x)[32] = v[ch & 1];
+        tmem_wait_ld();
+        if (ch < 3) tmem_ld32(s_tmem + 32 * (ch + 1), v[(ch + 1) & 1]);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float2 e = fma2(make_float2(x[2 * k], x[2 * k + 1]), make_float2(cj, cj),
-                            make_float2(ref, ref));
-            e.x = exp2_approx(e.x);
-            e.y = exp2_approx(e.y);
-            if (kMasked) {
-              if (32 * ch + 2 * k >= seen) e.x = 0.f;
-              if (32 * ch + 2 * k + 1 >= seen) e.y = 0.f;
-            }
-            sum = add2(sum, e);
-            w[ch][k] = pack_half2(e.x, e.y);
+        for (int k = 0; k < 16; ++k) {
+          float2 e = fma2(make_float2(x[2 * k], x[2 * k + 1]), make_float2(c, c),
+                          make_float2(-m, -m));
+          e.x = exp2_approx(e.x);
+          e.y = exp2_approx(e.y);
+          if (kMasked) {
+            if (32 * ch + 2 * k >= seen) e.x = 0.f;
+            if (32 * ch + 2 * k + 1 >= seen) e.y = 0.f;
           }
+          sum = add2(sum, e);
+          w[ch][k] = pack_half2(e.x, e.y);
         }
-        // no weight is larger than the sum (a NaN raises nothing)
-        const bool over = sum.x + sum.y > 32768.f;
-        if (!__any_sync(0xffffffffu, over)) break;
+      }
+      // no weight is larger than the sum (a NaN raises nothing)
+      *over = sum.x + sum.y > 32768.f;
+      if (__builtin_expect(__any_sync(0xffffffffu, *over || wide), 0)) return true;
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) tmem_st16(s_tmem + 16 * ch, w[ch]);
+      l += sum.x + sum.y;
+      return false;
+    };
+    // A step that `weights` did not do: the first, one whose sums passed 2^15, one
+    // of halved keys and values, and all of a warp with far scores.  Rows with
+    // `over` get a higher reference, so that the largest weight becomes 2^7, and
+    // the output so far is put on it; then the weights are formed, once, whatever
+    // they add up to: nothing here repeats.  `compared` (the same for the warp, whose
+    // lanes load tensor memory together): whether `over` is known.
+    //
+    // weights() subtracts the reference from the exact product.  From kFarScore on
+    // a rounded reference can be many units off the largest exact product, so there
+    // it is the largest rounded product itself, and the warp's products are rounded
+    // before the subtraction, as in a softmax of binary32 scores: the largest weight
+    // is 1.
+    auto rare_step = [&](int j, int seen, bool wide, bool compared, bool over) {
+      const float cj = wide ? 2.f * c : c;  // halved keys
+      // exponents of 32 tokens' weights; -inf where masked
+      auto exponents = [&](int ch, float (&x)[32]) {
+        tmem_ld32(s_tmem + 32 * ch, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float e = fmaf(far ? __fmul_rn(x[k], cj) : x[k], far ? 1.f : cj, -m);
+          x[k] = 32 * ch + k < seen ? e : -INFINITY;
+        }
+      };
+      if (!compared) {
+        // as weights() would have found it; halved values double their weights
+        float sum = 0.f;
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ++ch) {
+          float x[32];
+          exponents(ch, x);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) sum += exp2_approx(x[k]);
+        }
+        over = sum > 16384.f;
+      }
+      if (__any_sync(0xffffffffu, over)) {
         float top = -INFINITY;
 #pragma unroll 1
-        for (int k = 0; k < kTile; k += 16) {
-          float x[16];
-          gemm2::tmem_ld16(s_tmem + k, x);
+        for (int ch = 0; ch < 4; ++ch) {
+          float x[32];
+          tmem_ld32(s_tmem + 32 * ch, x);
           tmem_wait_ld();
 #pragma unroll
-          for (int n = 0; n < 16; ++n)
-            if (!kMasked || k + n < seen) top = fmaxf(top, x[n]);
+          for (int k = 0; k < 32; ++k)
+            if (32 * ch + k < seen) top = fmaxf(top, x[k]);
         }
-        const float next = over ? top * cj - 7.f : m;
+        const float product = __fmul_rn(top, cj);
+        float next = fabsf(product) >= kFarScore ? product : fmaf(top, cj, -7.f);
+        if (!over || top == -INFINITY) next = m;  // a row that sees nothing has no reference
+        far = far || __any_sync(0xffffffffu, next != m && fabsf(next) >= kFarScore);
         const float f = exp2_approx(m - next);
         m = next;
         l *= f;
@@ -614,18 +652,39 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
           }
         }
       }
+      const float doubled = wide ? 2.f : 1.f;
+      float2 sum = make_float2(0.f, 0.f);
+      // 32 scores make 16 words: those of chunk ch lie before the scores of ch + 1
+#pragma unroll 1
+      for (int ch = 0; ch < 4; ++ch) {
+        float x[32];
+        exponents(ch, x);
+        uint32_t w[16];
 #pragma unroll
-      for (int ch = 0; ch < 4; ++ch) tmem_st16(s_tmem + 16 * ch, w[ch]);
-      l += wide ? 0.5f * (sum.x + sum.y) : sum.x + sum.y;
+        for (int k = 0; k < 16; ++k) {
+          const float2 e = make_float2(exp2_approx(x[2 * k]), exp2_approx(x[2 * k + 1]));
+          sum = add2(sum, e);
+          w[k] = pack_half2(e.x * doubled, e.y * doubled);
+        }
+        tmem_st16(s_tmem + 16 * ch, w);
+      }
+      l += sum.x + sum.y;
     };
+    bool usual = false;  // neither the first step nor far scores
     for (int j = 0; j < steps; ++j) {
       ok = __all_sync(0xffffffffu, wait(&ctl->s_full[i], uint32_t(j) & 1u));
       if (!ok) break;
       tc_fence_after();
-      if (token0 + (j + 1) * kTile > least)
-        weights(std::true_type{}, j);
-      else
-        weights(std::false_type{}, j);
+      const bool wide = *reinterpret_cast<volatile int*>(&ctl->wide[j & 3]) != 0;
+      const int seen = my_limit - token0 - j * kTile;  // columns below `seen` count
+      bool over = true, rare = true;
+      if (usual)
+        rare = token0 + (j + 1) * kTile > least ? weights(std::true_type{}, seen, wide, &over)
+                                                : weights(std::false_type{}, seen, wide, &over);
+      if (__builtin_expect(rare, 0)) {
+        rare_step(j, seen, wide, j == 0 || (usual && !wide), over);
+        usual = !far;
+      }
       if (!ok) break;
       tmem_wait_st();
       tc_fence_before();
