@@ -39,10 +39,12 @@ def known(cache, table, n, p):
     w8 = np.repeat(np.einsum("tn,nhg->thg", p, s) * 8, g, -1)
     # many rows: half a step of each weight and of each value
     wabs = np.einsum("tn,nhd->thd", p, np.abs(values))
-    # weights below binary16's normal range (see ref.attention), and binary32
+    # weights below binary16's normal range (see ref.attention); scores below
+    # 2^12, of which the few-row kernel rounds those in steps with masked tokens by
+    # 2^-13 (ln 2 of that in the weight, in the numerator and the sum); and binary32
     # sums over the tokens, the zeros' correction being as large as the codes'
     tiny = n * 8 * 2.0 ** -25 * s.max(0).max(-1)[None, :, None]
-    sums = n * 2.0 ** -23 * (2 * w8 + wabs)
+    sums = n * 2.0 ** -23 * (2 * w8 + wabs) + 2.0 ** -12 * wabs
     return out, np.maximum(2.0 ** -11 * w8, 2.0 ** -10 * 1.01 * wabs) + tiny + sums
 
 
@@ -60,7 +62,7 @@ def levels_softmax(level, top, rows):
 
 def far_rows(rows, exponent, heads, gqa, d, pattern):
     """Queries whose base-2 scores with the pattern are about +-2^exponent."""
-    sign = torch.tensor([1.0, -1.0, -1.0, 1.0, 1.0]).repeat(rows)[:rows]
+    sign = torch.tensor([1.0, -1.0, -1.0, 1.0, 1.0]).roll(exponent).repeat(rows)[:rows]
     size = torch.exp2(exponent - 4 - torch.arange(rows) % 3)     # d/sqrt(d) log2(e) is about 2^4
     q = (sign * size * (128 / d) ** 0.5).view(-1, 1, 1) * pattern.sign().expand(rows, heads * gqa, d)
     return q, sign.numpy()
@@ -68,10 +70,12 @@ def far_rows(rows, exponent, heads, gqa, d, pattern):
 
 MANY = [(64, 32, 2, 4, 40, 300), (128, 64, 2, 4, 70, 300), (128, 128, 1, 2, 150, 700),
         (64, 64, 90, 3, 20, 200)]        # the last without splits
+FEW = [(64, 32, 2, 4, 1, 300), (128, 64, 2, 4, 3, 300), (128, 32, 2, 8, 2, 1200),
+       (128, 128, 1, 1, 1, 5000), (64, 64, 100, 20, 1, 200)]    # the last in blocks of rows
 
 
-@pytest.mark.parametrize("d,group,heads,gqa,rows,n", MANY)
-@pytest.mark.parametrize("exponent", [18, 23, 24, 25, 28, 29, 31, 34, 40, 100])
+@pytest.mark.parametrize("d,group,heads,gqa,rows,n", MANY + FEW)
+@pytest.mark.parametrize("exponent", [13, 18, 23, 24, 25, 28, 29, 31, 34, 40, 100])
 def test_scores_of_any_size(d, group, heads, gqa, rows, n, exponent):
     g = torch.Generator().manual_seed(exponent)
     pattern = torch.where(torch.rand(d, generator=g) < 0.5, -1.0, 1.0)
@@ -93,7 +97,7 @@ def test_scores_of_any_size(d, group, heads, gqa, rows, n, exponent):
     ref.check(got, out, bound)
 
 
-@pytest.mark.parametrize("d,group,heads,gqa,rows,n", MANY)
+@pytest.mark.parametrize("d,group,heads,gqa,rows,n", MANY + FEW)
 @pytest.mark.parametrize("exponent", [27, 29, 33])
 def test_any_large_scores_give_a_mean_of_values(d, group, heads, gqa, rows, n, exponent):
     """Scores without structure: whatever they round to, an output is a mean
@@ -110,7 +114,7 @@ def test_any_large_scores_give_a_mean_of_values(d, group, heads, gqa, rows, n, e
     assert wq().get_device_error() == 0
 
 
-@pytest.mark.parametrize("d,group,heads,gqa,rows,n", MANY)
+@pytest.mark.parametrize("d,group,heads,gqa,rows,n", MANY + FEW)
 @pytest.mark.parametrize("score", [0.0, 5.3, 33.3, 61.7, -1000.1, 70000.7, 2.0 ** 26])
 @pytest.mark.parametrize("large", ["k", "v", "kv"])
 def test_equal_scores_beside_the_largest_values(d, group, heads, gqa, rows, n, score, large):

@@ -21,6 +21,11 @@
 // s'_{t,g}, so that W_t fits binary16 whatever the values' scale, and
 // it is raised only when a W_t would pass 2^15 (a warp vote), then so that the
 // largest becomes 2^7: weights down to 2^-21 of the largest keep all their bits.
+// The exponent is the exact product less m, as long as m is small: from 2^12 on a
+// warp rounds every product first, as its steps with masked tokens always do, so
+// that equal scores have equal weights in all steps; and from 2^24 on, where the
+// rounding of m could take a weight out of binary16's range, m is the largest
+// rounded score itself, and the largest W_t the value scale.
 // Scores, sums, statistics and outputs are held in binary32.
 //
 // Work split.  A unit is 32 tokens of one (sequence, block of rows, head); the
@@ -249,6 +254,10 @@ constexpr float kNoReference = -0x1.fffffep127f;
 // within a few units of the exact one: half a step is 1 here, 16 at 2^28.
 constexpr float kFarScore = 0x1p24f;
 
+// References (base 2) from which the warp-level kernel rounds its products: a
+// product of this size rounds by 2^-12.
+constexpr float kLargeScore = 0x1p12f;
+
 // The segment of unit q, which is `rem` units behind the first of sequence b,
 // and q's place in it.
 template <int ROWS>
@@ -458,7 +467,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
     uint32_t q[NT][2 * NC][2];
     float sum_q[NT][NG][2], q_scale[NT][2], m[NT][2], l[NT][2], zc[NT][NG][2];
     int limit[NT][2], seen_by_all = 0;
-    bool fresh = true, alive = true;
+    bool fresh = true, alive = true, large = false;
 
     // lane group g holds tokens pi(g) and pi(g) + 8 of each 16: with this
     // order of the tokens the value loads below touch every bank group
@@ -473,7 +482,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
       if (to_copy > 0) copy_unit(st == 0 ? NS - 1 : st - 1);
       bool raise = fresh;
       if (fresh) {
-        fresh = false;
+        fresh = large = false;
         seen_by_all = cs.len - cs.rows + p.by_gqa(cs.rb * ROWS) + 1;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -547,7 +556,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
       const unsigned char* const stage = ring + st * C::kStageBytes;
       const int tok0 = unit * kUnit;
       // tokens that every row of the block sees need no mask
-      const bool masked = tok0 + kUnit > seen_by_all;
+      bool masked = large || tok0 + kUnit > seen_by_all;
 
 #pragma unroll
       for (int h0 = 0; h0 < 2; h0 += TILES) {
@@ -657,6 +666,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
               for (int k = 1; k < NG; ++k) top = fmaxf(top, meta_pair(vm[h][i][k]).x);
               lw[h][i] = log2_approx(top);
             }
+          float next[NT][2], most_next = 0.f;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -669,9 +679,37 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
 #pragma unroll
               for (int d = 4; d < 32; d *= 2)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-              const float next = fmaxf(m[nt][c], top - 7.f);
-              const float f = exp2_approx(m[nt][c] - next);
-              m[nt][c] = next;
+              next[nt][c] = fmaxf(m[nt][c], top - 7.f);
+              if (next[nt][c] != kNoReference) most_next = fmaxf(most_next, fabsf(next[nt][c]));
+            }
+          if (__any_sync(0xffffffffu, most_next >= kLargeScore)) {
+            // rounded products from here to the segment's end
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float high = -INFINITY;
+#pragma unroll
+                for (int h = 0; h < TILES; ++h)
+#pragma unroll
+                  for (int i = 0; i < 4; i += 2) {
+                    x[h][nt][c + i] = __fmul_rn(x[h][nt][c + i], scale[nt][c]);
+                    high = fmaxf(high, x[h][nt][c + i]);
+                  }
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2)
+                  high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
+                scale[nt][c] = 1.f;
+                if (fabsf(next[nt][c]) >= kFarScore) next[nt][c] = fmaxf(m[nt][c], high);
+              }
+            masked = large = true;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float f = exp2_approx(m[nt][c] - next[nt][c]);
+              m[nt][c] = next[nt][c];
               l[nt][c] *= f;
 #pragma unroll
               for (int k = 0; k < NG; ++k) zc[nt][k][c] *= f;
