@@ -152,3 +152,35 @@ def test_references_that_rise_row_by_row():
     out, bound = reference(q, cache, [n], [rows], table, d ** -0.5)
     ref.check(got, out, bound)
     assert wq().get_device_error() == 0
+
+
+@pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128)])
+@pytest.mark.parametrize("what", ["key beside values", "value beside keys", "value of a later token",
+                                  "key of a later token", "every seventh"])
+def test_values_near_binary16s_smallest_beside_its_largest(d, group, what):
+    """A key or a value that can stand for more than binary16's largest does
+    not change what the tokens around it hold, nor the other one of its token."""
+    heads, gqa, rows, n, at = 2, 4, 200, 400, 300
+    k, v = ref.keys(1, n, heads, d, 1.0).float(), ref.keys(2, n, heads, d, 1.0).float()
+    q = ref.keys(3, rows, heads * gqa, d, 1.0).float()
+    large = torch.where(ref.keys(4, n, heads, d, 1.0).float() < 0, -60000.0, 60000.0)
+    if what == "key beside values":
+        k[at], v = large[at], v * 2.0 ** -20
+        q *= 2.0 ** -8             # its score does not take every weight
+    elif what == "value beside keys":
+        k, v[at], q = k * 2.0 ** -20, large[at], q * 2.0 ** 20
+    elif what == "value of a later token":
+        v = v * 2.0 ** -20
+        v[at] = large[at]
+    elif what == "key of a later token":
+        k, q = k * 2.0 ** -20, q * 2.0 ** 20
+        k[at] = large[at]
+    else:
+        v[::7], k[3::7] = large[::7], large[3::7]
+        q *= 2.0 ** -14
+    cache, table = cached(d, group, k, v)
+    q = q.to(torch.bfloat16).cuda()
+    got = wq().kv4_attention(q, cache, ints([n]), ints(table))
+    assert wq().get_device_error() == 0
+    out, bound = reference(q, cache, [n], [rows], table, d ** -0.5)
+    ref.check(got, out, bound)

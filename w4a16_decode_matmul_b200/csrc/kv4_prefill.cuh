@@ -23,9 +23,12 @@
 // Roundings.  Queries: scaled by a power of two per row to [2^14, 2^15) and
 // rounded to binary16 (exact for every bfloat16 within 2^-21 of the row's
 // largest).  Keys and values: s (u - z) rounded once to binary16 (2^-11 half
-// step; exact where it is subnormal, since s is a multiple of 2^-24).  A tile
-// with a scale of 4368 or more, the only ones whose values can pass 65504, is
-// halved, and the softmax doubles it back.  Weights: 2^(S - m) rounded to
+// step; exact where it is subnormal, since s is a multiple of 2^-24).  A token's
+// key or value with a scale of 4368 or more, the only ones that can pass 65504, is
+// halved, and the softmax doubles its score or its weight; what other groups of
+// that key or value hold near binary16's smallest rounds by 2^-24 then.  Nothing
+// that is not halved is touched by it, in the same tile or otherwise.  Weights:
+// 2^(S - m) rounded to
 // binary16; the reference m is raised only when the weights of a step would add
 // up to more than 2^15, then so that the largest becomes 2^7 (and the row's
 // output is rescaled), or 1 where scores reach 2^24.
@@ -75,6 +78,15 @@ constexpr int kPrefillThreads = 16 * 32;  // four warpgroups; the last has one b
 // Scales from 4368 on (the binary16 after 4364) can stand for values past
 // 65504: 15 * 4364 = 65460.
 constexpr uint32_t kWideScaleBits = 0x6C44u;
+
+// Whether a token's key or value is halved (scale bits in the low halves).
+template <int NG>
+__device__ __forceinline__ bool is_wide(const uint32_t (&meta)[NG]) {
+  uint32_t most = meta[0];
+#pragma unroll
+  for (int k = 1; k < NG; ++k) most = hmax2(most, meta[k]);
+  return (most & 0xffffu) >= kWideScaleBits;
+}
 constexpr int kMmaWarp = 12;
 
 struct PrefillParams {
@@ -104,7 +116,8 @@ struct PrefillControl {
   uint64_t k_full[2], k_free[2], v_full[2], v_free[2];  // stages
   uint64_t s_full[2], p_full[2], o_done[2];              // tiles
   uint64_t mma_done;
-  int wide[4];  // of the last steps: values are halved
+  int wide[4];             // of the last steps: a key or a value is halved
+  uint8_t halved[4][2][16];  // which: a bit a token, of keys and of values
   uint32_t tmem;
   int abort;
 };
@@ -178,34 +191,42 @@ __device__ __forceinline__ bool named_barrier_or(uint32_t id, uint32_t threads, 
   return r != 0;
 }
 
-// Codes of four tokens, 32 apart, to a tile's values s (u - z), halved if wide,
-// in the unpack's order; `put` are the places of the first token's chunks.
-template <int NC, int NG, bool VALUES>
+// Codes of four tokens, 32 apart, to a tile's values s (u - z), in the unpack's
+// order; `put` are the places of the first token's chunks.  WIDE: the tile has
+// tokens to halve; the exact u - z is halved, so that the product is rounded once.
+template <int NC, int NG, bool VALUES, bool WIDE>
 __device__ __forceinline__ void expand_tile(const uint32_t (&code)[4][NC],
                                             const uint32_t (&meta)[4][NG],
-                                            const uint32_t (&put)[NC], uint32_t tile, bool wide) {
+                                            const uint32_t (&put)[NC], uint32_t tile) {
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
+    const uint32_t f = WIDE && is_wide(meta[u]) ? 0x38003800u : 0x3C003C00u;  // 1/2 or 1
     uint32_t s2 = 0, lo = 0, hi = 0;
 #pragma unroll
     for (int k = 0; k < NC; ++k) {
       if (k % (NC / NG) == 0) {
         const uint32_t m = meta[u][k / (NC / NG)], z2 = __byte_perm(m, m, 0x3232);
         s2 = __byte_perm(m, m, 0x1010);
-        if (wide) s2 = hmul2(s2, 0x38003800u);  // 1/2
-        lo = hadd2(z2, 0x64006400u);            // 1024 + z
-        hi = hsub2(0xD400D400u, z2);            // -(64 + z)
+        lo = hadd2(z2, 0x64006400u);  // 1024 + z
+        hi = hsub2(0xD400D400u, z2);  // -(64 + z)
+        if (WIDE) lo = hmul2(lo, f), hi = hmul2(hi, f);
       }
       // a value word is made of the halfwords of two g (see kv4.cuh)
       const uint32_t word = VALUES ? __byte_perm(code[u][k / 2], code[u][NC / 2 + k / 2],
                                                  (k & 1) ? 0x7632 : 0x5410)
                                    : code[u][k];
+      // u - z, times f, of the codes in the low and in the high nibbles of bytes
+      auto low = [&](uint32_t w) {
+        const uint32_t x = lop3_and_or(w, 0x000F000Fu, 0x64006400u);
+        return WIDE ? hfma2(x, f, lo ^ 0x80008000u) : hsub2(x, lo);
+      };
+      auto high = [&](uint32_t w) {
+        const uint32_t x = lop3_and_or(w, 0x00F000F0u, 0x64006400u);
+        return hfma2(x, WIDE ? hmul2(f, 0x2C002C00u) : 0x2C002C00u, hi);
+      };
       const uint32_t w8 = word >> 8;
-      sts128(tile + put[k] + 4096u * u,
-             hmul2(hsub2(lop3_and_or(word, 0x000F000Fu, 0x64006400u), lo), s2),
-             hmul2(hfma2(lop3_and_or(word, 0x00F000F0u, 0x64006400u), 0x2C002C00u, hi), s2),
-             hmul2(hsub2(lop3_and_or(w8, 0x000F000Fu, 0x64006400u), lo), s2),
-             hmul2(hfma2(lop3_and_or(w8, 0x00F000F0u, 0x64006400u), 0x2C002C00u, hi), s2));
+      sts128(tile + put[k] + 4096u * u, hmul2(low(word), s2), hmul2(high(word), s2),
+             hmul2(low(w8), s2), hmul2(high(w8), s2));
     }
   }
 }
@@ -244,6 +265,157 @@ __device__ __forceinline__ bool find_block(const PrefillParams& p, int index, in
   const int rb = index - first_block(lo);
   out->row = rb * kBlockRows;
   return rb >= 0 && out->row < out->columns && out->columns >= p.min_columns;
+}
+
+// Waits for a phase; false once any role's wait has run out of time.
+__device__ __forceinline__ bool prefill_wait(PrefillControl* ctl, uint64_t* bar, uint32_t parity) {
+  volatile int* const abort_flag = &ctl->abort;
+  if (mbar_test_wait(bar, parity)) return true;
+  if (*abort_flag) return false;
+  if (!mbar_wait(bar, parity)) {
+    *abort_flag = 1;
+    return false;
+  }
+  return true;
+}
+
+// The softmax's state of a row, and of its warp: whether a row's reference is
+// kFarScore or more, and whether no wait has given up.
+struct RowState {
+  float m, l;
+  bool far, ok;
+};
+
+// A step that `weights` did not do: the first, one whose sums passed 2^15, one
+// with halved keys or values, and all of a warp with far scores.  Rows with
+// `over` get a higher reference, so that the largest weight becomes 2^7, and
+// the output so far is put on it; then the weights are formed, once, whatever
+// they add up to: nothing here repeats.  `compared` (the same for the warp, whose
+// lanes load tensor memory together): whether `over` is known.
+//
+// weights() subtracts the reference from the exact product.  From kFarScore on
+// a rounded reference can be many units off the largest exact product, so there
+// it is the largest rounded product itself, and the warp's products are rounded
+// before the subtraction, as in a softmax of binary32 scores: the largest weight
+// is 1.
+//
+// A function of its own, so that the usual path has the registers and the
+// instruction cache to itself (inlined, a prompt took 4 % longer).
+template <int D>
+__device__ __noinline__ RowState rare_step(RowState row, PrefillControl* ctl, uint32_t s_tmem,
+                                           uint32_t o_tmem, uint64_t* o_done, float c, int j,
+                                           int seen, bool wide, bool compared, bool over) {
+  // which of 32 tokens have halved keys (0) or values (1)
+  auto halved = [&](int kind, int ch) {
+    return *reinterpret_cast<volatile uint32_t*>(&ctl->halved[j & 3][kind][4 * ch]);
+  };
+  if (wide) {
+    // scores of halved keys, doubled where they are
+#pragma unroll 1
+    for (int k = 0; k < kTile / 16; ++k) {
+      const uint32_t bits = halved(0, k >> 1) >> (16 * (k & 1));
+      float x[16];
+      gemm2::tmem_ld16(s_tmem + 16 * k, x);
+      tmem_wait_ld();
+      uint32_t r[16];
+#pragma unroll
+      for (int n = 0; n < 16; ++n)
+        r[n] = __float_as_uint((bits >> n) & 1u ? 2.f * x[n] : x[n]);
+      tmem_st16(s_tmem + 16 * k, r);
+    }
+    tmem_wait_st();
+  }
+  // exponents of 32 tokens' weights; -inf where masked
+  auto exponents = [&](int ch, float (&x)[32]) {
+    tmem_ld32(s_tmem + 32 * ch, x);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float e = fmaf(row.far ? __fmul_rn(x[k], c) : x[k], row.far ? 1.f : c, -row.m);
+      x[k] = 32 * ch + k < seen ? e : -INFINITY;
+    }
+  };
+  if (!compared) {
+    // as in weights(); halved values will double their weights
+    float sum = 0.f;
+#pragma unroll 1
+    for (int ch = 0; ch < 4; ++ch) {
+      float x[32];
+      exponents(ch, x);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) sum += exp2_approx(x[k]);
+    }
+    over = sum > 16384.f;
+  }
+  if (__any_sync(0xffffffffu, over)) {
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int ch = 0; ch < 4; ++ch) {
+      float x[32];
+      tmem_ld32(s_tmem + 32 * ch, x);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (32 * ch + k < seen) top = fmaxf(top, x[k]);
+    }
+    const float product = __fmul_rn(top, c);
+    float next = fabsf(product) >= kFarScore ? product : fmaf(top, c, -7.f);
+    if (!over || top == -INFINITY) next = row.m;  // a row that sees nothing has no reference
+    row.far = row.far || __any_sync(0xffffffffu, next != row.m && fabsf(next) >= kFarScore);
+    const float f = exp2_approx(row.m - next);
+    row.m = next;
+    row.l *= f;
+    if (j > 0) {
+      row.ok = __all_sync(0xffffffffu, prefill_wait(ctl, o_done, uint32_t(j - 1) & 1u));
+      if (!row.ok) return row;
+      tc_fence_after();
+#pragma unroll 1
+      for (int k = 0; k < D / 16; ++k) {
+        float o[16];
+        gemm2::tmem_ld16(o_tmem + 16 * k, o);
+        tmem_wait_ld();
+        uint32_t r[16];
+#pragma unroll
+        for (int n = 0; n < 16; ++n) r[n] = __float_as_uint(o[n] * f);
+        tmem_st16(o_tmem + 16 * k, r);
+      }
+    }
+  }
+  float2 sum = make_float2(0.f, 0.f);
+  // 32 scores make 16 words: those of chunk ch lie before the scores of ch + 1
+#pragma unroll 1
+  for (int ch = 0; ch < 4; ++ch) {
+    float x[32];
+    exponents(ch, x);
+    uint32_t w[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float2 e = make_float2(exp2_approx(x[2 * k]), exp2_approx(x[2 * k + 1]));
+      sum = add2(sum, e);
+      w[k] = pack_half2(e.x, e.y);
+    }
+    tmem_st16(s_tmem + 16 * ch, w);
+  }
+  row.l += sum.x + sum.y;
+  if (wide) {
+    // weights of halved values, doubled
+    tmem_wait_st();
+#pragma unroll 1
+    for (int ch = 0; ch < 4; ++ch) {
+      const uint32_t bits = halved(1, ch);
+      float x[16];
+      gemm2::tmem_ld16(s_tmem + 16 * ch, x);
+      tmem_wait_ld();
+      uint32_t w[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        w[k] = hmul2(__float_as_uint(x[k]), ((bits >> (2 * k)) & 1u ? 0x4000u : 0x3C00u) |
+                                                ((bits >> (2 * k + 1)) & 1u ? 0x40000000u
+                                                                            : 0x3C000000u));
+      tmem_st16(s_tmem + 16 * ch, w);
+    }
+  }
+  return row;
 }
 
 template <int D, int G>
@@ -288,7 +460,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
       raw_smem + ((1024u - (smem_addr(raw_smem) & 1023u)) & 1023u);  // swizzle atoms
   auto* ctl = reinterpret_cast<PrefillControl*>(smem);
   static_assert(sizeof(PrefillControl) <= C::kOffQ, "");
-  volatile int* const abort_flag = &ctl->abort;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->q_full[i], 4);
@@ -301,7 +472,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
       mbar_init(&ctl->o_done[i], 1);
     }
     mbar_init(&ctl->mma_done, 1);
-    *abort_flag = 0;
+    *reinterpret_cast<volatile int*>(&ctl->abort) = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -316,16 +487,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&ctl->tmem);
 
-  // Waits for a phase; false once any role's wait has run out of time.
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (mbar_test_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (!mbar_wait(bar, parity)) {
-      *abort_flag = 1;
-      return false;
-    }
-    return true;
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return prefill_wait(ctl, bar, parity); };
 
   // Registers: 512 threads at 128; the softmax holds a step's scores and
   // weights.  2 * 128 * 176 + 128 * 104 + 128 * 56 = 65,536 = 512 * 128.
@@ -474,7 +636,21 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
       // after a wait that gave up, the loop only keeps the barrier's count
       ok = ok && __all_sync(0xffffffffu, wait(&ctl->k_free[stage], parity));
       if (!ok) continue;
-      expand_tile<NC, NG, false>(kc, km, put, k_tiles + stage * C::kTileBytes, wide);
+      if (wide) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t keys = __reduce_or_sync(0xffffffffu, is_wide(km[u]) ? 1u << perm : 0u),
+                         values = __reduce_or_sync(0xffffffffu, is_wide(vm[u]) ? 1u << perm : 0u);
+          if (lane == 0) {
+            auto* const to = reinterpret_cast<volatile uint8_t*>(&ctl->halved[j & 3][0][0]);
+            to[4 * u + warp - 8] = uint8_t(keys);
+            to[16 + 4 * u + warp - 8] = uint8_t(values);
+          }
+        }
+        expand_tile<NC, NG, false, true>(kc, km, put, k_tiles + stage * C::kTileBytes);
+      } else {
+        expand_tile<NC, NG, false, false>(kc, km, put, k_tiles + stage * C::kTileBytes);
+      }
       if (tid == 256) *reinterpret_cast<volatile int*>(&ctl->wide[j & 3]) = wide ? 1 : 0;
       fence_async_shared();
       __syncwarp();
@@ -483,7 +659,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
 
       ok = __all_sync(0xffffffffu, wait(&ctl->v_free[stage], parity));
       if (!ok) continue;
-      expand_tile<NC, NG, true>(vc, vm, put, v_tiles + stage * C::kTileBytes, wide);
+      if (wide)
+        expand_tile<NC, NG, true, true>(vc, vm, put, v_tiles + stage * C::kTileBytes);
+      else
+        expand_tile<NC, NG, true, false>(vc, vm, put, v_tiles + stage * C::kTileBytes);
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->v_full[stage]);
@@ -582,94 +761,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
       l += sum.x + sum.y;
       return false;
     };
-    // A step that `weights` did not do: the first, one whose sums passed 2^15, one
-    // of halved keys and values, and all of a warp with far scores.  Rows with
-    // `over` get a higher reference, so that the largest weight becomes 2^7, and
-    // the output so far is put on it; then the weights are formed, once, whatever
-    // they add up to: nothing here repeats.  `compared` (the same for the warp, whose
-    // lanes load tensor memory together): whether `over` is known.
-    //
-    // weights() subtracts the reference from the exact product.  From kFarScore on
-    // a rounded reference can be many units off the largest exact product, so there
-    // it is the largest rounded product itself, and the warp's products are rounded
-    // before the subtraction, as in a softmax of binary32 scores: the largest weight
-    // is 1.
-    auto rare_step = [&](int j, int seen, bool wide, bool compared, bool over) {
-      const float cj = wide ? 2.f * c : c;  // halved keys
-      // exponents of 32 tokens' weights; -inf where masked
-      auto exponents = [&](int ch, float (&x)[32]) {
-        tmem_ld32(s_tmem + 32 * ch, x);
-        tmem_wait_ld();
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const float e = fmaf(far ? __fmul_rn(x[k], cj) : x[k], far ? 1.f : cj, -m);
-          x[k] = 32 * ch + k < seen ? e : -INFINITY;
-        }
-      };
-      if (!compared) {
-        // as weights() would have found it; halved values double their weights
-        float sum = 0.f;
-#pragma unroll 1
-        for (int ch = 0; ch < 4; ++ch) {
-          float x[32];
-          exponents(ch, x);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) sum += exp2_approx(x[k]);
-        }
-        over = sum > 16384.f;
-      }
-      if (__any_sync(0xffffffffu, over)) {
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int ch = 0; ch < 4; ++ch) {
-          float x[32];
-          tmem_ld32(s_tmem + 32 * ch, x);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (32 * ch + k < seen) top = fmaxf(top, x[k]);
-        }
-        const float product = __fmul_rn(top, cj);
-        float next = fabsf(product) >= kFarScore ? product : fmaf(top, cj, -7.f);
-        if (!over || top == -INFINITY) next = m;  // a row that sees nothing has no reference
-        far = far || __any_sync(0xffffffffu, next != m && fabsf(next) >= kFarScore);
-        const float f = exp2_approx(m - next);
-        m = next;
-        l *= f;
-        if (j > 0) {
-          ok = __all_sync(0xffffffffu, wait(&ctl->o_done[i], uint32_t(j - 1) & 1u));
-          if (!ok) return;
-          tc_fence_after();
-#pragma unroll 1
-          for (int k = 0; k < D / 16; ++k) {
-            float o[16];
-            gemm2::tmem_ld16(o_tmem + 16 * k, o);
-            tmem_wait_ld();
-            uint32_t r[16];
-#pragma unroll
-            for (int n = 0; n < 16; ++n) r[n] = __float_as_uint(o[n] * f);
-            tmem_st16(o_tmem + 16 * k, r);
-          }
-        }
-      }
-      const float doubled = wide ? 2.f : 1.f;
-      float2 sum = make_float2(0.f, 0.f);
-      // 32 scores make 16 words: those of chunk ch lie before the scores of ch + 1
-#pragma unroll 1
-      for (int ch = 0; ch < 4; ++ch) {
-        float x[32];
-        exponents(ch, x);
-        uint32_t w[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float2 e = make_float2(exp2_approx(x[2 * k]), exp2_approx(x[2 * k + 1]));
-          sum = add2(sum, e);
-          w[k] = pack_half2(e.x * doubled, e.y * doubled);
-        }
-        tmem_st16(s_tmem + 16 * ch, w);
-      }
-      l += sum.x + sum.y;
-    };
     bool usual = false;  // neither the first step nor far scores
     for (int j = 0; j < steps; ++j) {
       ok = __all_sync(0xffffffffu, wait(&ctl->s_full[i], uint32_t(j) & 1u));
@@ -682,7 +773,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
         rare = token0 + (j + 1) * kTile > least ? weights(std::true_type{}, seen, wide, &over)
                                                 : weights(std::false_type{}, seen, wide, &over);
       if (__builtin_expect(rare, 0)) {
-        rare_step(j, seen, wide, j == 0 || (usual && !wide), over);
+        const RowState row =
+            rare_step<D>({m, l, far, ok}, ctl, s_tmem, o_tmem, &ctl->o_done[i], c, j, seen, wide,
+                         j == 0 || (usual && !wide), over);
+        m = row.m, l = row.l, far = row.far, ok = row.ok;
         usual = !far;
       }
       if (!ok) break;
