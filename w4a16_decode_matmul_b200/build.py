@@ -31,8 +31,8 @@ ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMPILE_FLAGS = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-rdc=true",
                  "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 # Units compiled as a whole program (no relocatable device code): register
-# reallocation between warpgroups is ignored in relocatable code.  They keep a
-# device status word of their own.
+# reallocation between warpgroups is ignored in relocatable code.  They get the
+# device status word's address as an argument.
 WHOLE_PROGRAM = {"k_kv4_prefill.cu"}
 LINK_FLAGS = [*ARCH, "-rdc=true", "-shared", "-Xcompiler", "-fPIC"]
 

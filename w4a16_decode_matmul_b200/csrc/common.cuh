@@ -13,7 +13,8 @@ namespace wq {
 
 // Device status word: 0 = fine; otherwise a wq_status code recorded by a
 // kernel (first writer wins).  Read and cleared by wq_get_device_error().
-// Defined once, in wq.cu (the library is linked as relocatable device code).
+// Defined once, in wq.cu (the library is linked as relocatable device code); a unit
+// compiled as a whole program gets its address as an argument instead.
 extern __device__ unsigned int g_status;
 
 // A wait gives up after this many nanoseconds of wall time (globaltimer).
@@ -21,8 +22,9 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr unsigned int kStatusTimeout = 5;                  // WQ_ERR_TIMEOUT
 constexpr unsigned int kStatusInternal = 4;                 // WQ_ERR_CUDA: inconsistent launch
 
-__device__ __forceinline__ void record_status(unsigned int code) {
-  atomicCAS(&g_status, 0u, code);
+__device__ __forceinline__ void record_status(unsigned int code,
+                                              unsigned int* word = &g_status) {
+  atomicCAS(word, 0u, code);
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -89,13 +91,14 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 
 // Wait for the phase with the given parity to complete; false (and the
 // status word set) if it has not completed within kWaitLimitNs.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
+                                          unsigned int* status = &g_status) {
   if (mbar_test_wait(bar, parity)) return true;
   const unsigned long long start = global_timer_ns();
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
     if (global_timer_ns() - start > kWaitLimitNs) {
-      record_status(kStatusTimeout);
+      record_status(kStatusTimeout, status);
       return false;
     }
   }

@@ -40,6 +40,7 @@ kv4::Batch device_batch(const wq_kv4_batch& b, int page_size) {
   d.rows = b.rows;
   d.rows_per_seq = b.row_starts ? 0 : b.rows / b.seqs;
   d.max_len = int(std::min<int64_t>(int64_t(b.table_width) * page_size, 0x7fffff00));
+  d.status = status_address();
   return d;
 }
 
@@ -73,9 +74,11 @@ struct WriteOp {
   static cudaError_t run(const void* K, int64_t ks, const void* V, int64_t vs,
                          const wq_kv4_cache& c, const wq_kv4_batch& b, cudaStream_t s) {
     if (row_warps(c, b.rows) >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    const kv4::Batch batch = device_batch(b, c.page_size);
+    if (batch.status == nullptr) return cudaErrorInitializationError;
     kv4::write_kernel<D, G><<<row_ctas(c, b.rows), kv4::kRowWarps * 32, 0, s>>>(
         static_cast<const __nv_bfloat16*>(K), ks, static_cast<const __nv_bfloat16*>(V), vs,
-        device_cache(c), device_batch(b, c.page_size), row_chunks(c));
+        device_cache(c), batch, row_chunks(c));
     return cudaGetLastError();
   }
 };
@@ -85,8 +88,10 @@ struct ReadOp {
   static cudaError_t run(const wq_kv4_cache& c, const wq_kv4_batch& b, void* K, void* V,
                          cudaStream_t s) {
     if (row_warps(c, b.rows) >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    const kv4::Batch batch = device_batch(b, c.page_size);
+    if (batch.status == nullptr) return cudaErrorInitializationError;
     kv4::read_kernel<D, G><<<row_ctas(c, b.rows), kv4::kRowWarps * 32, 0, s>>>(
-        device_cache(c), device_batch(b, c.page_size), static_cast<__nv_bfloat16*>(K),
+        device_cache(c), batch, static_cast<__nv_bfloat16*>(K),
         static_cast<__nv_bfloat16*>(V), row_chunks(c));
     return cudaGetLastError();
   }
@@ -185,6 +190,7 @@ cudaError_t run_kv4_attention(const void* Q, int64_t q_stride, int q_heads,
   kv4::AttnParams p = {};
   p.cache = device_cache(cache);
   p.batch = device_batch(batch, cache.page_size);
+  if (p.batch.status == nullptr) return cudaErrorInitializationError;
   p.Q = static_cast<const __nv_bfloat16*>(Q);
   p.q_stride = q_stride;
   p.O = static_cast<__nv_bfloat16*>(O);
@@ -204,9 +210,8 @@ cudaError_t run_kv4_attention(const void* Q, int64_t q_stride, int q_heads,
   const int64_t bound = max_rows > 0 ? max_rows : batch.rows;
   p.max_columns = 1 << 30;
   if (bound * p.gqa > kFew && prefer_prefill(batch, cache.kv_heads, p.gqa, dev.sms)) {
-    kv4::PrefillParams pp = {p, kFew + 1, status_address(),
+    kv4::PrefillParams pp = {p, kFew + 1,
                              prefill_splits(batch, cache.kv_heads, p.gqa, dev.sms), p.partial};
-    if (pp.status == nullptr) return cudaErrorInitializationError;
     const cudaError_t e = run_kv4_prefill(cache.head_dim, cache.group, pp, s);
     if (e != cudaSuccess || !batch.row_starts) return e;
     p.max_columns = kFew;  // a ragged batch may hold both kinds

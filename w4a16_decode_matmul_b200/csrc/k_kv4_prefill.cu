@@ -1,10 +1,10 @@
 // k_kv4_prefill.cu -- launcher of the attention kernel for many rows.
 //
 // Compiled as a whole program: the kernel moves registers between its
-// warpgroups, which is ignored in relocatable device code.  So this unit has a
-// device status word of its own (outside relocatable code the declaration in
-// common.cuh defines it), and the kernel hands what it holds to the library's.
-#define g_status g_prefill_status
+// warpgroups, which is ignored in relocatable device code.  So the unit cannot name
+// the library's device status word (common.cuh's declaration would define another):
+// the kernel gets its address with the batch.
+#define g_status g_unused_status
 #include "kv4_host.h"
 #include "kv4_prefill.cuh"
 

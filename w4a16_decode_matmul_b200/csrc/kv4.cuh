@@ -49,6 +49,7 @@ struct Batch {
   int rows;
   int rows_per_seq;
   int max_len;  // tokens that a row of the page table can hold
+  unsigned int* status;  // the library's device status word
 };
 
 constexpr unsigned int kStatusInvalid = 1;  // WQ_ERR_INVALID_ARG
@@ -66,14 +67,14 @@ __device__ __forceinline__ Sequence load_sequence(const Batch& p, int b) {
     const int r0 = p.row_starts[b], r1 = p.row_starts[b + 1];
     s.row0 = min(max(r0, 0), p.rows);
     const int end = min(max(r1, s.row0), p.rows);
-    if (s.row0 != r0 || end != r1) record_status(kStatusInvalid);
+    if (s.row0 != r0 || end != r1) record_status(kStatusInvalid, p.status);
     s.rows = end - s.row0;
   } else {
     s.row0 = b * p.rows_per_seq;
     s.rows = p.rows_per_seq;
   }
   if (s.len > p.max_len) {
-    record_status(kStatusInvalid);
+    record_status(kStatusInvalid, p.status);
     s.len = p.max_len;
   }
   s.len = max(s.len, 0);
@@ -85,7 +86,7 @@ __device__ __forceinline__ Sequence load_sequence(const Batch& p, int b) {
 __device__ __forceinline__ int64_t load_page(const Batch& p, const Cache& c, int b, int pos) {
   const int64_t page = p.page_table[int64_t(b) * p.table_stride + (pos >> c.page_shift)];
   if (page < 0 || page >= c.pages) {
-    record_status(kStatusInvalid);
+    record_status(kStatusInvalid, p.status);
     return -1;
   }
   return page;

@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
       __syncwarp();
       if (sub < subs) {
         if (uint32_t(pf_page) >= uint32_t(p.cache.pages)) {
-          record_status(kStatusInvalid);
+          record_status(kStatusInvalid, p.batch.status);
           pf_page = 0;  // any page of the cache can be read
         }
         const int64_t token =

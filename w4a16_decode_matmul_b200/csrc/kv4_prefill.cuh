@@ -92,7 +92,6 @@ constexpr int kMmaWarp = 12;
 struct PrefillParams {
   AttnParams a;
   int min_columns;  // sequences with fewer rows times heads are left alone
-  unsigned* status;  // the library's device status word
   int splits;        // CTAs that share the tokens of a block (see below)
   float* partial;    // with splits > 1: one slot for each CTA of the grid
 };
@@ -268,11 +267,12 @@ __device__ __forceinline__ bool find_block(const PrefillParams& p, int index, in
 }
 
 // Waits for a phase; false once any role's wait has run out of time.
-__device__ __forceinline__ bool prefill_wait(PrefillControl* ctl, uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool prefill_wait(PrefillControl* ctl, uint64_t* bar, uint32_t parity,
+                                             unsigned int* status) {
   volatile int* const abort_flag = &ctl->abort;
   if (mbar_test_wait(bar, parity)) return true;
   if (*abort_flag) return false;
-  if (!mbar_wait(bar, parity)) {
+  if (!mbar_wait(bar, parity, status)) {
     *abort_flag = 1;
     return false;
   }
@@ -304,7 +304,8 @@ struct RowState {
 template <int D>
 __device__ __noinline__ RowState rare_step(RowState row, PrefillControl* ctl, uint32_t s_tmem,
                                            uint32_t o_tmem, uint64_t* o_done, float c, int j,
-                                           int seen, bool wide, bool compared, bool over) {
+                                           int seen, bool wide, bool compared, bool over,
+                                           unsigned int* status) {
   // which of 32 tokens have halved keys (0) or values (1)
   auto halved = [&](int kind, int ch) {
     return *reinterpret_cast<volatile uint32_t*>(&ctl->halved[j & 3][kind][4 * ch]);
@@ -366,7 +367,7 @@ __device__ __noinline__ RowState rare_step(RowState row, PrefillControl* ctl, ui
     row.m = next;
     row.l *= f;
     if (j > 0) {
-      row.ok = __all_sync(0xffffffffu, prefill_wait(ctl, o_done, uint32_t(j - 1) & 1u));
+      row.ok = __all_sync(0xffffffffu, prefill_wait(ctl, o_done, uint32_t(j - 1) & 1u, status));
       if (!row.ok) return row;
       tc_fence_after();
 #pragma unroll 1
@@ -431,15 +432,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
   const int cta = int(gridDim.x) - 1 - int(blockIdx.x);
   const int split = cta % p.splits, group = cta / p.splits;
   const int head = group % heads;
-  // what this unit's status word holds goes to the library's
-  auto report = [&] {
-    if (tid == 0 && *reinterpret_cast<volatile unsigned*>(&g_status) != 0u)
-      atomicCAS(p.status, 0u, atomicExch(&g_status, 0u));
-  };
-  if (!find_block(p, group / heads, lane, &block)) {
-    report();
-    return;
-  }
+  if (!find_block(p, group / heads, lane, &block)) return;
   const Sequence& seq = block.s;
   const int rows = min(kBlockRows, block.columns - block.row);
   const int tiles = rows > kTile ? 2 : 1;
@@ -447,10 +440,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
   const int limit = seq.len - seq.rows + p.a.by_gqa(block.row + rows - 1) + 1;
   const int all_steps = (max(limit, 0) + kTile - 1) / kTile;
   const int splits = max(1, min(p.splits, all_steps));
-  if (split >= splits) {
-    report();
-    return;
-  }
+  if (split >= splits) return;
   // this CTA's steps, and its first token
   const int step0 = int(int64_t(split) * all_steps / splits);
   const int steps = int(int64_t(split + 1) * all_steps / splits) - step0;
@@ -487,7 +477,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&ctl->tmem);
 
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return prefill_wait(ctl, bar, parity); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return prefill_wait(ctl, bar, parity, p.a.batch.status);
+  };
 
   // Registers: 512 threads at 128; the softmax holds a step's scores and
   // weights.  2 * 128 * 176 + 128 * 104 + 128 * 56 = 65,536 = 512 * 128.
@@ -552,7 +544,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
       // all of this CTA's products are done before tensor memory is freed
       if (leader) tc_commit(&ctl->mma_done);
       __syncwarp();
-      mbar_wait(&ctl->mma_done, 0);
+      mbar_wait(&ctl->mma_done, 0, p.a.batch.status);
     }
   } else if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
@@ -596,7 +588,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
         for (int k = 0; k < NG; ++k) km[u][k] = 0u;
         if (pos >= limit) continue;
         if (uint32_t(page[u]) >= uint32_t(cache.pages)) {
-          record_status(kStatusInvalid);
+          record_status(kStatusInvalid, p.a.batch.status);
           page[u] = 0;  // any page of the cache can be read
         }
         at[u] = ((int64_t(page[u]) * heads + head) << cache.page_shift) + (pos & page_mask);
@@ -775,7 +767,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
       if (__builtin_expect(rare, 0)) {
         const RowState row =
             rare_step<D>({m, l, far, ok}, ctl, s_tmem, o_tmem, &ctl->o_done[i], c, j, seen, wide,
-                         j == 0 || (usual && !wide), over);
+                         j == 0 || (usual && !wide), over, p.a.batch.status);
         m = row.m, l = row.l, far = row.far, ok = row.ok;
         usual = !far;
       }
@@ -886,7 +878,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
   }
-  report();
 }
 
 }  // namespace kv4
