@@ -274,9 +274,10 @@ typedef struct wq_kv4_cache {
  *
  * All arrays are int32 in device memory and read when the call runs, so a
  * captured graph may be replayed with other contents.  What they hold is
- * checked there: a row range outside 0 .. rows, a length above table_width *
- * page_size and, for a token the call needs, a page outside 0 .. pages - 1
- * record WQ_ERR_INVALID_ARG in the device status word; the results of that
+ * checked there: a row range outside 0 .. rows or that ends before it begins, a
+ * length above table_width * page_size (of any sequence, with rows or without)
+ * and, for a token the call needs, a page outside 0 .. pages - 1 record
+ * WQ_ERR_INVALID_ARG in the device status word; the results of that
  * sequence are unspecified and nothing outside the caller's buffers is
  * touched.  Rows behind the last sequence (row_starts[seqs] .. rows - 1) are
  * left as they were. */

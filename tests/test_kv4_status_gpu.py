@@ -80,3 +80,27 @@ def test_a_process_may_capture_its_first_calls(rows):
     run = subprocess.run([sys.executable, "-c", CAPTURE_FIRST.format(root=ROOT, rows=rows)],
                          capture_output=True, text=True, timeout=300, cwd=ROOT)
     assert run.returncode == 0 and "captured" in run.stdout, run.stderr[-2000:]
+
+
+@pytest.mark.parametrize("lens,starts", [
+    ([40, 40], [0, 4, 10]),              # a range behind the last row
+    ([40, 40], [-2, 0, 4]),              # one before the first
+    ([40, 40, 40], [0, 4, 2, 4]),        # one that ends before it begins
+    ([40, 10 ** 6, 40], [0, 2, 2, 4]),   # a sequence without rows, too long
+    ([40] * 4999 + [10 ** 6], [0, 4] + [4] * 4999)])
+def test_sequences_without_a_row_of_the_call_are_checked(lens, starts):
+    """In every call: rows 0 .. 3 belong to other sequences than the bad one."""
+    d, group, heads, page, rows = 64, 32, 2, 16, 4
+    table = np.tile(np.arange(3, dtype=np.int32), (len(lens), 1))
+    cache = new_cache(3, heads, d, page, group)
+    fill(cache, [40], table[:1])
+    x = ref.keys(1, rows, heads, d).cuda()
+    good = ints([40] * len(lens)), ints(table), ints([0] + [rows] * len(lens))
+    bad = ints(lens), ints(table), ints(starts)
+    calls = [lambda b: wq().kv4_write(x, x, cache, *b), lambda b: wq().kv4_read(cache, *b, rows=rows),
+             lambda b: wq().kv4_attention(x, cache, *b)]
+    for call in calls:
+        call(bad)
+        assert wq().get_device_error() == 1
+        call(good)
+        assert wq().get_device_error() == 0

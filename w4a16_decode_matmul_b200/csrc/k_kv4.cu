@@ -65,18 +65,23 @@ int row_chunks(const wq_kv4_cache& c) {
 
 int64_t row_warps(const wq_kv4_cache& c, int rows) { return int64_t(rows) * row_chunks(c); }
 
-unsigned row_ctas(const wq_kv4_cache& c, int rows) {
-  return unsigned((row_warps(c, rows) + kv4::kRowWarps - 1) / kv4::kRowWarps);
+// And some that check the sequences, 32 a warp and at once.
+constexpr int kCheckWarps = 1024;
+
+unsigned row_ctas(const wq_kv4_cache& c, const wq_kv4_batch& b) {
+  const int64_t warps =
+      row_warps(c, b.rows) + std::min<int64_t>((int64_t(b.seqs) + 31) / 32, kCheckWarps);
+  return unsigned((warps + kv4::kRowWarps - 1) / kv4::kRowWarps);
 }
 
 template <int D, int G>
 struct WriteOp {
   static cudaError_t run(const void* K, int64_t ks, const void* V, int64_t vs,
                          const wq_kv4_cache& c, const wq_kv4_batch& b, cudaStream_t s) {
-    if (row_warps(c, b.rows) >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if (row_warps(c, b.rows) + kCheckWarps >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     const kv4::Batch batch = device_batch(b, c.page_size);
     if (batch.status == nullptr) return cudaErrorInitializationError;
-    kv4::write_kernel<D, G><<<row_ctas(c, b.rows), kv4::kRowWarps * 32, 0, s>>>(
+    kv4::write_kernel<D, G><<<row_ctas(c, b), kv4::kRowWarps * 32, 0, s>>>(
         static_cast<const __nv_bfloat16*>(K), ks, static_cast<const __nv_bfloat16*>(V), vs,
         device_cache(c), batch, row_chunks(c));
     return cudaGetLastError();
@@ -87,10 +92,10 @@ template <int D, int G>
 struct ReadOp {
   static cudaError_t run(const wq_kv4_cache& c, const wq_kv4_batch& b, void* K, void* V,
                          cudaStream_t s) {
-    if (row_warps(c, b.rows) >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if (row_warps(c, b.rows) + kCheckWarps >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     const kv4::Batch batch = device_batch(b, c.page_size);
     if (batch.status == nullptr) return cudaErrorInitializationError;
-    kv4::read_kernel<D, G><<<row_ctas(c, b.rows), kv4::kRowWarps * 32, 0, s>>>(
+    kv4::read_kernel<D, G><<<row_ctas(c, b), kv4::kRowWarps * 32, 0, s>>>(
         device_cache(c), batch, static_cast<__nv_bfloat16*>(K),
         static_cast<__nv_bfloat16*>(V), row_chunks(c));
     return cudaGetLastError();
