@@ -18,6 +18,10 @@ namespace {
 
 namespace kv4 = wq::kv4;
 
+// Test hooks of the timeout path (wq_internal_kv4_timeout_test).
+int g_kv4_stuck_cta = -1;
+unsigned int g_kv4_wait_ns = unsigned(wq::kWaitLimitNs);
+
 kv4::Cache device_cache(const wq_kv4_cache& c) {
   kv4::Cache d = {};
   d.k_codes = static_cast<uint8_t*>(c.k_codes);
@@ -206,6 +210,8 @@ cudaError_t run_kv4_attention(const void* Q, int64_t q_stride, int q_heads,
   p.arrived = static_cast<unsigned*>(workspace);
   p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
                                        round_up(kCounterBytes, 256));
+  p.test_stuck_cta = g_kv4_stuck_cta;
+  p.wait_ns = g_kv4_wait_ns;
   const int64_t max_rows = batch.row_starts ? batch.max_rows : batch.rows / batch.seqs;
   // Sequences with up to 16 rows (times the heads of a group) stream the cache
   // through the warp-level kernel.  With more there is the choice between that
@@ -226,3 +232,17 @@ cudaError_t run_kv4_attention(const void* Q, int64_t q_stride, int q_heads,
 }
 
 }  // namespace wqh
+
+extern "C" {
+
+// Test hook, not part of the public ABI: make the timeout path of the attention
+// kernels run.  In CTA `stuck_cta` (-1: none) the first warp's copies, or the
+// keys of the kernel for many rows, never count as complete; the waits of every
+// CTA give up after `wait_ns` nanoseconds (0 restores the default limit).  Every
+// copy and product that the CTA starts ends by itself long before.
+void wq_internal_kv4_timeout_test(int stuck_cta, unsigned int wait_ns) {
+  wqh::g_kv4_stuck_cta = stuck_cta;
+  wqh::g_kv4_wait_ns = wait_ns > 0 ? wait_ns : unsigned(wq::kWaitLimitNs);
+}
+
+}  // extern "C"

@@ -84,6 +84,11 @@ struct AttnParams {
   int max_columns;    // sequences with more rows times gqa are another kernel's
   FastDiv by_gqa;
   float scale_log2;   // softmax scale times log2 e
+  // Test hooks of the timeout path (set only through an internal export): the
+  // CTA whose copies never count as complete (-1: none; they are made all the
+  // same), and the limit of the kernels' waits, in nanoseconds.
+  int test_stuck_cta;
+  unsigned int wait_ns;
   unsigned* arrived;  // [kMaxCtas][kMaxRows] zero counters
   float* partial;     // [2 kMaxCtas][piece]
 };
@@ -311,6 +316,17 @@ __device__ __forceinline__ int find_segment(const AttnParams& p, const AttnContr
   return segment_at<ROWS>(p, b, seq, rem, q, out);
 }
 
+// Waits, for a limited time each, for the `copies` stages of a ring from `st` on.
+static __device__ __noinline__ void wait_for_copies(uint64_t* full, int stages, int st,
+                                                    uint32_t parity, int copies,
+                                                    unsigned int* status,
+                                                    unsigned long long limit_ns) {
+  for (; copies > 0; --copies) {
+    mbar_wait(&full[st], parity, status, limit_ns);
+    if (++st == stages) st = 0, parity ^= 1u;
+  }
+}
+
 template <int D, int G, int NT, int WARPS, int TILES>
 __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p) {
   using C = AttnConfig<D, G, NT, WARPS>;
@@ -459,6 +475,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
     };
     read_page();
     if (kAhead) load_queries(0);
+    // (at the kernel's start, where the parameters are not in the constant cache
+    // yet, this comparison cost 0.4 us)
+    if (int(blockIdx.x) == p.test_stuck_cta && tid == 0) mbar_expect_tx(&ctl->full[0][0], 16u);
     for (int s = 0; s < NS - 1; ++s)
       if (to_copy > 0) copy_unit(s);
 
@@ -467,7 +486,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
     uint32_t q[NT][2 * NC][2];
     float sum_q[NT][NG][2], q_scale[NT][2], m[NT][2], l[NT][2], zc[NT][NG][2];
     int limit[NT][2], seen_by_all = 0;
-    bool fresh = true, alive = true, large = false;
+    bool fresh = true, large = false;
 
     // lane group g holds tokens pi(g) and pi(g) + 8 of each 16: with this
     // order of the tokens the value loads below touch every bank group
@@ -552,7 +571,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
         }
       }
 
-      if (alive) alive = mbar_wait(&ctl->full[warp][st], parity);
+      if (!__all_sync(0xffffffffu, mbar_wait(&ctl->full[warp][st], parity, p.batch.status,
+                                             p.wait_ns))) {
+        // given up: no more copies, and none in flight when the warp's ring is used
+        // for a piece or the CTA ends
+        wait_for_copies(ctl->full[warp], NS, st, parity, left - to_copy, p.batch.status, p.wait_ns);
+        break;
+      }
       const unsigned char* const stage = ring + st * C::kStageBytes;
       const int tok0 = unit * kUnit;
       // tokens that every row of the block sees need no mask

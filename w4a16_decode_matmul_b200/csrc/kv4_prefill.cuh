@@ -268,11 +268,11 @@ __device__ __forceinline__ bool find_block(const PrefillParams& p, int index, in
 
 // Waits for a phase; false once any role's wait has run out of time.
 __device__ __forceinline__ bool prefill_wait(PrefillControl* ctl, uint64_t* bar, uint32_t parity,
-                                             unsigned int* status) {
+                                             unsigned int* status, unsigned long long limit_ns) {
   volatile int* const abort_flag = &ctl->abort;
   if (mbar_test_wait(bar, parity)) return true;
   if (*abort_flag) return false;
-  if (!mbar_wait(bar, parity, status)) {
+  if (!mbar_wait(bar, parity, status, limit_ns)) {
     *abort_flag = 1;
     return false;
   }
@@ -305,7 +305,8 @@ template <int D>
 __device__ __noinline__ RowState rare_step(RowState row, PrefillControl* ctl, uint32_t s_tmem,
                                            uint32_t o_tmem, uint64_t* o_done, float c, int j,
                                            int seen, bool wide, bool compared, bool over,
-                                           unsigned int* status) {
+                                           unsigned int* status,
+                                           unsigned long long limit_ns) {
   // which of 32 tokens have halved keys (0) or values (1)
   auto halved = [&](int kind, int ch) {
     return *reinterpret_cast<volatile uint32_t*>(&ctl->halved[j & 3][kind][4 * ch]);
@@ -367,7 +368,8 @@ __device__ __noinline__ RowState rare_step(RowState row, PrefillControl* ctl, ui
     row.m = next;
     row.l *= f;
     if (j > 0) {
-      row.ok = __all_sync(0xffffffffu, prefill_wait(ctl, o_done, uint32_t(j - 1) & 1u, status));
+      row.ok = __all_sync(0xffffffffu,
+                          prefill_wait(ctl, o_done, uint32_t(j - 1) & 1u, status, limit_ns));
       if (!row.ok) return row;
       tc_fence_after();
 #pragma unroll 1
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->q_full[i], 4);
-      mbar_init(&ctl->k_full[i], 4);
+      mbar_init(&ctl->k_full[i], cta == p.a.test_stuck_cta ? 5 : 4);
       mbar_init(&ctl->v_full[i], 4);
       mbar_init(&ctl->k_free[i], 1);
       mbar_init(&ctl->v_free[i], 1);
@@ -478,7 +480,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&ctl->tmem);
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return prefill_wait(ctl, bar, parity, p.a.batch.status);
+    return prefill_wait(ctl, bar, parity, p.a.batch.status, p.a.wait_ns);
   };
 
   // Registers: 512 threads at 128; the softmax holds a step's scores and
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
       // all of this CTA's products are done before tensor memory is freed
       if (leader) tc_commit(&ctl->mma_done);
       __syncwarp();
-      mbar_wait(&ctl->mma_done, 0, p.a.batch.status);
+      mbar_wait(&ctl->mma_done, 0, p.a.batch.status, p.a.wait_ns);
     }
   } else if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
@@ -767,7 +769,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
       if (__builtin_expect(rare, 0)) {
         const RowState row =
             rare_step<D>({m, l, far, ok}, ctl, s_tmem, o_tmem, &ctl->o_done[i], c, j, seen, wide,
-                         j == 0 || (usual && !wide), over, p.a.batch.status);
+                         j == 0 || (usual && !wide), over, p.a.batch.status, p.a.wait_ns);
         m = row.m, l = row.l, far = row.far, ok = row.ok;
         usual = !far;
       }
