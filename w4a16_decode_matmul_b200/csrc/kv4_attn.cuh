@@ -993,6 +993,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
         }
         before = __shfl_sync(0xffffffffu, before, 0);
         if (before != unsigned(c1 - c0)) continue;
+        __syncwarp();  // lane 0's fence holds for the other lanes' loads
         // every CTA of the segment has brought its row
         if (lane == 0) p.arrived[c0 * kMaxRows + rl] = 0u;
         constexpr int kAtOnce = 8;

@@ -842,6 +842,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const Prefi
         }
         before = __shfl_sync(0xffffffffu, before, 0);
         if (before == unsigned(splits - 1)) {
+          __syncwarp();  // lane 0's fence holds for the other lanes' loads
           if (lane == 0) *arrived = 0u;
           float top = kNoReference;
           for (int c = 0; c < splits; ++c) top = fmaxf(top, __ldcg(stats(c)));
