@@ -184,3 +184,17 @@ def test_values_near_binary16s_smallest_beside_its_largest(d, group, what):
     assert wq().get_device_error() == 0
     out, bound = reference(q, cache, [n], [rows], table, d ** -0.5)
     ref.check(got, out, bound)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 40])
+@pytest.mark.parametrize("scale", [3.4e38, -3.4e38, 2.4e38, 1e-45, 0.0])
+def test_queries_of_zero_give_the_mean_at_every_scale(rows, scale):
+    d, group, heads, gqa, n = 64, 32, 2, 4, 300
+    cache, table = cached(d, group, ref.keys(1, n, heads, d), ref.keys(2, n, heads, d, 1.0))
+    q = torch.zeros(rows, heads * gqa, d, dtype=torch.bfloat16, device="cuda")
+    got = wq().kv4_attention(q, cache, ints([n]), ints(table), scale=scale)
+    p = np.zeros((rows, n))
+    for i in range(rows):
+        p[i, :n - rows + i + 1] = 1 / (n - rows + i + 1)
+    out, bound = known(cache, table, n, p)
+    ref.check(got, np.repeat(out, gqa, 1), np.repeat(bound, gqa, 1))

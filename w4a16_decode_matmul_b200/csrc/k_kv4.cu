@@ -1,6 +1,7 @@
 // k_kv4.cu -- launchers of the 4-bit key/value cache's kernels: rows in,
 // rows out, and attention of a few rows per sequence.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "kv4_host.h"
@@ -206,7 +207,9 @@ cudaError_t run_kv4_attention(const void* Q, int64_t q_stride, int q_heads,
   p.o_stride = o_stride;
   p.gqa = q_heads / cache.kv_heads;
   p.by_gqa = fast_div(uint32_t(p.gqa));
-  p.scale_log2 = float(double(scale) * 1.4426950408889634);
+  // finite for every finite scale: an infinite one would make NaN of scores of zero
+  p.scale_log2 = float(std::clamp(double(scale) * 1.4426950408889634, -double(FLT_MAX),
+                                  double(FLT_MAX)));
   p.arrived = static_cast<unsigned*>(workspace);
   p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
                                        round_up(kCounterBytes, 256));
