@@ -329,12 +329,24 @@ size_t wq_kv4_attention_workspace_bytes(void);
  * codes and never written to memory in 16 bits.  Q and O bfloat16
  * [rows][q_heads][head_dim], heads contiguous, row strides in elements;
  * q_heads a multiple of kv_heads; scale finite.  A row that sees no token
- * gets zeros.  Products are of exact codes with binary16 operands (queries
- * scaled by a power of two per row; a weight times its value scale within
- * 2^-11, or 2^-25 of the largest weight times the largest value scale of the
- * row's tokens where that is more), sums and softmax in binary32.
- * The same call gives the same bits; within the roundings above, a row's may
- * depend on the other rows of its call.  O may not overlap Q. */
+ * gets zeros.  scale * q_d * k_d and their sums have to stay inside binary32's
+ * range; scores of any size inside it are good to binary32's precision.
+ *
+ * Scores, sums and softmax are in binary32.  Rounded to binary16 are
+ *   - the queries, scaled by a power of two per row: exact within 2^-21 of the
+ *     row's largest element;
+ *   - in sequences with up to 16 rows times heads of a group, the weights times
+ *     their value scales: within 2^-11, or 2^-25 of the largest weight times the
+ *     largest value scale of the row's tokens where that is more.  Codes are
+ *     exact there;
+ *   - in sequences with more, either the same or, as the sizes of the call
+ *     decide, the weights (2^-11, or 2^-25 of the largest) and the keys and values
+ *     s (u - z) themselves: within 2^-11, exact below 2^-14, and within 2^-24
+ *     where another group of the same key or value has a scale of 4368 or more.
+ *     Rounded keys move a score by up to |scale| sum_d |q_d k_d| 2^-11, and a
+ *     weight by the exponential of that.
+ * The same call gives the same bits; within these roundings, a row's may depend
+ * on the other rows of its call and on max_rows.  O may not overlap Q. */
 wq_status wq_kv4_attention(const void *Q, int64_t q_stride, int32_t q_heads,
                            const wq_kv4_cache *cache, const wq_kv4_batch *batch, float scale,
                            void *O, int64_t o_stride, void *workspace, size_t workspace_bytes,

@@ -522,12 +522,13 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, seq_lens: torch.Tensor,
     [rows, q_heads, head_dim], over their sequences' cached tokens (the rows'
     own included: write them first).
 
-    ``max_rows`` bounds the rows of one sequence where ``row_starts`` is given
-    (it chooses the kernel; the result does not depend on it).  ``scale`` is
+    ``max_rows`` bounds the rows of one sequence where ``row_starts`` is given.
+    It takes part in the choice of the kernel, so results may differ with it
+    within the roundings that ``include/wq.h`` states.  ``scale`` is
     1/sqrt(head_dim) by default.  ``workspace`` is a ``kv4_workspace`` that the
     caller keeps, for instance in a captured graph; without it each call makes
-    its own.  Rows behind the last sequence are left as they were in ``out``
-    (zeros without it)."""
+    and zero-fills its own.  ``out`` may not overlap ``q``; rows behind the last
+    sequence are left as they were in it (zeros without it)."""
     _, _, heads, d, _ = cache._sizes
     index = cache.k_codes.get_device()
     rows, q_heads, qs = _kv4_rows(q, None, d, index, "q")

@@ -124,8 +124,9 @@ cudaError_t launch_attn(const kv4::AttnParams& p, cudaStream_t s, int sms) {
 // format needs (12 warps leave 168 a thread, 8 warps 255).  Measured on B200:
 //   one block of 8 columns, four groups: one tile 67 us, two (spilling) 118;
 //     one or two groups: 58 either way;
-//   two blocks of columns, head dim 128: 8 warps 46 us, 12 (spilling) 72; head
-//     dim 64: 12 warps 34 us, 8 37.
+//   two blocks of columns, groups of 64, head dim 128: 8 warps 46 us, 12
+//     (spilling) 72; head dim 64: 12 warps 34 us, 8 37.  Groups of 32 spill in
+//     both of the forms chosen (about 210 and 60 bytes).
 // A batch of up to four units of 32 tokens per warp takes 8 warps (one sequence
 // of 1,000 tokens, 8 kv heads: 10.1 us, with 12 warps 12.2; of 16,000: 16.7 and
 // 16.5); a larger one is limited by how many instructions are in flight (8
@@ -160,7 +161,11 @@ int prefill_splits(const wq_kv4_batch& b, int kv_heads, int gqa, int sms) {
 // Measured on B200 (head dim 128), time per cached token: 0.054 ns for each
 // block of 16 rows and head in the warp-level kernel (all SMs share them), 17.7
 // ns for each wave of CTAs of 256 rows in the tensor-memory kernel, divided by
-// its splits.
+// its splits.  The constants are used for head dim 64 too.  Where row_starts is
+// given the host does not know how the rows are spread, and every sequence counts
+// as a block of its own, also those of one row: a chunk of 512 rows beside 127
+// single tokens counts as eight waves, though it is one, and goes to the
+// warp-level kernel.
 bool prefer_prefill(const wq_kv4_batch& b, int kv_heads, int gqa, int sms) {
   const int64_t columns = int64_t(b.rows) * gqa;  // rows times heads of a group
   const int64_t each = b.row_starts ? 0 : columns / b.seqs;

@@ -323,8 +323,8 @@ __device__ __forceinline__ uint4 values8(uint32_t word, __half2 meta) {
 
 // Warps of a CTA of the two row kernels: one, so that a row's place on the SM is
 // free as soon as the row is done (against 8, 4 and 2 a CTA at the same
-// registers, the sizes below: read 144,000 rows 79 us, 92, 86, 82; write 32,768
-// and read them back 85, 88, 88, 88).
+// registers, kernels alone, back to back: read 85,514 rows 80 us, 92, 86, 82; write
+// 32,768 and read them back 85, 88, 88, 88).
 constexpr int kRowWarps = 1;
 constexpr int kRowIterations = 2;  // pieces of 16 keys and 16 values per lane
 
@@ -359,7 +359,7 @@ struct RowLane {
 // 4 D read and D + 8 D/G written per row and head.
 //
 // Measured on B200: 32,768 rows of 8 heads of 128 (134 MB in, 36 MB out, groups
-// of 128) 54 us, 3.2 TB/s.  Instructions (17 per value and lane, issue 59 %) and
+// of 128) 52 us, 3.2 TB/s.  Instructions (17 per value and lane, issue 60 %) and
 // the wait of each row for its page and its values share the time: quotients
 // formed from the bfloat16, several instructions a pair fewer, measured no
 // faster (written and read back 87.4 and 88.2 us).  With
@@ -422,7 +422,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 32)
 
 // The values of cached rows, bfloat16 [rows][kv_heads][D].  Rows of a
 // sequence that hold no token get zeros; rows of no sequence are left alone.
-// HBM bound, six bytes written for each read: 460 MB in 79 us (5.8 TB/s).
+// HBM bound, six bytes written for each read: 85,514 rows of 8 heads of 128 in
+// groups of 32 (460 MB) in 80 us alone (5.7 TB/s), 88 us a call through the binding.
 template <int D, int G>
 __global__ void __launch_bounds__(kRowWarps * 32, 32)
     read_kernel(Cache cache, Batch batch, __nv_bfloat16* __restrict__ K,

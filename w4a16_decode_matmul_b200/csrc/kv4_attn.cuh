@@ -42,12 +42,12 @@
 // deterministic.
 //
 // Measured on B200 (8 kv heads, 4 query heads each, D = 128, G = 64): 128
-// sequences of 2,048 to 8,192 tokens (763 MB) 207 us, 3.7 TB/s; the copies alone
-// with the same plan take 134 us.  What bounds it: about 390 warp instructions
+// sequences of 2,048 to 8,192 tokens (763 MB) 206 us, 3.7 TB/s; the copies alone
+// with the same plan take 134 us.  What bounds it: about 440 warp instructions
 // per 16 tokens and head, half of them unpack and products, the rest scores,
-// weights and copies, at 2.2 a cycle (issue 55 %, ALU 44 % of active cycles);
+// weights, copies and plan, at 2.2 a cycle (issue 56 %, ALU 44 % of active cycles);
 // short batches by the chain of dependent steps (sequence length, page number,
-// copy, one unit, two merges: 9.6 us for one sequence of 1,000 tokens).  Tried
+// copy, one unit, two merges: 10.1 us for one sequence of 1,000 tokens).  Tried
 // and slower: one warp that issues all copies (58 -> 69 us for a quarter of the
 // batch: its lanes serve few warps at a time), 16 warps (spills) and 8 warps
 // (latency shows) where there is work for 12; without effect: accumulators

@@ -45,7 +45,8 @@
 // while the other roles load shared and tensor memory; 1,024 alone) and
 // hand-overs, and the two tiles' softmax warps share their schedulers with the
 // dequantize warps.  Measured on B200: a prompt of 8,192 tokens, 32 query heads
-// on 8 kv heads (550 GFLOP) 560 us, 980 TFLOP/s.  (The form before, 580 us:
+// on 8 kv heads (550 GFLOP) 573 us alone, ten in a row (960 TFLOP/s), 615 to 630
+// in a longer run, whose clocks are lower (875-895).  (A form of 580 us alone:
 // without dequantizing 515, without softmax 430, without both 410.)  Tried and
 // slower: polling instead of suspended waits
 // (620-670), handing over half of the weights early (730), scores of half
