@@ -352,6 +352,224 @@ wq_status wq_kv4_attention(const void *Q, int64_t q_stride, int32_t q_heads,
                            void *O, int64_t o_stride, void *workspace, size_t workspace_bytes,
                            wq_stream_t stream);
 
+/* ---- pages chosen for each query ------------------------------------------
+ * Attention of a query over a few pages of a long cache: the first ones, the
+ * last ones, and those whose keys can have the largest scores with it.  The
+ * other tokens stay in the cache for later queries.
+ *
+ * Bounds of a page and kv head: the smallest and the largest value of every
+ * dimension among the page's keys (the values that the codes stand for), in 8
+ * bits on a grid of 2^e, e the smallest integer with 127 2^e >= the magnitude of
+ * all of them (0 where all are 0): floor(smallest / 2^e) and ceil(largest / 2^e).
+ * Two device buffers that the caller owns (16-byte aligned):
+ *   codes  int8 [pages][kv_heads][2][head_dim]: smallest, largest
+ *   grid   binary32 [pages][kv_heads]: 2^e
+ */
+typedef struct wq_kv4_bounds {
+    void *codes, *grid;
+} wq_kv4_bounds;
+
+/* The pages of every row and kv head, in the order of their tokens, and the
+ * tokens that they hold (device memory, caller-owned).  Bit for bit the same on
+ * every call. */
+typedef struct wq_kv4_selection {
+    int32_t max_pages;  /* pages of a list, 1 or more                          */
+    int32_t first;      /* a sequence's first pages that are always chosen     */
+    int32_t last;       /* the last, 1 or more: the row's own token is there   */
+    int32_t *lists;     /* [rows][kv_heads][max_pages]: pages of the cache, -1
+                         * behind the last                                     */
+    int32_t *lens;      /* [rows]: tokens up to the row's own in its pages; 0
+                         * for a row that sees none, -1 for one of no sequence */
+} wq_kv4_selection;
+
+/* Bounds of every page that the batch's rows are in (the tokens len - T .. len -
+ * 1 of each sequence), from the cache's codes of the page's tokens up to len -
+ * 1.  Call it after wq_kv4_write, with the same batch, before the rows' queries
+ * choose pages.  A page that two sequences share must hold the same number of
+ * tokens in both, or only one of them may have rows in it.  Errors as wq_kv4_read;
+ * a page outside the cache is recorded and skipped. */
+wq_status wq_kv4_update_bounds(const wq_kv4_cache *cache, const wq_kv4_bounds *bounds,
+                               const wq_kv4_batch *batch, wq_stream_t stream);
+
+/* Choose the pages.  Row r of kv head h, whose token lies in page n - 1 of its
+ * sequence (from 0), has all n pages if n <= max_pages; otherwise pages 0 ..
+ * first - 1, n - last .. n - 1, and as many of the others as make max_pages: those
+ * of the largest score, the lower page where scores are equal.  The score of page j:
+ *   binary32(sum_d (up_d largest_jd + down_d smallest_jd)) * grid_j,
+ *   up_d = sum_i max(c_id, 0), down_d = sum_i min(c_id, 0), c_id = round(q_id / 2^k)
+ * over the queries i of the kv head's group, k the smallest integer with 127 2^k >=
+ * |q_id| for all of them; round is half-to-even, the sum exact.  It is the sum of the
+ * heads' largest possible scores, for a positive softmax scale.  Queries that hold a
+ * NaN or an infinity choose unspecified pages.
+ *
+ * q_heads a multiple of kv_heads, at most 256 times; 0 <= first, 1 <= last, first +
+ * last <= max_pages.  Errors as wq_kv4_attention, and WQ_ERR_INVALID_ARG for the
+ * selection's sizes, WQ_ERR_UNSUPPORTED for a larger group and for a table_width
+ * above 425,984 pages. */
+wq_status wq_kv4_select(const void *Q, int64_t q_stride, int32_t q_heads,
+                        const wq_kv4_cache *cache, const wq_kv4_bounds *bounds,
+                        const wq_kv4_batch *batch, const wq_kv4_selection *selection,
+                        wq_stream_t stream);
+
+/* Attention of each row over the tokens of its lists (the lists and lens of a
+ * selection; first and last are not looked at): O as wq_kv4_attention's, the sum
+ * over those tokens alone.  A row of length 0 gets zeros, one of negative length
+ * is left as it was.  Lists may hold any pages of the cache, in any order; token t of
+ * a list is in slot t % page_size of its page t / page_size.  A length above
+ * max_pages * page_size and, for a token of it, a page outside the cache record
+ * WQ_ERR_INVALID_ARG in the device status word; that row's results are
+ * unspecified.  Roundings as in sequences of few rows.  Workspace and errors as
+ * wq_kv4_attention. */
+wq_status wq_kv4_attention_pages(const void *Q, int64_t q_stride, int32_t q_heads,
+                                 const wq_kv4_cache *cache, int32_t rows,
+                                 const wq_kv4_selection *selection, float scale, void *O,
+                                 int64_t o_stride, void *workspace, size_t workspace_bytes,
+                                 wq_stream_t stream);
+
+/* wq_kv4_update_bounds, wq_kv4_select and wq_kv4_attention_pages one after the
+ * other, the arguments of all checked first: the attention of a step's rows, which
+ * wq_kv4_write has written. */
+wq_status wq_kv4_sparse_attention(const void *Q, int64_t q_stride, int32_t q_heads,
+                                  const wq_kv4_cache *cache, const wq_kv4_bounds *bounds,
+                                  const wq_kv4_batch *batch,
+                                  const wq_kv4_selection *selection, float scale, void *O,
+                                  int64_t o_stride, void *workspace, size_t workspace_bytes,
+                                  wq_stream_t stream);
+
+/* ---- rotary positions ------------------------------------------------------
+ * Element pairs of a head turn by the angle p f_i of the row's position p: pair i
+ * is (i, i + dim/2), or (2i, 2i + 1) where interleaved is not 0, i < dim/2; the
+ * elements from dim on stay as they are.
+ *   y1 = x1 c - x2 s, y2 = x2 c + x1 s, c = amplitude cos(p f_i), s = amplitude sin(p f_i)
+ * The angle is a binary64 product, c and s are rounded to binary32.  Used on
+ * queries and keys before wq_kv4_write. */
+typedef struct wq_rotary_spec {
+    const float *freqs;   /* [dim/2] radians a position, device memory         */
+    int32_t dim;          /* even, 2 .. head_dim                               */
+    int32_t interleaved;  /* 0: halves; 1: neighbours                          */
+    float amplitude;      /* finite; 1 unless the positions are scaled         */
+} wq_rotary_spec;
+
+/* How wq_rotary_frequencies stretches the positions of a model that was trained on
+ * `context` of them to `factor` times as many. */
+enum {
+    WQ_ROTARY_PLAIN = 0,   /* f_i = base^(-2i/dim)                             */
+    WQ_ROTARY_LINEAR = 1,  /* f_i / factor                                     */
+    WQ_ROTARY_BASE = 2,    /* base factor^(dim/(dim-2)) in base's place: the
+                            * slowest pair is stretched by factor, the fastest
+                            * not at all                                       */
+    WQ_ROTARY_PARTS = 3    /* f_i (g + (1 - g) / factor), g = (t - low) / (high
+                            * - low) inside [0, 1], t = context f_i / 2 pi turns:
+                            * pairs of up to low turns are stretched, those of
+                            * high or more not                                 */
+};
+
+/* Frequencies for a wq_rotary_spec, in binary64 rounded to binary32, written to HOST
+ * memory (dim/2 values); no device work.  dim even and 2 or more (4 for
+ * WQ_ROTARY_BASE), base > 0, factor >= 1; context > 0 and low < high for
+ * WQ_ROTARY_PARTS; else WQ_ERR_INVALID_ARG. */
+wq_status wq_rotary_frequencies(int32_t dim, double base, int32_t scaling, double factor,
+                                double context, double low, double high, float *freqs);
+
+/* Flags of wq_rotary. */
+enum { WQ_ROTARY_TRANSPOSE = 1 /* -s in s's place: the gradient of a rotation */ };
+
+/* Y = X turned, bfloat16 [rows][heads][head_dim], heads contiguous, row strides in
+ * elements; positions int32 [rows], device memory, any sign.  Products and sums in
+ * binary32, rounded once to bfloat16 (half a step 2^-8).  Y may be X itself (the
+ * same address and stride), else they may not overlap.  heads may be several tensors'
+ * side by side (queries and keys of a fused projection).
+ * head_dim a multiple of 8, at most 512.  WQ_ERR_INVALID_ARG for sizes, pointers and
+ * flags outside this, WQ_ERR_UNSUPPORTED for another head_dim, WQ_ERR_ALIGNMENT for
+ * X, Y, positions or freqs not 16-byte (positions: 4-byte) aligned and strides that
+ * are no multiple of 8.  rows = 0 is a call without work. */
+wq_status wq_rotary(const void *X, int64_t x_stride, int32_t rows, int32_t heads,
+                    int32_t head_dim, const int32_t *positions, const wq_rotary_spec *spec,
+                    unsigned int flags, void *Y, int64_t y_stride, wq_stream_t stream);
+
+/* Queries turned into Q_out, and wq_kv4_write of the turned keys and the values, in
+ * one call.  Positions are those of the rows' tokens, or `positions` (int32
+ * [rows], 4-byte aligned) where it is given.  Queries as wq_rotary's; keys are turned
+ * exactly, rounded to binary32 and then to bfloat16 and quantized as wq_kv4_write
+ * quantizes (a key that neither of its roundings can decide within 2^-40 may fall to
+ * either side).  Q bfloat16 [rows][q_heads][head_dim]; Q_out may be Q itself (the
+ * same address and stride), else it may not overlap Q, K or V; q_heads 0: keys and
+ * values alone, Q and Q_out not looked at.  A row of a sequence that holds no token
+ * has its query turned and nothing written; rows behind the last sequence are left
+ * alone.  spec->dim a multiple of 16 (WQ_ERR_UNSUPPORTED otherwise: use wq_rotary and
+ * wq_kv4_write).  Other errors as those two. */
+wq_status wq_kv4_write_rotary(const void *Q, int64_t q_stride, int32_t q_heads, void *Q_out,
+                              int64_t qo_stride, const void *K, int64_t k_stride, const void *V,
+                              int64_t v_stride, const wq_rotary_spec *spec,
+                              const int32_t *positions, const wq_kv4_cache *cache,
+                              const wq_kv4_batch *batch, wq_stream_t stream);
+
+/* ---- verification of drafted tokens -----------------------------------------
+ * "vLLM 量化与推测解码" (speculative decoding: a = min(1, p/q), residual max(p - q,
+ * 0)).  The rows of a sequence are those that were written into the cache and given to
+ * the target: a token that stands, and drafts.  With T rows, the draft in row i (i >=
+ * 1) is accepted while
+ *   uniform_i q_i(token_i) < p_{i-1}(token_i)
+ * and all before it were, p_{i-1} the distribution that the target gave behind row i
+ * - 1, q_i the distribution that the draft was drawn from.  Behind the a accepted
+ * drafts one token is sampled with the number uniform_0: from max(p_a - q_{a+1}, 0)
+ * where a draft was rejected (from p_a if that is 0 everywhere), from p_a where none
+ * was; it is the first token whose running sum of masses is greater than uniform_0 times
+ * the whole.  With T = 1 this is sampling. */
+enum {
+    WQ_VERIFY_LOGITS = 1  /* target and draft hold logits, not probabilities: the
+                           * masses are softmax(logits / temperature)            */
+};
+
+typedef struct wq_verification {
+    int32_t rows, seqs, vocab;  /* vocab >= 1                                    */
+    int32_t dtype;              /* of target and draft: WQ_OUT_F32, WQ_OUT_BF16  */
+    uint32_t flags;             /* 0 or WQ_VERIFY_LOGITS                         */
+    const int32_t *row_starts;  /* [seqs + 1] as in wq_kv4_batch, or NULL        */
+    const void *target;         /* [rows][vocab]: p behind each row              */
+    int64_t target_stride;      /* elements from row to row, vocab or more       */
+    const void *draft;          /* [rows][vocab]: q of each row's token (a
+                                 * sequence's first row is not read); NULL: the
+                                 * drafted token had all of the mass             */
+    int64_t draft_stride;
+    const int32_t *tokens;      /* [rows] the tokens of the rows; one outside
+                                 * 0 .. vocab - 1 is never accepted              */
+    const float *uniform;       /* [rows] numbers in [0, 1); others are clamped,
+                                 * a NaN counts as 0                             */
+    const float *temperature;   /* [seqs], with WQ_VERIFY_LOGITS only; NULL: 1.
+                                 * Not above 0: all mass on the largest logit (the
+                                 * lowest token of it); there a draft is accepted
+                                 * if it is that token                           */
+    const int32_t *seq_lens;    /* [seqs] with out_lens: tokens with the rows
+                                 * included                                      */
+    int32_t *out_tokens;        /* [rows]: accepted drafts, the sampled token, -1
+                                 * in a sequence's other rows                    */
+    int32_t *accepted;          /* [seqs]: a                                     */
+    int32_t *out_lens;          /* [seqs] or NULL: seq_lens without the rejected
+                                 * rows, where the next wq_kv4_write goes on     */
+} wq_verification;
+
+/* Bytes of the workspace of a call with WQ_VERIFY_LOGITS (any contents, 16-byte
+ * aligned; calls that may run at the same time need different ones). */
+size_t wq_verify_workspace_bytes(int64_t rows);
+
+/* All masses and sums in binary64 (exponentials within 2^-43), so that the tokens are
+ * those of exact arithmetic unless a number falls within 10^-12 of a border.
+ * Probabilities need not sum to 1; negative ones and NaN count as 0, NaN logits as
+ * -infinity; of logits of +infinity each has the same mass; a row without any mass
+ * gives the token -1.  A sequence without rows gets accepted 0; rows behind the last
+ * sequence are left as they were.  Two sequences' rows may not overlap.  Outputs may
+ * not overlap inputs, but out_lens may be seq_lens.
+ *
+ * Pointers 16-byte aligned, temperature, seq_lens, row_starts, tokens, uniform and
+ * the outputs 4-byte.  Errors: WQ_ERR_INVALID_ARG for a size, pointer or flag outside
+ * this and a workspace that is missing or too small, WQ_ERR_ALIGNMENT.  row_starts are
+ * read when the call runs; a range outside 0 .. rows or that ends before it begins
+ * records WQ_ERR_INVALID_ARG in the device status word and is clamped.  rows = 0 is a
+ * call without work. */
+wq_status wq_verify_drafts(const wq_verification *v, void *workspace, size_t workspace_bytes,
+                           wq_stream_t stream);
+
 /* Read and clear the device status word (WQ_OK if no kernel recorded an
  * error).  Synchronizes `stream` first. */
 wq_status wq_get_device_error(wq_stream_t stream);

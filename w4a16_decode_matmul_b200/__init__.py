@@ -19,6 +19,15 @@ packed rows of a batch of sequences:
     kv4_write(k, v, cache, seq_lens, page_table)
     O = kv4_attention(q, cache, seq_lens, page_table)
     k, v = kv4_read(cache, seq_lens, page_table, rows=n)
+
+Around that attention, in a step of speculative decoding: queries and keys at
+their positions (``Rotary``), the pages of a long cache that each query attends
+to (``KV4Bounds``, made by ``kv4_bounds``), and the drafts that stand:
+
+    q = kv4_write_rotary(q, k, v, cache, rot, seq_lens, page_table)
+    O, lists, lens = kv4_sparse_attention(q, cache, bounds, seq_lens, page_table, max_pages=64)
+    tokens, accepted, seq_lens = verify_drafts(target, tokens, uniform, draft, seqs=n,
+                                               seq_lens=seq_lens)
 """
 from __future__ import annotations
 
@@ -36,6 +45,9 @@ WQ_OK = 0
 WQ_OUT_F32 = 0
 WQ_OUT_BF16 = 1
 WQ_MATMUL_STATIC_WEIGHTS = 1
+WQ_ROTARY_TRANSPOSE = 1
+WQ_VERIFY_LOGITS = 1
+ROTARY_SCALINGS = {None: 0, "linear": 1, "base": 2, "parts": 3}
 
 STATUS_NAMES = {0: "WQ_OK", 1: "WQ_ERR_INVALID_ARG", 2: "WQ_ERR_UNSUPPORTED",
                 3: "WQ_ERR_ALIGNMENT", 4: "WQ_ERR_CUDA", 5: "WQ_ERR_TIMEOUT"}
@@ -65,12 +77,41 @@ class _KV4BatchStruct(ctypes.Structure):
                 ("table_stride", ctypes.c_int64), ("max_rows", ctypes.c_int32)]
 
 
-# The same two structs as bytes (native alignment, trailing padding included):
+class _KV4BoundsStruct(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("grid", ctypes.c_void_p)]
+
+
+class _KV4SelectionStruct(ctypes.Structure):
+    _fields_ = [("max_pages", ctypes.c_int32), ("first", ctypes.c_int32),
+                ("last", ctypes.c_int32), ("lists", ctypes.c_void_p), ("lens", ctypes.c_void_p)]
+
+
+class _RotarySpecStruct(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_float)]
+
+
+class _VerificationStruct(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("seqs", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("row_starts", ctypes.c_void_p), ("target", ctypes.c_void_p),
+                ("target_stride", ctypes.c_int64), ("draft", ctypes.c_void_p),
+                ("draft_stride", ctypes.c_int64), ("tokens", ctypes.c_void_p),
+                ("uniform", ctypes.c_void_p), ("temperature", ctypes.c_void_p),
+                ("seq_lens", ctypes.c_void_p), ("out_tokens", ctypes.c_void_p),
+                ("accepted", ctypes.c_void_p), ("out_lens", ctypes.c_void_p)]
+
+
+# The same structs as bytes (native alignment, trailing padding included):
 # packing is a few times cheaper than filling a ctypes structure.
 _BF16, _I32 = torch.bfloat16, torch.int32
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 _pack_kv4_cache = struct.Struct("@PPPPqiiii").pack
 _pack_kv4_batch = struct.Struct("@iiPPPiqi0q").pack
+_pack_kv4_bounds = struct.Struct("@PP").pack
+_pack_kv4_selection = struct.Struct("@iiiPP").pack
+_pack_rotary_spec = struct.Struct("@Piif0q").pack
+_pack_verification = struct.Struct("@iiiiIPPqPqPPPPPPP").pack
 
 
 def _load() -> ctypes.CDLL:
@@ -113,6 +154,28 @@ def _load() -> ctypes.CDLL:
     lib.wq_kv4_attention_workspace_bytes.restype = sz
     lib.wq_kv4_attention.argtypes = [vp, i64, i32, vp, vp, ctypes.c_float, vp, i64, vp, sz, vp]
     lib.wq_kv4_attention.restype = i32
+    f64 = ctypes.c_double
+    lib.wq_kv4_update_bounds.argtypes = [vp, vp, vp, vp]
+    lib.wq_kv4_update_bounds.restype = i32
+    lib.wq_kv4_select.argtypes = [vp, i64, i32, vp, vp, vp, vp, vp]
+    lib.wq_kv4_select.restype = i32
+    lib.wq_kv4_attention_pages.argtypes = [vp, i64, i32, vp, i32, vp, ctypes.c_float, vp, i64, vp,
+                                           sz, vp]
+    lib.wq_kv4_attention_pages.restype = i32
+    lib.wq_kv4_sparse_attention.argtypes = [vp, i64, i32, vp, vp, vp, vp, ctypes.c_float, vp, i64,
+                                            vp, sz, vp]
+    lib.wq_kv4_sparse_attention.restype = i32
+    lib.wq_rotary_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp]
+    lib.wq_rotary_frequencies.restype = i32
+    lib.wq_rotary.argtypes = [vp, i64, i32, i32, i32, vp, vp, ctypes.c_uint, vp, i64, vp]
+    lib.wq_rotary.restype = i32
+    lib.wq_kv4_write_rotary.argtypes = [vp, i64, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp,
+                                        vp]
+    lib.wq_kv4_write_rotary.restype = i32
+    lib.wq_verify_workspace_bytes.argtypes = [i64]
+    lib.wq_verify_workspace_bytes.restype = sz
+    lib.wq_verify_drafts.argtypes = [vp, vp, sz, vp]
+    lib.wq_verify_drafts.restype = i32
     lib.wq_get_device_error.argtypes = [vp]
     lib.wq_get_device_error.restype = i32
     lib.wq_status_string.argtypes = [i32]
@@ -548,6 +611,351 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, seq_lens: torch.Tensor,
         cache._struct(), _kv4_batch(index, rows, seq_lens, page_table, row_starts, max_rows),
         d ** -0.5 if scale is None else float(scale), out.data_ptr(), os_, workspace.data_ptr(),
         workspace.nbytes)
+    return out
+
+
+@dataclasses.dataclass(frozen=True)
+class KV4Bounds:
+    """Bounds of the keys of every page of a ``KV4Cache`` (see
+    ``include/wq.h``): codes int8 [pages, kv_heads, 2, head_dim], the smallest and
+    the largest value of each dimension on the page's grid float32 [pages,
+    kv_heads]."""
+    codes: torch.Tensor
+    grid: torch.Tensor
+
+    def __post_init__(self):
+        _require_cuda(self.codes, self.grid)
+        if self.codes.dim() != 4 or self.codes.dtype != torch.int8 or self.codes.shape[2] != 2:
+            raise ValueError("codes must be int8 [pages, kv_heads, 2, head_dim]")
+        if self.grid.dtype != torch.float32 or self.grid.shape != self.codes.shape[:2]:
+            raise ValueError("grid must be float32 [pages, kv_heads]")
+
+    def _struct(self, cache: KV4Cache) -> bytes:
+        c, k = self.codes, cache.k_codes
+        pages, _, heads, d, _ = cache._sizes
+        if c.shape != (pages, heads, 2, d):
+            raise ValueError("the bounds are another cache's")
+        if c.get_device() != k.get_device():
+            raise ValueError("the bounds must be on the cache's device")
+        return _pack_kv4_bounds(c.data_ptr(), self.grid.data_ptr())
+
+
+def kv4_bounds(cache: KV4Cache) -> KV4Bounds:
+    """Bounds for a cache (those of pages never updated hold whatever the memory
+    held)."""
+    pages, _, heads, d, _ = cache._sizes
+    device = cache.k_codes.device
+    return KV4Bounds(torch.empty((pages, heads, 2, d), dtype=torch.int8, device=device),
+                     torch.empty((pages, heads), dtype=torch.float32, device=device))
+
+
+def kv4_update_bounds(cache: KV4Cache, bounds: KV4Bounds, seq_lens: torch.Tensor,
+                      page_table: torch.Tensor, row_starts: torch.Tensor | None = None,
+                      rows: int | None = None) -> None:
+    """``wq_kv4_update_bounds``: the bounds of the pages that the rows are in, from
+    the cache; the arguments as for ``kv4_write``, which comes before.  ``rows`` is
+    the number of rows (None: one a sequence)."""
+    index = cache.k_codes.get_device()
+    if rows is None:
+        if row_starts is not None:
+            raise ValueError("rows is required with row_starts")
+        rows = seq_lens.shape[0]
+    _on(index, lib.wq_kv4_update_bounds, "wq_kv4_update_bounds", cache._struct(),
+        bounds._struct(cache), _kv4_batch(index, rows, seq_lens, page_table, row_starts, None))
+
+
+def _kv4_lists(index: int, rows: int, heads: int, max_pages, lists, lens, first: int, last: int,
+               device):
+    """(lists, lens, their struct), made where they are not given."""
+    if lists is None:
+        if max_pages is None:
+            raise ValueError("max_pages or lists is required")
+        lists = torch.empty((rows, heads, max_pages), dtype=torch.int32, device=device)
+    if lens is None:
+        lens = torch.empty((rows,), dtype=torch.int32, device=device)
+    if (lists.dtype is not _I32 or lists.dim() != 3 or lists.shape[0] != rows
+            or lists.shape[1] != heads or not lists.is_contiguous()):
+        raise ValueError("lists must be a contiguous int32 tensor [rows, kv_heads, max_pages]")
+    if max_pages is None:
+        max_pages = lists.shape[2]
+    elif lists.shape[2] != max_pages:
+        raise ValueError("lists must hold max_pages pages")
+    if lens.dtype is not _I32 or lens.shape != (rows,) or not lens.is_contiguous():
+        raise ValueError("lens must be a contiguous int32 tensor [rows]")
+    if lists.get_device() != index or lens.get_device() != index:
+        raise ValueError("lists and lens must be on the cache's device")
+    return lists, lens, _pack_kv4_selection(max_pages, first, last, lists.data_ptr(),
+                                            lens.data_ptr())
+
+
+def kv4_select(q: torch.Tensor, cache: KV4Cache, bounds: KV4Bounds, seq_lens: torch.Tensor,
+               page_table: torch.Tensor, row_starts: torch.Tensor | None = None,
+               max_pages: int | None = None, first: int = 1, last: int = 2,
+               lists: torch.Tensor | None = None, lens: torch.Tensor | None = None):
+    """``wq_kv4_select``: the pages that each row and kv head attends to -- the
+    first ``first``, the last ``last`` and those of the largest scores, ``max_pages``
+    in all -- as (lists int32 [rows, kv_heads, max_pages], lens int32 [rows])."""
+    _, _, heads, d, _ = cache._sizes
+    index = cache.k_codes.get_device()
+    rows, q_heads, qs = _kv4_rows(q, None, d, index, "q")
+    if q_heads == 0 or q_heads % heads:
+        raise ValueError("q_heads must be a multiple of kv_heads")
+    lists, lens, selection = _kv4_lists(index, rows, heads, max_pages, lists, lens, first, last,
+                                        q.device)
+    _on(index, lib.wq_kv4_select, "wq_kv4_select", q.data_ptr(), qs, q_heads, cache._struct(),
+        bounds._struct(cache), _kv4_batch(index, rows, seq_lens, page_table, row_starts, None),
+        selection)
+    return lists, lens
+
+
+def _kv4_output(q, out, workspace, rows: int, q_heads: int, d: int, index: int, make):
+    """(out, its row stride, workspace) of an attention call."""
+    if out is None:
+        out = make(q.shape, dtype=_BF16, device=q.device)
+    out_rows, _, os_ = _kv4_rows(out, q_heads, d, index, "out")
+    if out_rows != rows:
+        raise ValueError("out must have the rows of q")
+    if workspace is None:
+        workspace = kv4_workspace(q.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the cache's device")
+    return out, os_, workspace
+
+
+def kv4_attention_pages(q: torch.Tensor, cache: KV4Cache, lists: torch.Tensor,
+                        lens: torch.Tensor, scale: float | None = None,
+                        out: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """``wq_kv4_attention_pages``: attention of the rows' queries over the tokens of
+    their lists (``kv4_select``'s).  ``scale``, ``out`` and ``workspace`` as for
+    ``kv4_attention``; a row of negative length is left as it was in ``out`` (zeros
+    without it)."""
+    _, _, heads, d, _ = cache._sizes
+    index = cache.k_codes.get_device()
+    rows, q_heads, qs = _kv4_rows(q, None, d, index, "q")
+    if q_heads == 0 or q_heads % heads:
+        raise ValueError("q_heads must be a multiple of kv_heads")
+    _, _, selection = _kv4_lists(index, rows, heads, None, lists, lens, 0, 1, q.device)
+    out, os_, workspace = _kv4_output(q, out, workspace, rows, q_heads, d, index, torch.zeros)
+    _on(index, lib.wq_kv4_attention_pages, "wq_kv4_attention_pages", q.data_ptr(), qs, q_heads,
+        cache._struct(), rows, selection, d ** -0.5 if scale is None else float(scale),
+        out.data_ptr(), os_, workspace.data_ptr(), workspace.nbytes)
+    return out
+
+
+def kv4_sparse_attention(q: torch.Tensor, cache: KV4Cache, bounds: KV4Bounds,
+                         seq_lens: torch.Tensor, page_table: torch.Tensor,
+                         row_starts: torch.Tensor | None = None, max_pages: int | None = None,
+                         first: int = 1, last: int = 2, scale: float | None = None,
+                         out: torch.Tensor | None = None, lists: torch.Tensor | None = None,
+                         lens: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None):
+    """``wq_kv4_sparse_attention``: ``kv4_update_bounds``, ``kv4_select`` and
+    ``kv4_attention_pages`` in one call, for rows that ``kv4_write`` has written.
+    Returns (out, lists, lens)."""
+    _, _, heads, d, _ = cache._sizes
+    index = cache.k_codes.get_device()
+    rows, q_heads, qs = _kv4_rows(q, None, d, index, "q")
+    if q_heads == 0 or q_heads % heads:
+        raise ValueError("q_heads must be a multiple of kv_heads")
+    lists, lens, selection = _kv4_lists(index, rows, heads, max_pages, lists, lens, first, last,
+                                        q.device)
+    out, os_, workspace = _kv4_output(q, out, workspace, rows, q_heads, d, index,
+                                      torch.empty if row_starts is None else torch.zeros)
+    _on(index, lib.wq_kv4_sparse_attention, "wq_kv4_sparse_attention", q.data_ptr(), qs, q_heads,
+        cache._struct(), bounds._struct(cache),
+        _kv4_batch(index, rows, seq_lens, page_table, row_starts, None), selection,
+        d ** -0.5 if scale is None else float(scale), out.data_ptr(), os_, workspace.data_ptr(),
+        workspace.nbytes)
+    return out, lists, lens
+
+
+def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str | None = None,
+                       factor: float = 1.0, context: float = 0.0, low: float = 1.0,
+                       high: float = 32.0) -> torch.Tensor:
+    """``wq_rotary_frequencies``: float32 [dim/2] on the host, radians a position.
+    ``scaling`` None, "linear", "base" or "parts" (see ``include/wq.h``)."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {list(ROTARY_SCALINGS)}")
+    out = torch.empty(max(0, dim // 2), dtype=torch.float32)
+    _check(lib.wq_rotary_frequencies(dim, base, ROTARY_SCALINGS[scaling], factor, context, low,
+                                     high, _ptr(out)), "wq_rotary_frequencies")
+    return out
+
+
+@dataclasses.dataclass(frozen=True)
+class Rotary:
+    """Rotary positions of a model: frequencies float32 [dim/2] on the GPU, the layout
+    of the pairs, and the factor of cosines and sines."""
+    freqs: torch.Tensor
+    interleaved: bool = False
+    amplitude: float = 1.0
+
+    def __post_init__(self):
+        _require_cuda(self.freqs)
+        if self.freqs.dim() != 1 or self.freqs.dtype != torch.float32 or not self.freqs.numel():
+            raise ValueError("freqs must be a 1-D float32 tensor")
+
+    def _struct(self, index: int) -> bytes:
+        if self.freqs.get_device() != index:
+            raise ValueError("freqs must be on the rows' device")
+        return _pack_rotary_spec(self.freqs.data_ptr(), 2 * self.freqs.shape[0],
+                                 bool(self.interleaved), self.amplitude)
+
+
+def _positions(positions, rows: int, index: int) -> int:
+    if positions is None:
+        return 0
+    if positions.dtype is not _I32 or positions.shape != (rows,) or not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous int32 tensor [rows]")
+    if positions.get_device() != index:
+        raise ValueError("positions must be on the rows' device")
+    return positions.data_ptr()
+
+
+def rotary(x: torch.Tensor, positions: torch.Tensor, rot: Rotary, inverse: bool = False,
+           out: torch.Tensor | None = None) -> torch.Tensor:
+    """``wq_rotary``: x bfloat16 [rows, heads, head_dim] (heads contiguous, rows any
+    stride that is a multiple of 8) turned by its positions, int32 [rows].
+    ``inverse`` turns by the transpose: the gradient with respect to x of a rotation
+    of x.  ``out`` may be ``x`` itself."""
+    if x.dim() != 3 or not x.is_cuda:
+        raise ValueError("x must be a bfloat16 tensor [rows, heads, head_dim] on a CUDA device")
+    index = x.get_device()
+    rows, heads, xs = _kv4_rows(x, None, x.shape[2], index, "x")
+    if out is None:
+        out = torch.empty(x.shape, dtype=_BF16, device=x.device)
+    out_rows, _, os_ = _kv4_rows(out, heads, x.shape[2], index, "out")
+    if out_rows != rows:
+        raise ValueError("out must have the rows of x")
+    if positions is None:
+        raise ValueError("positions is required")
+    _on(index, lib.wq_rotary, "wq_rotary", x.data_ptr(), xs, rows, heads, x.shape[2],
+        _positions(positions, rows, index), rot._struct(index),
+        WQ_ROTARY_TRANSPOSE if inverse else 0, out.data_ptr(), os_)
+    return out
+
+
+def kv4_write_rotary(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: KV4Cache,
+                     rot: Rotary, seq_lens: torch.Tensor, page_table: torch.Tensor,
+                     row_starts: torch.Tensor | None = None,
+                     positions: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None) -> torch.Tensor | None:
+    """``wq_kv4_write_rotary``: ``kv4_write`` of the keys turned by their positions
+    (those of the rows' tokens, or ``positions`` int32 [rows]) and of the values;
+    returns the turned queries in ``out`` (which may be ``q``).  ``q`` None: keys and
+    values alone."""
+    _, _, heads, d, _ = cache._sizes
+    index = cache.k_codes.get_device()
+    rows, _, ks = _kv4_rows(k, heads, d, index, "k")
+    v_rows, _, vs = _kv4_rows(v, heads, d, index, "v")
+    if rows != v_rows:
+        raise ValueError("k and v must have the same rows")
+    q_ptr, out_ptr, q_heads, qs, os_ = 0, 0, 0, 0, 0
+    if q is not None:
+        q_rows, q_heads, qs = _kv4_rows(q, None, d, index, "q")
+        if out is None:
+            make = torch.empty if row_starts is None else torch.zeros
+            out = make(q.shape, dtype=_BF16, device=q.device)
+        out_rows, _, os_ = _kv4_rows(out, q_heads, d, index, "out")
+        if q_rows != rows or out_rows != rows:
+            raise ValueError("q, k and out must have the same rows")
+        q_ptr, out_ptr = q.data_ptr(), out.data_ptr()
+    _on(index, lib.wq_kv4_write_rotary, "wq_kv4_write_rotary", q_ptr, qs, q_heads, out_ptr, os_,
+        k.data_ptr(), ks, v.data_ptr(), vs, rot._struct(index),
+        _positions(positions, rows, index), cache._struct(),
+        _kv4_batch(index, rows, seq_lens, page_table, row_starts, None))
+    return out if q is not None else None
+
+
+def verify_workspace(rows: int, device: torch.device | str = "cuda") -> torch.Tensor:
+    """A workspace of ``verify_drafts`` for up to ``rows`` rows of logits.  One serves
+    all calls of a stream; calls that may run at the same time need one each."""
+    return torch.empty(lib.wq_verify_workspace_bytes(rows), dtype=torch.uint8, device=device)
+
+
+def _verify_rows(x: torch.Tensor, rows: int, vocab: int, dtype, index: int, what: str) -> int:
+    """Row stride of [rows, vocab], the vocabulary contiguous."""
+    if x.dim() != 2 or x.shape != (rows, vocab) or x.dtype is not dtype:
+        raise ValueError(f"{what} must be {dtype} [{rows}, {vocab}]")
+    if x.get_device() != index:
+        raise ValueError(f"{what} must be on target's device")
+    row, step = x.stride()
+    if step != 1 and vocab > 1:
+        raise ValueError(f"the rows of {what} must be contiguous")
+    return row if rows > 1 else vocab
+
+
+def _words(x, dtype, shape, index: int, what: str) -> int:
+    if x is None:
+        return 0
+    if x.dtype is not dtype or x.shape != shape or not x.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor {list(shape)}")
+    if x.get_device() != index:
+        raise ValueError(f"{what} must be on target's device")
+    return x.data_ptr()
+
+
+def verify_drafts(target: torch.Tensor, tokens: torch.Tensor, uniform: torch.Tensor,
+                  draft: torch.Tensor | None = None, seqs: int | None = None,
+                  row_starts: torch.Tensor | None = None, logits: bool = False,
+                  temperature: torch.Tensor | None = None, seq_lens: torch.Tensor | None = None,
+                  out=None, workspace: torch.Tensor | None = None):
+    """``wq_verify_drafts``: which drafts stand, and the token behind them.
+
+    target [rows, vocab], float32 or bfloat16, holds the target's probabilities behind
+    every row (``logits``: its logits, divided by temperature float32 [seqs], 0 for the
+    largest); draft, of the same shape and type, the distribution that each row's token
+    int32 [rows] was drawn from (None: it had all of the mass); uniform float32 [rows]
+    in [0, 1).  The rows of a sequence are one that stands and its drafts; ``seqs``
+    sequences of rows/seqs rows each, or row_starts int32 [seqs + 1].
+
+    Returns (tokens int32 [rows]: the accepted drafts, the sampled token, -1s; accepted
+    int32 [seqs]; ``seq_lens`` without the rejected rows, or None).  ``out`` is those
+    three tensors; rows behind the last sequence are left as they were (-1 without
+    it).  ``workspace`` (``verify_workspace``) is used for logits; without it each call
+    makes its own."""
+    if target.dtype is not torch.float32 and target.dtype is not _BF16 or target.dim() != 2:
+        raise ValueError("target must be float32 or bfloat16 [rows, vocab]")
+    if not target.is_cuda:
+        raise ValueError("target must be on a CUDA device")
+    index = target.get_device()
+    rows, vocab = target.shape
+    if row_starts is not None:
+        n = row_starts.shape[0] - 1
+        if seqs is not None and seqs != n:
+            raise ValueError("row_starts must have seqs + 1 elements")
+        seqs = n
+    elif seqs is None:
+        raise ValueError("seqs or row_starts is required")
+    ts = _verify_rows(target, rows, vocab, target.dtype, index, "target")
+    ds = 0 if draft is None else _verify_rows(draft, rows, vocab, target.dtype, index, "draft")
+    if out is None:
+        out = (torch.full((rows,), -1, dtype=_I32, device=target.device),
+               torch.empty((seqs,), dtype=_I32, device=target.device),
+               None if seq_lens is None else torch.empty_like(seq_lens))
+    if logits and workspace is None:
+        workspace = verify_workspace(max(rows, 1), target.device)
+    if workspace is not None and (workspace.get_device() != index
+                                  or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous and on target's device")
+    if (out[2] is None) != (seq_lens is None):
+        raise ValueError("seq_lens and out[2] go together")
+    n_shape, b_shape = (rows,), (seqs,)
+    v = _pack_verification(
+        rows, seqs, vocab, WQ_OUT_BF16 if target.dtype is _BF16 else WQ_OUT_F32,
+        WQ_VERIFY_LOGITS if logits else 0,
+        _words(row_starts, _I32, (seqs + 1,), index, "row_starts"), target.data_ptr(), ts,
+        0 if draft is None else draft.data_ptr(), ds, _words(tokens, _I32, n_shape, index, "tokens"),
+        _words(uniform, torch.float32, n_shape, index, "uniform"),
+        _words(temperature, torch.float32, b_shape, index, "temperature"),
+        _words(seq_lens, _I32, b_shape, index, "seq_lens"),
+        _words(out[0], _I32, n_shape, index, "out[0]"),
+        _words(out[1], _I32, b_shape, index, "out[1]"),
+        _words(out[2], _I32, b_shape, index, "out[2]"))
+    _on(index, lib.wq_verify_drafts, "wq_verify_drafts", v,
+        0 if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.nbytes)
     return out
 
 

@@ -5,7 +5,7 @@
 #include <cmath>
 
 #include "kv4_host.h"
-#include "kv4.cuh"
+#include "kv4_launch.cuh"
 #include "kv4_attn.cuh"
 #include "kv4_prefill.cuh"
 
@@ -17,56 +17,9 @@ cudaError_t run_kv4_prefill(int head_dim, int group, const wq::kv4::PrefillParam
 
 namespace {
 
-namespace kv4 = wq::kv4;
-
 // Test hooks of the timeout path (wq_internal_kv4_timeout_test).
 int g_kv4_stuck_cta = -1;
 unsigned int g_kv4_wait_ns = unsigned(wq::kWaitLimitNs);
-
-kv4::Cache device_cache(const wq_kv4_cache& c) {
-  kv4::Cache d = {};
-  d.k_codes = static_cast<uint8_t*>(c.k_codes);
-  d.k_meta = static_cast<__half2*>(c.k_meta);
-  d.v_codes = static_cast<uint8_t*>(c.v_codes);
-  d.v_meta = static_cast<__half2*>(c.v_meta);
-  d.pages = c.pages;
-  while ((1 << d.page_shift) < c.page_size) ++d.page_shift;
-  d.kv_heads = c.kv_heads;
-  return d;
-}
-
-kv4::Batch device_batch(const wq_kv4_batch& b, int page_size) {
-  kv4::Batch d = {};
-  d.row_starts = b.row_starts;
-  d.seq_lens = b.seq_lens;
-  d.page_table = b.page_table;
-  d.table_stride = b.table_stride;
-  d.seqs = b.seqs;
-  d.rows = b.rows;
-  d.rows_per_seq = b.row_starts ? 0 : b.rows / b.seqs;
-  d.max_len = int(std::min<int64_t>(int64_t(b.table_width) * page_size, 0x7fffff00));
-  d.status = status_address();
-  return d;
-}
-
-// Calls every (head dim, group) the cache supports through F<D, G>::run.
-template <template <int, int> class F, typename... Args>
-cudaError_t dispatch_kv4(int head_dim, int group, const Args&... args) {
-#define WQ_CASE(D, G) \
-  if (head_dim == D && group == G) return F<D, G>::run(args...);
-  WQ_CASE(64, 32) WQ_CASE(64, 64)
-  WQ_CASE(128, 32) WQ_CASE(128, 64) WQ_CASE(128, 128)
-#undef WQ_CASE
-  return cudaErrorInvalidValue;
-}
-
-// Warps per row (each takes up to kRowIterations * 32 pieces of 16 elements),
-// and the CTAs that all rows make.
-int row_chunks(const wq_kv4_cache& c) {
-  const int64_t pieces = int64_t(c.kv_heads) * (c.head_dim / 16);
-  const int per_warp = kv4::kRowIterations * 32;
-  return int((pieces + per_warp - 1) / per_warp);
-}
 
 int64_t row_warps(const wq_kv4_cache& c, int rows) { return int64_t(rows) * row_chunks(c); }
 
@@ -143,13 +96,6 @@ struct AttnOp {
   }
 };
 
-kv4::FastDiv fast_div(uint32_t d) {
-  uint32_t shift = 0;
-  while ((uint64_t(1) << shift) < d) ++shift;
-  const uint64_t one = uint64_t(1) << 32;
-  return {uint32_t(one * ((uint64_t(1) << shift) - d) / d + 1), shift};
-}
-
 // CTAs of the tensor-memory kernel that share a block's tokens: as many as fit
 // on the SMs together (each has a slot of the workspace), where that is two or
 // more.
@@ -179,6 +125,30 @@ bool prefer_prefill(const wq_kv4_batch& b, int kv_heads, int gqa, int sms) {
 
 constexpr size_t kCounterBytes = kv4::kMaxCtas * kv4::kMaxRows * 4;
 
+// The parameters that both forms of the attention share.
+kv4::AttnParams attn_params(const void* Q, int64_t q_stride, int q_heads,
+                            const wq_kv4_cache& cache, float scale, void* O, int64_t o_stride,
+                            void* workspace) {
+  kv4::AttnParams p = {};
+  p.cache = device_cache(cache);
+  p.Q = static_cast<const __nv_bfloat16*>(Q);
+  p.q_stride = q_stride;
+  p.O = static_cast<__nv_bfloat16*>(O);
+  p.o_stride = o_stride;
+  p.gqa = q_heads / cache.kv_heads;
+  p.by_gqa = fast_div(uint32_t(p.gqa));
+  // finite for every finite scale: an infinite one would make NaN of scores of zero
+  p.scale_log2 = float(std::clamp(double(scale) * 1.4426950408889634, -double(FLT_MAX),
+                                  double(FLT_MAX)));
+  p.arrived = static_cast<unsigned*>(workspace);
+  p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
+                                       round_up(kCounterBytes, 256));
+  p.test_stuck_cta = g_kv4_stuck_cta;
+  p.wait_ns = g_kv4_wait_ns;
+  p.max_columns = 1 << 30;
+  return p;
+}
+
 }  // namespace
 
 size_t kv4_workspace_bytes() {
@@ -202,24 +172,9 @@ cudaError_t run_kv4_attention(const void* Q, int64_t q_stride, int q_heads,
                               const wq_kv4_cache& cache, const wq_kv4_batch& batch, float scale,
                               void* O, int64_t o_stride, void* workspace, cudaStream_t s,
                               const DeviceInfo& dev) {
-  kv4::AttnParams p = {};
-  p.cache = device_cache(cache);
+  kv4::AttnParams p = attn_params(Q, q_stride, q_heads, cache, scale, O, o_stride, workspace);
   p.batch = device_batch(batch, cache.page_size);
   if (p.batch.status == nullptr) return cudaErrorInitializationError;
-  p.Q = static_cast<const __nv_bfloat16*>(Q);
-  p.q_stride = q_stride;
-  p.O = static_cast<__nv_bfloat16*>(O);
-  p.o_stride = o_stride;
-  p.gqa = q_heads / cache.kv_heads;
-  p.by_gqa = fast_div(uint32_t(p.gqa));
-  // finite for every finite scale: an infinite one would make NaN of scores of zero
-  p.scale_log2 = float(std::clamp(double(scale) * 1.4426950408889634, -double(FLT_MAX),
-                                  double(FLT_MAX)));
-  p.arrived = static_cast<unsigned*>(workspace);
-  p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
-                                       round_up(kCounterBytes, 256));
-  p.test_stuck_cta = g_kv4_stuck_cta;
-  p.wait_ns = g_kv4_wait_ns;
   const int64_t max_rows = batch.row_starts ? batch.max_rows : batch.rows / batch.seqs;
   // Sequences with up to 16 rows (times the heads of a group) stream the cache
   // through the warp-level kernel.  With more there is the choice between that
@@ -227,7 +182,6 @@ cudaError_t run_kv4_attention(const void* Q, int64_t q_stride, int q_heads,
   // kernel, once per 256 rows with a CTA for each.
   constexpr int kFew = kv4::kMaxRows;
   const int64_t bound = max_rows > 0 ? max_rows : batch.rows;
-  p.max_columns = 1 << 30;
   if (bound * p.gqa > kFew && prefer_prefill(batch, cache.kv_heads, p.gqa, dev.sms)) {
     kv4::PrefillParams pp = {p, kFew + 1,
                              prefill_splits(batch, cache.kv_heads, p.gqa, dev.sms), p.partial};
@@ -237,6 +191,22 @@ cudaError_t run_kv4_attention(const void* Q, int64_t q_stride, int q_heads,
   }
   const int max_columns = int(std::min<int64_t>(bound * p.gqa, kFew));
   return dispatch_kv4<AttnOp>(cache.head_dim, cache.group, p, max_columns, s, dev.sms);
+}
+
+cudaError_t run_kv4_attention_pages(const void* Q, int64_t q_stride, int q_heads,
+                                    const wq_kv4_cache& cache, int rows,
+                                    const wq_kv4_selection& sel, float scale, void* O,
+                                    int64_t o_stride, void* workspace, cudaStream_t s,
+                                    const DeviceInfo& dev) {
+  kv4::AttnParams p = attn_params(Q, q_stride, q_heads, cache, scale, O, o_stride, workspace);
+  const wq_kv4_batch each_row = {rows,       rows,      nullptr,
+                                 sel.lens,   sel.lists, sel.max_pages,
+                                 int64_t(sel.max_pages) * cache.kv_heads, 1};
+  p.batch = device_batch(each_row, cache.page_size);
+  if (p.batch.status == nullptr) return cudaErrorInitializationError;
+  p.head_stride = sel.max_pages;
+  return dispatch_kv4<AttnOp>(cache.head_dim, cache.group, p, std::min(p.gqa, kv4::kMaxRows), s,
+                              dev.sms);
 }
 
 }  // namespace wqh

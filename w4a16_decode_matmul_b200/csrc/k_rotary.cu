@@ -1,0 +1,103 @@
+// k_rotary.cu -- launchers of the rotary kernels: rows turned where they are or
+// into other memory, and on their way into the 4-bit cache.
+#include <algorithm>
+
+#include "kv4_launch.cuh"
+#include "rotary.cuh"
+#include "rotary_host.h"
+
+namespace wqh {
+namespace {
+
+namespace rotary = wq::rotary;
+
+rotary::Spec device_spec(const wq_rotary_spec& s) { return {s.freqs, s.dim, s.amplitude}; }
+
+template <int D, int G>
+struct WriteRotaryOp {
+  static cudaError_t run(rotary::WriteParams p, const wq_kv4_cache& c, int interleaved,
+                         cudaStream_t s) {
+    p.chunks = row_chunks(c);
+    const int per_head = interleaved ? (p.copy_q ? D : p.spec.dim) / 8
+                                     : p.spec.dim / 16 + (p.copy_q ? (D - p.spec.dim) / 8 : 0);
+    const int64_t units = int64_t(p.q_heads) * per_head, share = 32 * rotary::kQueryUnits;
+    const int items = p.chunks + int((units + share - 1) / share);
+    const int warps = std::min(items, rotary::kMaxWarps);
+    // CTAs behind the rows' check the sequences, 32 a warp
+    const int64_t check =
+        std::min<int64_t>((int64_t(p.batch.seqs) + 32 * warps - 1) / (32 * warps), 1024);
+    const unsigned ctas = unsigned(p.batch.rows + check);
+    if (interleaved)
+      rotary::write_rotary_kernel<D, G, true><<<ctas, warps * 32, 0, s>>>(p, items);
+    else
+      rotary::write_rotary_kernel<D, G, false><<<ctas, warps * 32, 0, s>>>(p, items);
+    return cudaGetLastError();
+  }
+};
+
+}  // namespace
+
+cudaError_t run_rotary(const void* X, int64_t x_stride, int rows, int heads, int head_dim,
+                       const int* positions, const wq_rotary_spec& spec, bool transpose, void* Y,
+                       int64_t y_stride, cudaStream_t s, int sms) {
+  rotary::RotaryParams p = {};
+  p.X = static_cast<const __nv_bfloat16*>(X);
+  p.x_stride = x_stride;
+  p.Y = static_cast<__nv_bfloat16*>(Y);
+  p.y_stride = y_stride;
+  p.positions = positions;
+  p.spec = device_spec(spec);
+  p.heads = heads;
+  p.head_dim = head_dim;
+  p.copy = X != Y;
+  p.sign = transpose ? -1.f : 1.f;
+  const bool pairs = !spec.interleaved && spec.dim % 16 != 0;
+  int per_head;
+  if (pairs)
+    per_head = spec.dim / 2 + (p.copy ? head_dim - spec.dim : 0);
+  else if (spec.interleaved)
+    per_head = p.copy ? head_dim / 8 : (spec.dim + 7) / 8;
+  else
+    per_head = spec.dim / 16 + (p.copy ? (head_dim - spec.dim) / 8 : 0);
+  const int64_t units = int64_t(heads) * per_head;
+  // One CTA a row, as many threads as its units need in whole rounds; where there
+  // are fewer rows than SMs a row's units are spread over CTAs of 128.
+  const int64_t split = std::min<int64_t>(std::max(1, 2 * sms / rows), (units + 127) / 128);
+  const int64_t mine = (units + split - 1) / split;
+  const int64_t rounds = (mine + 511) / 512;
+  const int threads = int(((mine + rounds - 1) / rounds + 31) / 32 * 32);
+  const dim3 grid{unsigned(rows), unsigned(split)};
+  if (pairs)
+    rotary::rotary_pair_kernel<<<grid, threads, 0, s>>>(p);
+  else if (spec.interleaved)
+    rotary::rotary_kernel<true><<<grid, threads, 0, s>>>(p);
+  else
+    rotary::rotary_kernel<false><<<grid, threads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t run_kv4_write_rotary(const void* Q, int64_t q_stride, int q_heads, void* Q_out,
+                                 int64_t qo_stride, const void* K, int64_t k_stride,
+                                 const void* V, int64_t v_stride, const wq_rotary_spec& spec,
+                                 const int* positions, const wq_kv4_cache& cache,
+                                 const wq_kv4_batch& batch, cudaStream_t s) {
+  rotary::WriteParams p = {};
+  p.Q = static_cast<const __nv_bfloat16*>(Q);
+  p.q_stride = q_stride;
+  p.Q_out = static_cast<__nv_bfloat16*>(Q_out);
+  p.qo_stride = qo_stride;
+  p.q_heads = q_heads;
+  p.copy_q = Q != Q_out;
+  p.K = static_cast<const __nv_bfloat16*>(K);
+  p.k_stride = k_stride;
+  p.V = static_cast<const __nv_bfloat16*>(V);
+  p.v_stride = v_stride;
+  p.positions = positions;
+  p.spec = device_spec(spec);
+  p.cache = device_cache(cache);
+  p.batch = device_batch(batch, cache.page_size);
+  if (p.batch.status == nullptr) return cudaErrorInitializationError;
+  return dispatch_kv4<WriteRotaryOp>(cache.head_dim, cache.group, p, cache, spec.interleaved, s);
+}
+
+}  // namespace wqh

@@ -82,6 +82,10 @@ struct AttnParams {
   int64_t o_stride;
   int gqa;            // query heads per kv head
   int max_columns;    // sequences with more rows times gqa are another kernel's
+  // Elements from one kv head's pages to the next's in the page table: 0, or, where
+  // every head has a list of its own, its width.  There each row is a sequence, and one
+  // of negative length is left alone.
+  int64_t head_stride;
   FastDiv by_gqa;
   float scale_log2;   // softmax scale times log2 e
   // Test hooks of the timeout path (set only through an internal export): the
@@ -147,6 +151,7 @@ struct AttnControl {
 __device__ __forceinline__ Sequence attn_sequence(const AttnParams& p, int b) {
   Sequence s = load_sequence(p.batch, b);
   if (s.rows * p.gqa > p.max_columns) s.rows = 0;
+  if (p.head_stride != 0 && p.batch.seq_lens[b] < 0) s.rows = 0;
   return s;
 }
 
@@ -431,7 +436,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
       const int pos = pf_unit * kUnit + (sub << sub_shift);
       if (sub < (kUnit >> sub_shift) && pos < pf.limit)
         pf_page = p.batch.page_table[int64_t(pf.b) * p.batch.table_stride +
-                                     (pos >> p.cache.page_shift)];
+                                     pf.h * p.head_stride + (pos >> p.cache.page_shift)];
     };
     auto copy_unit = [&](int s) {
       const int tok0 = pf_unit * kUnit;

@@ -12,6 +12,8 @@
 #include "wq.h"
 #include "host.h"
 #include "kv4_host.h"
+#include "rotary_host.h"
+#include "verify_host.h"
 #include "common.cuh"
 #include "stream.cuh"
 
@@ -526,6 +528,58 @@ wq_status check_kv4_rows(const void* p, int64_t stride, int64_t heads, int head_
   return WQ_OK;
 }
 
+// What the forms of the attention share, for rows > 0.
+wq_status check_kv4_attention(const void* Q, int64_t q_stride, int32_t q_heads,
+                              const wq_kv4_cache* cache, int32_t rows, const void* O,
+                              int64_t o_stride, const void* workspace, size_t workspace_bytes) {
+  // a row index times the heads of its group stays inside 32 bits
+  if (int64_t(rows) * (q_heads / cache->kv_heads) >= (int64_t(1) << 30)) return WQ_ERR_INVALID_ARG;
+  wq_status st = check_kv4_rows(Q, q_stride, q_heads, cache->head_dim);
+  if (st != WQ_OK) return st;
+  if ((st = check_kv4_rows(O, o_stride, q_heads, cache->head_dim)) != WQ_OK) return st;
+  if (!workspace || workspace_bytes < wqh::kv4_workspace_bytes()) return WQ_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return WQ_ERR_ALIGNMENT;
+  return WQ_OK;
+}
+
+// Bounds of a batch with rows > 0; the grids of the two kernels fit 31 bits.
+wq_status check_kv4_bounds(const wq_kv4_bounds* bounds, const wq_kv4_cache* cache,
+                           const wq_kv4_batch* batch) {
+  if (!bounds || !bounds->codes || !bounds->grid) return WQ_ERR_INVALID_ARG;
+  const int64_t pages = int64_t(batch->rows) / cache->page_size + 2 * int64_t(batch->seqs);
+  if (pages * cache->kv_heads >= (int64_t(1) << 30)) return WQ_ERR_INVALID_ARG;
+  if (!aligned16(bounds->codes) || !aligned16(bounds->grid)) return WQ_ERR_ALIGNMENT;
+  return WQ_OK;
+}
+
+// The lists of a selection.
+wq_status check_kv4_selection(const wq_kv4_selection* s, const wq_kv4_cache* cache,
+                              int32_t rows) {
+  if (!s || !s->lists || !s->lens || s->max_pages < 1) return WQ_ERR_INVALID_ARG;
+  if (int64_t(rows) * cache->kv_heads >= (int64_t(1) << 27)) return WQ_ERR_INVALID_ARG;
+  if (!aligned16(s->lists) || !aligned16(s->lens)) return WQ_ERR_ALIGNMENT;
+  return WQ_OK;
+}
+
+// How they are chosen.
+wq_status check_kv4_choice(const wq_kv4_selection* s, int32_t q_heads, const wq_kv4_cache* cache,
+                           const wq_kv4_batch* batch) {
+  if (s->first < 0 || s->last < 1 || int64_t(s->first) + s->last > s->max_pages)
+    return WQ_ERR_INVALID_ARG;
+  if (q_heads / cache->kv_heads > wqh::kv4_select_max_group() ||
+      batch->table_width > wqh::kv4_select_max_pages())
+    return WQ_ERR_UNSUPPORTED;
+  return WQ_OK;
+}
+
+wq_status check_rotary(const wq_rotary_spec* s, int32_t head_dim) {
+  if (!s || !s->freqs || s->dim < 2 || s->dim % 2 != 0 || s->dim > head_dim ||
+      (s->interleaved != 0 && s->interleaved != 1) || !std::isfinite(s->amplitude))
+    return WQ_ERR_INVALID_ARG;
+  if (!aligned16(s->freqs)) return WQ_ERR_ALIGNMENT;
+  return WQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -570,18 +624,211 @@ wq_status wq_kv4_attention(const void* Q, int64_t q_stride, int32_t q_heads,
     return WQ_ERR_INVALID_ARG;
   if (batch->rows == 0) return WQ_OK;
   if ((st = check_kv4_batch(batch)) != WQ_OK) return st;
-  // a row index times the heads of its group stays inside 32 bits
-  if (int64_t(batch->rows) * (q_heads / cache->kv_heads) >= (int64_t(1) << 30))
-    return WQ_ERR_INVALID_ARG;
-  if ((st = check_kv4_rows(Q, q_stride, q_heads, cache->head_dim)) != WQ_OK) return st;
-  if ((st = check_kv4_rows(O, o_stride, q_heads, cache->head_dim)) != WQ_OK) return st;
-  if (!workspace || workspace_bytes < wqh::kv4_workspace_bytes()) return WQ_ERR_INVALID_ARG;
-  if (!aligned16(workspace)) return WQ_ERR_ALIGNMENT;
+  if ((st = check_kv4_attention(Q, q_stride, q_heads, cache, batch->rows, O, o_stride, workspace,
+                                workspace_bytes)) != WQ_OK)
+    return st;
   DeviceInfo dev;
   if (!wqh::device_info(&dev)) return WQ_ERR_CUDA;
   return from_cuda(wqh::run_kv4_attention(Q, q_stride, q_heads, *cache, *batch, scale, O,
                                           o_stride, workspace,
                                           reinterpret_cast<cudaStream_t>(stream), dev));
+}
+
+// ------------------------------------------------ pages chosen for each query
+
+wq_status wq_kv4_update_bounds(const wq_kv4_cache* cache, const wq_kv4_bounds* bounds,
+                               const wq_kv4_batch* batch, wq_stream_t stream) {
+  wq_status st = check_kv4_cache(cache);
+  if (st != WQ_OK) return st;
+  if (!batch || batch->rows < 0) return WQ_ERR_INVALID_ARG;
+  if (batch->rows == 0) return WQ_OK;
+  if ((st = check_kv4_batch(batch)) != WQ_OK) return st;
+  if ((st = check_kv4_bounds(bounds, cache, batch)) != WQ_OK) return st;
+  return from_cuda(wqh::run_kv4_update_bounds(*cache, *bounds, *batch,
+                                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
+wq_status wq_kv4_select(const void* Q, int64_t q_stride, int32_t q_heads,
+                        const wq_kv4_cache* cache, const wq_kv4_bounds* bounds,
+                        const wq_kv4_batch* batch, const wq_kv4_selection* selection,
+                        wq_stream_t stream) {
+  wq_status st = check_kv4_cache(cache);
+  if (st != WQ_OK) return st;
+  if (!batch || batch->rows < 0 || q_heads < 1 || q_heads % cache->kv_heads != 0)
+    return WQ_ERR_INVALID_ARG;
+  if (batch->rows == 0) return WQ_OK;
+  if ((st = check_kv4_batch(batch)) != WQ_OK) return st;
+  if ((st = check_kv4_bounds(bounds, cache, batch)) != WQ_OK) return st;
+  if ((st = check_kv4_selection(selection, cache, batch->rows)) != WQ_OK) return st;
+  if ((st = check_kv4_choice(selection, q_heads, cache, batch)) != WQ_OK) return st;
+  if ((st = check_kv4_rows(Q, q_stride, q_heads, cache->head_dim)) != WQ_OK) return st;
+  DeviceInfo dev;
+  if (!wqh::device_info(&dev)) return WQ_ERR_CUDA;
+  return from_cuda(wqh::run_kv4_select(Q, q_stride, q_heads, *cache, *bounds, *batch, *selection,
+                                       reinterpret_cast<cudaStream_t>(stream), dev.sms));
+}
+
+wq_status wq_kv4_attention_pages(const void* Q, int64_t q_stride, int32_t q_heads,
+                                 const wq_kv4_cache* cache, int32_t rows,
+                                 const wq_kv4_selection* selection, float scale, void* O,
+                                 int64_t o_stride, void* workspace, size_t workspace_bytes,
+                                 wq_stream_t stream) {
+  wq_status st = check_kv4_cache(cache);
+  if (st != WQ_OK) return st;
+  if (rows < 0 || q_heads < 1 || q_heads % cache->kv_heads != 0 || !std::isfinite(scale))
+    return WQ_ERR_INVALID_ARG;
+  if (rows == 0) return WQ_OK;
+  if ((st = check_kv4_selection(selection, cache, rows)) != WQ_OK) return st;
+  if ((st = check_kv4_attention(Q, q_stride, q_heads, cache, rows, O, o_stride, workspace,
+                                workspace_bytes)) != WQ_OK)
+    return st;
+  DeviceInfo dev;
+  if (!wqh::device_info(&dev)) return WQ_ERR_CUDA;
+  return from_cuda(wqh::run_kv4_attention_pages(Q, q_stride, q_heads, *cache, rows, *selection,
+                                                scale, O, o_stride, workspace,
+                                                reinterpret_cast<cudaStream_t>(stream), dev));
+}
+
+wq_status wq_kv4_sparse_attention(const void* Q, int64_t q_stride, int32_t q_heads,
+                                  const wq_kv4_cache* cache, const wq_kv4_bounds* bounds,
+                                  const wq_kv4_batch* batch,
+                                  const wq_kv4_selection* selection, float scale, void* O,
+                                  int64_t o_stride, void* workspace, size_t workspace_bytes,
+                                  wq_stream_t stream) {
+  wq_status st = check_kv4_cache(cache);
+  if (st != WQ_OK) return st;
+  if (!batch || batch->rows < 0 || q_heads < 1 || q_heads % cache->kv_heads != 0 ||
+      !std::isfinite(scale))
+    return WQ_ERR_INVALID_ARG;
+  if (batch->rows == 0) return WQ_OK;
+  if ((st = check_kv4_batch(batch)) != WQ_OK) return st;
+  if ((st = check_kv4_bounds(bounds, cache, batch)) != WQ_OK) return st;
+  if ((st = check_kv4_selection(selection, cache, batch->rows)) != WQ_OK) return st;
+  if ((st = check_kv4_choice(selection, q_heads, cache, batch)) != WQ_OK) return st;
+  if ((st = check_kv4_attention(Q, q_stride, q_heads, cache, batch->rows, O, o_stride, workspace,
+                                workspace_bytes)) != WQ_OK)
+    return st;
+  DeviceInfo dev;
+  if (!wqh::device_info(&dev)) return WQ_ERR_CUDA;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((st = from_cuda(wqh::run_kv4_update_bounds(*cache, *bounds, *batch, s))) != WQ_OK) return st;
+  if ((st = from_cuda(wqh::run_kv4_select(Q, q_stride, q_heads, *cache, *bounds, *batch,
+                                          *selection, s, dev.sms))) != WQ_OK)
+    return st;
+  return from_cuda(wqh::run_kv4_attention_pages(Q, q_stride, q_heads, *cache, batch->rows,
+                                                *selection, scale, O, o_stride, workspace, s,
+                                                dev));
+}
+
+// --------------------------------------------------------- rotary positions
+
+wq_status wq_rotary_frequencies(int32_t dim, double base, int32_t scaling, double factor,
+                                double context, double low, double high, float* freqs) {
+  if (!freqs || dim < 2 || dim % 2 != 0 || !(base > 0) || !std::isfinite(base))
+    return WQ_ERR_INVALID_ARG;
+  if (scaling < WQ_ROTARY_PLAIN || scaling > WQ_ROTARY_PARTS) return WQ_ERR_INVALID_ARG;
+  if (scaling != WQ_ROTARY_PLAIN && (!(factor >= 1) || !std::isfinite(factor)))
+    return WQ_ERR_INVALID_ARG;
+  if (scaling == WQ_ROTARY_BASE) {
+    if (dim < 4) return WQ_ERR_INVALID_ARG;
+    base *= std::pow(factor, double(dim) / (dim - 2));
+  }
+  if (scaling == WQ_ROTARY_PARTS &&
+      (!(context > 0) || !std::isfinite(context) || !(low < high) || !std::isfinite(low) ||
+       !std::isfinite(high)))
+    return WQ_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / dim);
+    if (scaling == WQ_ROTARY_LINEAR) f /= factor;
+    if (scaling == WQ_ROTARY_PARTS) {
+      const double turns = context * f / 6.283185307179586;
+      const double keep = std::clamp((turns - low) / (high - low), 0.0, 1.0);
+      f *= keep + (1 - keep) / factor;
+    }
+    freqs[i] = float(f);
+  }
+  return WQ_OK;
+}
+
+wq_status wq_rotary(const void* X, int64_t x_stride, int32_t rows, int32_t heads,
+                    int32_t head_dim, const int32_t* positions, const wq_rotary_spec* spec,
+                    unsigned int flags, void* Y, int64_t y_stride, wq_stream_t stream) {
+  if (rows < 0 || heads < 1 || heads > (1 << 20) || head_dim < 1) return WQ_ERR_INVALID_ARG;
+  if ((flags & ~unsigned(WQ_ROTARY_TRANSPOSE)) != 0) return WQ_ERR_INVALID_ARG;
+  if (head_dim % 8 != 0 || head_dim > 512) return WQ_ERR_UNSUPPORTED;
+  wq_status st = check_rotary(spec, head_dim);
+  if (st != WQ_OK) return st;
+  if (rows == 0) return WQ_OK;
+  if (!positions) return WQ_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(positions) & 3u) != 0) return WQ_ERR_ALIGNMENT;
+  if ((st = check_kv4_rows(X, x_stride, heads, head_dim)) != WQ_OK) return st;
+  if ((st = check_kv4_rows(Y, y_stride, heads, head_dim)) != WQ_OK) return st;
+  if (X == Y && x_stride != y_stride && rows > 1) return WQ_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if (!wqh::device_info(&dev)) return WQ_ERR_CUDA;
+  return from_cuda(wqh::run_rotary(X, x_stride, rows, heads, head_dim, positions, *spec,
+                                   (flags & WQ_ROTARY_TRANSPOSE) != 0, Y, y_stride,
+                                   reinterpret_cast<cudaStream_t>(stream), dev.sms));
+}
+
+wq_status wq_kv4_write_rotary(const void* Q, int64_t q_stride, int32_t q_heads, void* Q_out,
+                              int64_t qo_stride, const void* K, int64_t k_stride, const void* V,
+                              int64_t v_stride, const wq_rotary_spec* spec,
+                              const int32_t* positions, const wq_kv4_cache* cache,
+                              const wq_kv4_batch* batch, wq_stream_t stream) {
+  wq_status st = check_kv4_cache(cache);
+  if (st != WQ_OK) return st;
+  if ((st = check_rotary(spec, cache->head_dim)) != WQ_OK) return st;
+  if (spec->dim % 16 != 0) return WQ_ERR_UNSUPPORTED;
+  if (!batch || batch->rows < 0 || q_heads < 0 || q_heads > (1 << 20)) return WQ_ERR_INVALID_ARG;
+  if (batch->rows == 0) return WQ_OK;
+  if ((st = check_kv4_batch(batch)) != WQ_OK) return st;
+  if (batch->rows >= (1 << 30)) return WQ_ERR_INVALID_ARG;
+  if (positions && (reinterpret_cast<uintptr_t>(positions) & 3u) != 0) return WQ_ERR_ALIGNMENT;
+  if (q_heads > 0) {
+    if ((st = check_kv4_rows(Q, q_stride, q_heads, cache->head_dim)) != WQ_OK) return st;
+    if ((st = check_kv4_rows(Q_out, qo_stride, q_heads, cache->head_dim)) != WQ_OK) return st;
+    if (Q == Q_out && q_stride != qo_stride && batch->rows > 1) return WQ_ERR_INVALID_ARG;
+  }
+  if ((st = check_kv4_rows(K, k_stride, cache->kv_heads, cache->head_dim)) != WQ_OK) return st;
+  if ((st = check_kv4_rows(V, v_stride, cache->kv_heads, cache->head_dim)) != WQ_OK) return st;
+  return from_cuda(wqh::run_kv4_write_rotary(Q, q_stride, q_heads, Q_out, qo_stride, K, k_stride,
+                                             V, v_stride, *spec, positions, *cache, *batch,
+                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// -------------------------------------------- verification of drafted tokens
+
+size_t wq_verify_workspace_bytes(int64_t rows) {
+  return rows < 1 || rows >= (int64_t(1) << 31) ? 0 : wqh::verify_workspace_bytes(rows);
+}
+
+wq_status wq_verify_drafts(const wq_verification* v, void* workspace, size_t workspace_bytes,
+                           wq_stream_t stream) {
+  if (!v || v->rows < 0) return WQ_ERR_INVALID_ARG;
+  if (v->rows == 0) return WQ_OK;
+  if (v->seqs < 1 || v->vocab < 1 || (!v->row_starts && v->rows % v->seqs != 0))
+    return WQ_ERR_INVALID_ARG;
+  if (v->dtype != WQ_OUT_F32 && v->dtype != WQ_OUT_BF16) return WQ_ERR_INVALID_ARG;
+  if ((v->flags & ~uint32_t(WQ_VERIFY_LOGITS)) != 0) return WQ_ERR_INVALID_ARG;
+  const bool logits = (v->flags & WQ_VERIFY_LOGITS) != 0;
+  if (!v->target || !v->tokens || !v->uniform || !v->out_tokens || !v->accepted ||
+      (v->out_lens && !v->seq_lens) || (v->temperature && !logits))
+    return WQ_ERR_INVALID_ARG;
+  if (v->target_stride < v->vocab || (v->draft && v->draft_stride < v->vocab))
+    return WQ_ERR_INVALID_ARG;
+  if (logits && (!workspace || workspace_bytes < wqh::verify_workspace_bytes(v->rows)))
+    return WQ_ERR_INVALID_ARG;
+  if (!aligned16(v->target) || !aligned16(v->draft) || (logits && !aligned16(workspace)))
+    return WQ_ERR_ALIGNMENT;
+  const void* const words[] = {v->row_starts, v->tokens,     v->uniform,  v->temperature,
+                               v->seq_lens,   v->out_tokens, v->accepted, v->out_lens};
+  for (const void* p : words)
+    if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return WQ_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  if (!wqh::device_info(&dev)) return WQ_ERR_CUDA;
+  return from_cuda(wqh::run_verify_drafts(*v, workspace, reinterpret_cast<cudaStream_t>(stream),
+                                          dev.sms));
 }
 
 }  // extern "C"
