@@ -17,7 +17,7 @@ template <int D, int G>
 struct WriteRotaryOp {
   static cudaError_t run(rotary::WriteParams p, const wq_kv4_cache& c, int interleaved,
                          cudaStream_t s) {
-    p.chunks = row_chunks(c);
+    p.chunks = (c.kv_heads * (D / 16) + 31) / 32;
     const int per_head = interleaved ? (p.copy_q ? D : p.spec.dim) / 8
                                      : p.spec.dim / 16 + (p.copy_q ? (D - p.spec.dim) / 8 : 0);
     const int64_t units = int64_t(p.q_heads) * per_head, share = 32 * rotary::kQueryUnits;

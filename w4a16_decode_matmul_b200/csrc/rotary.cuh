@@ -8,7 +8,7 @@
 // with a the amplitude.  The transpose (the gradient) is the same with -s.
 //
 // Roundings.  The angle is a product in binary64 (exact below 2^29 positions)
-// and goes to CUDA's binary64 sincos: a binary32 product is off by up to 2^-24 of
+// and so are sine and cosine: a binary32 product is off by up to 2^-24 of
 // itself, 0.03 radians at position 10^6.  c and s are rounded to binary32, the
 // result to bfloat16.  Between the two, queries take a multiply-add in binary32;
 // keys that go into the cache are the exact result rounded to binary32 (but for
@@ -27,12 +27,36 @@ struct Spec {
   float amplitude;
 };
 
-// (c, s) of one position and frequency.  The cost is binary64 arithmetic, paid
-// once per row and pair and shared by all heads.
+// (c, s) of one position and frequency, in binary64 arithmetic that all heads share.
+// The angle less a multiple of pi/2 that is held in two parts (W. J. Cody and W. Waite,
+// 1980), then the series of sine and cosine to the 15th and 16th power: for |r| <= pi/4
+// the next terms are below 2^-54.
 __device__ __forceinline__ float2 turn_of(int position, float freq, float amplitude) {
-  double s, c;
-  sincos(double(position) * double(freq), &s, &c);
-  return make_float2(float(double(amplitude) * c), float(double(amplitude) * s));
+  const double a = double(position) * double(freq);
+  const double k = rint(a * 0.6366197723675814);         // 2/pi
+  double r = fma(-k, 1.5707963267948966, a);             // pi/2 ...
+  r = fma(-k, 6.123233995736766e-17, r);                 // ... and the rest of it
+  const double z = r * r;
+  double s = fma(z, -1.0 / 1307674368000.0, 1.0 / 6227020800.0);
+  double c = fma(z, 1.0 / 20922789888000.0, -1.0 / 87178291200.0);
+  s = fma(s, z, -1.0 / 39916800.0);
+  c = fma(c, z, 1.0 / 479001600.0);
+  s = fma(s, z, 1.0 / 362880.0);
+  c = fma(c, z, -1.0 / 3628800.0);
+  s = fma(s, z, -1.0 / 5040.0);
+  c = fma(c, z, 1.0 / 40320.0);
+  s = fma(s, z, 1.0 / 120.0);
+  c = fma(c, z, -1.0 / 720.0);
+  s = fma(s, z, -1.0 / 6.0);
+  c = fma(c, z, 1.0 / 24.0);
+  s = fma(s * z, r, r);
+  c = fma(c, z, -0.5);
+  c = fma(c, z, 1.0);
+  const int quarter = int(__double2ll_rn(k)) & 3;
+  const double x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;
+  const double m = double(amplitude);
+  return make_float2(float(((quarter + 1) & 2) ? -(m * x) : m * x),
+                     float((quarter & 2) ? -(m * y) : m * y));
 }
 
 __device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
@@ -63,20 +87,23 @@ struct Units {
 };
 
 __device__ __forceinline__ void turn_runs(uint4& a, uint4& b, const float2* turn) {
-  uint32_t* x = &a.x;
-  uint32_t* y = &b.x;
+  uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 p = kv4::bf16x2_to_float2(x[i]), q = kv4::bf16x2_to_float2(y[i]);
-    const float2 lo = turn_pair(p.x, q.x, turn[2 * i]), hi = turn_pair(p.y, q.y, turn[2 * i + 1]);
+    const float4 t = *reinterpret_cast<const float4*>(turn + 2 * i);
+    const float2 lo = turn_pair(p.x, q.x, make_float2(t.x, t.y));
+    const float2 hi = turn_pair(p.y, q.y, make_float2(t.z, t.w));
     x[i] = pack_bf162(lo.x, hi.x);
     y[i] = pack_bf162(lo.y, hi.y);
   }
+  a = make_uint4(x[0], x[1], x[2], x[3]);
+  b = make_uint4(y[0], y[1], y[2], y[3]);
 }
 
 // Pairs side by side; the first `pairs` of the run's four turn.
 __device__ __forceinline__ void turn_interleaved(uint4& a, const float2* turn, int pairs) {
-  uint32_t* x = &a.x;
+  uint32_t x[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (i < pairs) {
@@ -84,6 +111,7 @@ __device__ __forceinline__ void turn_interleaved(uint4& a, const float2* turn, i
       const float2 y = turn_pair(p.x, p.y, turn[i]);
       x[i] = pack_bf162(y.x, y.y);
     }
+  a = make_uint4(x[0], x[1], x[2], x[3]);
 }
 
 constexpr int kMaxHead = 512;
@@ -104,8 +132,8 @@ struct RotaryParams {
 // units (blockIdx.y): the loads of each thread's first unit, the row's angles, then
 // all heads.  HBM bound, two bytes in and two out an element.
 template <bool INTERLEAVED>
-__global__ void __launch_bounds__(512) rotary_kernel(const RotaryParams p) {
-  __shared__ float2 turn[kMaxHead / 2];
+__global__ void __launch_bounds__(512, 2) rotary_kernel(const RotaryParams p) {
+  __shared__ __align__(16) float2 turn[kMaxHead / 2];
   const int64_t r = blockIdx.x;
   const Units<INTERLEAVED> u(p.spec.dim, p.head_dim, p.copy);
   const unsigned units = unsigned(p.heads) * unsigned(u.all);
@@ -148,8 +176,8 @@ __global__ void __launch_bounds__(512) rotary_kernel(const RotaryParams p) {
 
 // The same for half layouts whose halves are not whole runs of eight elements
 // (dim not a multiple of 16): a pair, or an element that stays, at a time.
-static __global__ void __launch_bounds__(512) rotary_pair_kernel(const RotaryParams p) {
-  __shared__ float2 turn[kMaxHead / 2];
+static __global__ void __launch_bounds__(512, 2) rotary_pair_kernel(const RotaryParams p) {
+  __shared__ __align__(16) float2 turn[kMaxHead / 2];
   const int64_t r = blockIdx.x;
   const int half = p.spec.dim / 2;
   const unsigned all = unsigned(half + (p.copy ? p.head_dim - 2 * half : 0));
@@ -219,6 +247,16 @@ __device__ __forceinline__ uint4 turn_keys(const uint4& x, const uint4& z, float
   return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
+// The place of a lane in a row's keys and values: 16 elements of one head, the row's
+// share of a warp being 512 elements (half of kv4.cuh's write kernel's, for its
+// registers: with 1,024 two CTAs fit an SM).
+template <int D, int G>
+struct KeyLane : kv4::RowLane<D, G> {
+  __device__ KeyLane(int lane, int share) : kv4::RowLane<D, G>(lane, 0) {
+    this->head += share * kv4::RowLane<D, G>::kHeads;
+  }
+};
+
 struct WriteParams {
   const __nv_bfloat16 *Q, *K, *V;
   int64_t q_stride, k_stride, v_stride;
@@ -228,7 +266,7 @@ struct WriteParams {
   Spec spec;
   kv4::Cache cache;
   kv4::Batch batch;
-  int q_heads, chunks;  // warps' shares of a row's keys and values
+  int q_heads, chunks;  // chunks: warps' shares of a row's keys and values
   bool copy_q;          // Q_out is other memory than Q
 };
 
@@ -236,14 +274,14 @@ constexpr int kMaxWarps = 8;
 constexpr int kQueryUnits = 2;  // units of queries a lane has in flight
 
 // Queries turned, keys turned and quantized, values quantized: one CTA a row, whose
-// angles its warps share; the first `chunks` shares are those of kv4.cuh's write
-// kernel (1,024 keys and values), the others 64 units of queries.  CTAs behind the
+// angles its warps share; the first `chunks` shares are 512 keys and values each, the
+// others 64 units of queries.  CTAs behind the
 // rows check the sequences.
 template <int D, int G, bool INTERLEAVED>
-__global__ void __launch_bounds__(kMaxWarps * 32)
+__global__ void __launch_bounds__(kMaxWarps * 32, 4)
     write_rotary_kernel(const WriteParams p, int warps_of_rows) {
-  using L = kv4::RowLane<D, G>;
-  __shared__ float2 turn[D / 2];
+  using L = KeyLane<D, G>;
+  __shared__ __align__(16) float2 turn[D / 2];
   __shared__ float4 split[D / 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   if (int(blockIdx.x) >= p.batch.rows) {
@@ -311,8 +349,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
     }
     // ---- keys and values
     const L my(lane, item);
-    constexpr int kIt = kv4::kRowIterations;
-    uint4 k[kIt][2], v[kIt][2], z[kIt][2];
+    const bool there = my.head < p.cache.kv_heads;
+    uint4 k[2], v[2], z[2];
     const __nv_bfloat16* from_k = p.K + int64_t(r) * p.k_stride + my.head * D + my.elem;
     const __nv_bfloat16* from_v = p.V + int64_t(r) * p.v_stride + my.head * D + my.elem;
     // a run of eight keys lies in the first half of the turned elements, in the
@@ -324,48 +362,39 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
       const int e = my.elem + 8 * i;
       run_at[i] = e >= p.spec.dim ? -1 : INTERLEAVED ? e / 2 : e >= u.half ? e - u.half : e;
       sign[i] = e < u.half ? 1.f : -1.f;
-    }
-#pragma unroll
-    for (int it = 0; it < kIt; ++it)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        k[it][i] = v[it][i] = z[it][i] = make_uint4(0, 0, 0, 0);
-        if (my.head + it * L::kHeads < p.cache.kv_heads) {
-          const __nv_bfloat16* at = from_k + it * (L::kHeads * D) + 8 * i;
-          k[it][i] = *reinterpret_cast<const uint4*>(at);
-          v[it][i] = *reinterpret_cast<const uint4*>(from_v + it * (L::kHeads * D) + 8 * i);
-          if (!INTERLEAVED && run_at[i] >= 0)
-            z[it][i] = *reinterpret_cast<const uint4*>(at + (sign[i] > 0.f ? u.half : -u.half));
-        }
+      k[i] = v[i] = z[i] = make_uint4(0, 0, 0, 0);
+      if (there) {
+        k[i] = *reinterpret_cast<const uint4*>(from_k + 8 * i);
+        v[i] = *reinterpret_cast<const uint4*>(from_v + 8 * i);
+        if (!INTERLEAVED && run_at[i] >= 0)
+          z[i] = *reinterpret_cast<const uint4*>(from_k + 8 * i +
+                                                 (sign[i] > 0.f ? u.half : -u.half));
       }
+    }
     make_turns();
     if (token < 0) continue;  // the row holds no token
     const int64_t page = kv4::load_page(p.batch, p.cache, b, token);
     if (page < 0) continue;
     const int slot = token & ((1 << p.cache.page_shift) - 1);
-    int64_t at = ((page * p.cache.kv_heads + my.head) << p.cache.page_shift) + slot;
+    const int64_t at = ((page * p.cache.kv_heads + my.head) << p.cache.page_shift) + slot;
 #pragma unroll
-    for (int it = 0; it < kIt; ++it) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (run_at[i] >= 0)
-          k[it][i] = turn_keys<INTERLEAVED>(k[it][i], z[it][i], sign[i], split + run_at[i]);
-      float ks, kz, vs, vz;
-      const uint2 kw = kv4::quantize16<G / 16>(k[it], &ks, &kz);
-      const uint2 vw = kv4::swap_chunks(kv4::quantize16<G / 16>(v[it], &vs, &vz), my.odd);
-      if (my.head + it * L::kHeads < p.cache.kv_heads) {
-        uint32_t* const to_k = reinterpret_cast<uint32_t*>(p.cache.k_codes + at * (D / 2));
-        uint32_t* const to_v = reinterpret_cast<uint32_t*>(p.cache.v_codes + at * (D / 2));
-        to_k[my.key_word(0)] = kw.x;
-        to_k[my.key_word(1)] = kw.y;
-        to_v[my.value_word(0)] = vw.x;
-        to_v[my.value_word(1)] = vw.y;
-        if (my.owns_meta) {
-          p.cache.k_meta[at * L::NG + my.group] = __floats2half2_rn(ks, kz);
-          p.cache.v_meta[at * L::NG + my.group] = __floats2half2_rn(vs, vz);
-        }
+    for (int i = 0; i < 2; ++i)
+      if (run_at[i] >= 0)
+        k[i] = turn_keys<INTERLEAVED>(k[i], z[i], sign[i], split + run_at[i]);
+    float ks, kz, vs, vz;
+    const uint2 kw = kv4::quantize16<G / 16>(k, &ks, &kz);
+    const uint2 vw = kv4::swap_chunks(kv4::quantize16<G / 16>(v, &vs, &vz), my.odd);
+    if (there) {
+      uint32_t* const to_k = reinterpret_cast<uint32_t*>(p.cache.k_codes + at * (D / 2));
+      uint32_t* const to_v = reinterpret_cast<uint32_t*>(p.cache.v_codes + at * (D / 2));
+      to_k[my.key_word(0)] = kw.x;
+      to_k[my.key_word(1)] = kw.y;
+      to_v[my.value_word(0)] = vw.x;
+      to_v[my.value_word(1)] = vw.y;
+      if (my.owns_meta) {
+        p.cache.k_meta[at * L::NG + my.group] = __floats2half2_rn(ks, kz);
+        p.cache.v_meta[at * L::NG + my.group] = __floats2half2_rn(vs, vz);
       }
-      at += int64_t(L::kHeads) << p.cache.page_shift;
     }
   }
 }

@@ -9,16 +9,22 @@
 // draft was rejected, from p_a where none was, by u_0: the first token whose running
 // sum passes u_0 times the whole.
 //
-// Precision.  That token is an integer, decided by a running sum over the vocabulary:
-// with an error of e of the whole, about 2 e vocabulary of all numbers u_0 lead to a
-// neighbour.  In binary32 that is a draw in a hundred.  So all masses and sums are in
-// binary64, exponentials within 2^-43 (below): one draw in 10^7.
+// Precision.  That token is an integer, decided by a running sum over the vocabulary.
+// An error of e in every mass, of either sign, puts a boundary off by e times the root
+// of the masses' squares' sum, about e / 20, so that about vocabulary e / 20 of all
+// numbers u_0 lead to a neighbour: one in a hundred with binary32's exponentials,
+// one in 10^9 with those below.  An error of the sums that p and q are divided by
+// moves all boundaries of max(p - q, 0) at once and costs twenty times as much.  So the
+// sampled row's (and its draft row's) masses and sums are in binary64, exponentials
+// within 2^-43.  A draft's acceptance has one border: there the sums of exponentials
+// are binary32's, added in binary64 from 32 terms on, off by some 10^-7.
 //
 // Two kernels.  Logits first go through stats_kernel: largest logit and sum of
 // exponentials of every piece of every row, which reads each row once.  verify_kernel,
-// a cluster per sequence, joins the pieces, accepts, and samples: each warp sums its
-// share of the one row (and draft row) that is left, and the warp in whose share the
-// number falls looks for it.  Probabilities need no statistics and no first kernel.
+// a cluster per sequence, joins the pieces, accepts, and samples: where max(p - q, 0)
+// is needed it forms the two rows' sums again in binary64, then each warp sums its share
+// of the masses, and the warp in whose share the number falls looks for the token.
+// Probabilities need no statistics and no first kernel.
 #pragma once
 
 #include "common.cuh"
@@ -69,45 +75,59 @@ __device__ __forceinline__ Rows load_rows(const Params& p, int b) {
   return {first, end - first};
 }
 
-// ---- exponentials.  2^(k/64 + r) = 2^(k div 64) 2^((k mod 64)/64) 2^r with the table
-// of 64 powers in shared memory and 2^r, |r| <= 1/128, by its series to r^4: the next
-// term is (r ln 2)^5 / 120 < 2^-44.  Table-driven exponentials: P. T. P. Tang, ACM TOMS
-// 15 (1989).
+// ---- exponentials.  exp(d / temperature) = 2^(k/64) 2^(r/64), |r| <= 1/2: the table's
+// 2^((k mod 64)/64), shared memory, times the exponent k div 64 and the series of 2^(r/64)
+// to r^4: the next term is (r ln 2 / 64)^5 / 120 < 2^-44.  Table-driven exponentials:
+// P. T. P. Tang, ACM TOMS 15 (1989).
 struct Exp {
   const double* table;  // 2^(j/64)
   double scale;         // 64 log2(e) / temperature
-  // exp(d / temperature) for d <= 0; 0 for d = -inf, a NaN, and results below 2^-1000
-  __device__ __forceinline__ double operator()(double d) const {
-    const double t = d * scale;
-    if (!(t > -64000.0)) return 0.0;
-    const double magic = 6755399441055744.0;  // 1.5 * 2^52
-    const double shifted = t + magic;
+  double top;           // the largest logit
+  float cut;            // logits below it (or NaN) have no mass: less than 2^-995 of the largest's
+  __device__ __forceinline__ double operator()(float x) const {
+    const double d = double(fmaxf(x, cut)) - top;
+    const double magic = 6755399441055744.0;  // 1.5 * 2^52: rounds to an integer, the low word
+    const double shifted = fma(d, scale, magic);
     const int k = __double2loint(shifted);
-    const double r = (t - (shifted - magic)) * (0.6931471805599453 / 64);  // times ln 2
-    double e = fma(r, 1.0 / 24, 1.0 / 6);
-    e = fma(e, r, 0.5);
-    e = fma(e, r, 1.0);
+    const double r = fma(d, scale, magic - shifted);
+    constexpr double c = 0.6931471805599453 / 64;  // ln 2 / 64
+    double e = fma(r, c * c * c * c / 24, c * c * c / 6);
+    e = fma(e, r, c * c / 2);
+    e = fma(e, r, c);
     const double base = table[k & 63];
     e = fma(e * r, base, base);
-    return __hiloint2double(__double2hiint(e) + ((k >> 6) << 20), __double2loint(e));
+    const double y =
+        __hiloint2double(__double2hiint(e) + (k & ~63) * (1 << 14), __double2loint(e));
+    return x >= cut ? y : 0.0;
   }
 };
+
+__device__ __forceinline__ Exp make_exp(const double* table, float top, float hot) {
+  const float cut = fmaxf(top - 690.f * hot, -3.4028234e38f);
+  return {table, 64 * 1.4426950408889634 / double(hot), double(top), cut};
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 __device__ __forceinline__ void fill_table(double* table) {
   if (threadIdx.x < 64) table[threadIdx.x] = exp2(double(threadIdx.x) * (1.0 / 64));
 }
 
-// A distribution over one row.
+// A distribution over one row.  kShared: all logits of +infinity have the same mass.
 struct Mass {
-  enum Kind { kNone, kProbabilities, kLogits, kOne };
+  enum Kind { kNone, kProbabilities, kLogits, kShared, kOne };
   Kind kind;
-  float top;
+  int one;         // kOne: the token that has all
   double inverse;  // of the sum
-  int one;         // kOne: the token that has all (or -1)
   Exp exp;
   __device__ __forceinline__ double operator()(float x, int i) const {
     if (kind == kProbabilities) return x > 0.f ? double(x) : 0.0;
-    if (kind == kLogits) return exp(x == top ? 0.0 : double(x) - double(top)) * inverse;
+    if (kind == kLogits) return exp(x) * inverse;
+    if (kind == kShared) return x == INFINITY ? inverse : 0.0;
     return kind == kOne && i == one ? 1.0 : 0.0;
   }
 };
@@ -161,7 +181,6 @@ __device__ __forceinline__ int row_lead(const T* row) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) stats_kernel(const Params p) {
   constexpr int N = 16 / int(sizeof(T)), kRuns = kPerThread / N;
-  __shared__ double table[64];
   __shared__ double sums[kThreads / 32];
   __shared__ float tops[kThreads / 32];
   __shared__ int firsts[kThreads / 32];
@@ -199,19 +218,19 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const Params p) {
                                 : static_cast<const T*>(p.target) + int64_t(r) * p.target_stride;
   const int64_t begin = int64_t(piece) * p.piece - row_lead(row);
   const int64_t end = min(begin + p.piece, int64_t(p.vocab));
-  fill_table(table);
-  __syncthreads();
-  const Exp exp = {table, 64 * 1.4426950408889634 / double(hot)};
+  // log2(e) / temperature in two parts: a binary32 product would be off by 2^-24 of the
+  // exponent, for all terms in the same direction
+  const double log2_unit = fmin(fmax(1.4426950408889634 / double(hot), 1e-30), 1e30);
+  const float unit = float(log2_unit), unit_low = float(log2_unit - double(unit));
+  const float lowest = -200.f / unit;  // 2^-200: nothing in binary32
   double sum = 0.0;
   float top = -INFINITY;
   int first = 0x7fffffff;
   for (int64_t tile = begin; tile < end; tile += kTile) {
     float x[kRuns][N];
 #pragma unroll
-    for (int k = 0; k < kRuns; ++k) {
-      const int64_t at = tile + (k * kThreads + tid) * N;
-      load_run<T, N>(row, at, end, -INFINITY, x[k]);
-    }
+    for (int k = 0; k < kRuns; ++k)
+      load_run<T, N>(row, tile + (k * kThreads + tid) * N, end, -INFINITY, x[k]);
     float high = -INFINITY;
 #pragma unroll
     for (int k = 0; k < kRuns; ++k)
@@ -229,17 +248,28 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const Params p) {
       continue;
     }
     // each thread relative to its own largest
-    const float next = fmaxf(top, high);
-    if (next == -INFINITY) continue;
-    if (next > top) {
-      sum *= exp(top == -INFINITY ? -INFINITY : double(top) - double(next));
-      top = next;
+    if (fmaxf(top, high) == -INFINITY) continue;
+    if (high > top) {
+      sum *= double(exp2_approx(fmaxf(top - high, lowest) * unit));
+      top = high;
     }
+    float part[4] = {0.f, 0.f, 0.f, 0.f};
+    if (top == INFINITY) {
 #pragma unroll
-    for (int k = 0; k < kRuns; ++k)
+      for (int k = 0; k < kRuns; ++k)
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        sum += exp(x[k][i] == top ? 0.0 : double(x[k][i]) - double(top));
+        for (int i = 0; i < N; ++i) part[i & 3] += x[k][i] == INFINITY ? 1.f : 0.f;
+    } else {
+#pragma unroll
+      for (int k = 0; k < kRuns; ++k)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float d = fmaxf(x[k][i] - top, lowest);
+          const float e = exp2_approx(fmaf(d, unit, d * unit_low));
+          part[i & 3] += x[k][i] >= -3.4028234e38f ? e : 0.f;
+        }
+    }
+    sum += double((part[0] + part[1]) + (part[2] + part[3]));
   }
   // ---- the CTA's
   float high = top;
@@ -250,10 +280,7 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const Params p) {
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) high = fmaxf(high, tops[w]);
   int at = top == high ? first : 0x7fffffff;
-  if (greedy || high == -INFINITY)
-    sum = 0.0;
-  else
-    sum *= exp(top == high ? 0.0 : double(top) - double(high));
+  if (top != high) sum *= double(exp2_approx(fmaxf(top - high, lowest) * unit));
 #pragma unroll
   for (int m = 1; m < 32; m *= 2) {
     sum += __shfl_xor_sync(0xffffffffu, sum, m);
@@ -271,8 +298,8 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const Params p) {
 }
 
 // The distribution of a row from its pieces, by all lanes of a warp.
-__device__ __forceinline__ Mass join_pieces(const Params& p, bool is_draft, int r, bool greedy,
-                                            const Exp& exp, int lane) {
+__device__ __forceinline__ Mass join_pieces(const Params& p, bool is_draft, int r, float hot,
+                                            const double* table, int lane) {
   const Piece* from = p.pieces + (int64_t(is_draft ? p.rows : 0) + r) * kPieces;
   Piece mine[kPieces / 32];
   float top = -INFINITY;
@@ -289,22 +316,26 @@ __device__ __forceinline__ Mass join_pieces(const Params& p, bool is_draft, int 
   }
 #pragma unroll
   for (int m = 1; m < 32; m *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+  const Exp exp = make_exp(table, top, hot);
   double sum = 0.0;
   int first = 0x7fffffff;
 #pragma unroll
   for (int k = 0; k < kPieces / 32; ++k) {
-    if (mine[k].top == top) first = min(first, mine[k].first);
-    if (mine[k].top != -INFINITY)
-      sum += mine[k].sum * exp(mine[k].top == top ? 0.0 : double(mine[k].top) - double(top));
+    if (mine[k].top == top) {
+      first = min(first, mine[k].first);
+      sum += mine[k].sum;
+    } else if (hot > 0.f) {
+      sum += mine[k].sum * exp(mine[k].top);
+    }
   }
 #pragma unroll
   for (int m = 1; m < 32; m *= 2) {
     sum += __shfl_xor_sync(0xffffffffu, sum, m);
     first = min(first, __shfl_xor_sync(0xffffffffu, first, m));
   }
-  if (top == -INFINITY) return {Mass::kNone, top, 0.0, -1, exp};
-  if (greedy) return {Mass::kOne, top, 1.0, first, exp};
-  return {Mass::kLogits, top, 1.0 / sum, -1, exp};
+  if (top == -INFINITY) return {Mass::kNone, -1, 0.0, exp};
+  if (!(hot > 0.f)) return {Mass::kOne, first, 1.0, exp};
+  return {top == INFINITY ? Mass::kShared : Mass::kLogits, -1, 1.0 / sum, exp};
 }
 
 // A uniform number as it is used: inside [0, 1), a NaN as 0.
@@ -339,8 +370,9 @@ template <typename T, bool LOGITS>
 __global__ void __launch_bounds__(kSampleThreads) verify_kernel(const Params p) {
   constexpr int N = 16 / int(sizeof(T));
   __shared__ double table[64];
-  __shared__ double sums[kSampleWarps];  // of the warps' shares
-  __shared__ double cta_sum;
+  // sums of the warps' shares, and of the CTA's: of both rows, of the masses that are
+  // left, of the target's
+  __shared__ double sums[4][kSampleWarps], cta_sum[4];
   __shared__ int rejected;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = p.ctas > 1 ? int(cluster_ctarank()) : 0;
@@ -357,23 +389,23 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(const Params p) 
   if (tid == 0) rejected = rows.count - 1;
   const float hot = LOGITS && p.temperature != nullptr ? p.temperature[b] : 1.f;
   const bool greedy = !(hot > 0.f);
-  const Exp exp = {table, 64 * 1.4426950408889634 / double(hot)};
+  const Exp no_exp = {};
   __syncthreads();
   if (LOGITS) grid_dependency_wait();
 
   auto target_row = [&](int r) { return static_cast<const T*>(p.target) + r * p.target_stride; };
   auto draft_row = [&](int r) { return static_cast<const T*>(p.draft) + r * p.draft_stride; };
   auto target_mass = [&](int r) -> Mass {
-    if (!LOGITS) return {Mass::kProbabilities, 0.f, 1.0, -1, exp};
-    return join_pieces(p, false, r, greedy, exp, lane);
+    if (!LOGITS) return {Mass::kProbabilities, -1, 1.0, no_exp};
+    return join_pieces(p, false, r, hot, table, lane);
   };
   auto draft_mass = [&](int r, int token) -> Mass {
-    if (p.draft == nullptr) return {Mass::kOne, 0.f, 1.0, token, exp};
-    if (!LOGITS) return {Mass::kProbabilities, 0.f, 1.0, -1, exp};
+    if (p.draft == nullptr) return {Mass::kOne, token, 1.0, no_exp};
+    if (!LOGITS) return {Mass::kProbabilities, -1, 1.0, no_exp};
     // greedy: whatever the draft's distribution, the token is accepted if it is the
     // target's, and what is left is the target's
-    if (greedy) return {Mass::kOne, 0.f, 1.0, token, exp};
-    return join_pieces(p, true, r, greedy, exp, lane);
+    if (greedy) return {Mass::kOne, token, 1.0, no_exp};
+    return join_pieces(p, true, r, hot, table, lane);
   };
 
   // ---- drafts
@@ -402,14 +434,14 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(const Params p) 
   }
 
   // ---- the token behind them
-  const Mass target = target_mass(at);
+  Mass target = target_mass(at);
   if (target.kind == Mass::kNone || target.kind == Mass::kOne) {
     if (rank == 0 && tid == 0) p.out_tokens[at] = target.one;
     return;
   }
   const T* const row = target_row(at);
   const T* other = nullptr;
-  Mass draft = {Mass::kNone, 0.f, 0.0, -1, exp};
+  Mass draft = {Mass::kNone, -1, 0.0, no_exp};
   if (refused) {
     draft = draft_mass(at + 1, p.tokens[at + 1]);
     if (draft.kind != Mass::kOne) other = draft_row(at + 1);
@@ -434,8 +466,62 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(const Params p) 
         m[k] = fmax(m[k] - draft(other != nullptr ? y[k] : 0.f, int(i) + k), 0.0);
     }
   };
+  // What the CTA's warps and the cluster's CTAs hold of one sum: this CTA's warps' in
+  // sums[which], all CTAs' in cta_sums, and their total.
+  auto exchange = [&](double sum, int which, double (&all)[kMaxCluster]) -> double {
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    if (lane == 0) sums[which][warp] = sum;
+    __syncthreads();
+    if (tid == 0) {
+      double s = 0.0;
+      for (int w = 0; w < kSampleWarps; ++w) s += sums[which][w];
+      cta_sum[which] = s;
+    }
+    double total = 0.0;
+    if (p.ctas > 1) {
+      cluster_sync();
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        all[c] = c < p.ctas
+                     ? ld_dsmem_f64(map_to_rank(smem_addr(&cta_sum[which]), uint32_t(c)))
+                     : 0.0;
+        total += all[c];
+      }
+    } else {
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) all[c] = c == 0 ? cta_sum[which] : 0.0;
+      total = all[0];
+    }
+    return total;
+  };
+  auto leave = [&] {  // no CTA ends while its sums are read
+    if (p.ctas > 1) cluster_sync();
+  };
+  double cta_sums[kMaxCluster];
+  // ---- both rows' sums, where one is taken from the other; alone a row's masses may
+  // keep any common factor
+  if (LOGITS && other != nullptr) {
+    target.inverse = draft.inverse = 1.0;
+    double sum_p = 0.0, sum_q = 0.0;
+    for (int64_t i = begin + lane * N; i < end; i += 32 * N) {
+      float x[N];
+      load_run<T, N>(row, i, end, -INFINITY, x);
+#pragma unroll
+      for (int k = 0; k < N; ++k) sum_p += target(x[k], int(i) + k);
+      load_run<T, N>(other, i, end, -INFINITY, x);
+#pragma unroll
+      for (int k = 0; k < N; ++k) sum_q += draft(x[k], int(i) + k);
+    }
+    target.inverse = 1.0 / exchange(sum_p, 0, cta_sums);
+    sum_q = exchange(sum_q, 1, cta_sums);
+    draft.inverse = sum_q > 0.0 ? 1.0 / sum_q : 0.0;
+  } else if (target.kind == Mass::kLogits) {
+    target.inverse = 1.0;
+  }
   bool less = refused;
-  while (true) {
+  for (int round = 2;; ++round) {
     double sum = 0.0;
     for (int64_t i = begin + lane * N; i < end; i += 32 * N) {
       double m[N];
@@ -443,48 +529,28 @@ __global__ void __launch_bounds__(kSampleThreads) verify_kernel(const Params p) 
 #pragma unroll
       for (int k = 0; k < N; ++k) sum += m[k];
     }
-#pragma unroll
-    for (int m = 1; m < 32; m *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    __syncthreads();  // the sums of a first round have been read
-    if (lane == 0) sums[warp] = sum;
-    __syncthreads();
-    if (tid == 0) {
-      double s = 0.0;
-      for (int w = 0; w < kSampleWarps; ++w) s += sums[w];
-      cta_sum = s;
-    }
-    double before = 0.0, total = 0.0, cta_sums[kMaxCluster];
-    if (p.ctas > 1) {
-      cluster_sync();
-#pragma unroll
-      for (int c = 0; c < kMaxCluster; ++c) {
-        cta_sums[c] =
-            c < p.ctas ? ld_dsmem_f64(map_to_rank(smem_addr(&cta_sum), uint32_t(c))) : 0.0;
-        if (c < rank) before += cta_sums[c];
-        total += cta_sums[c];
-      }
-      cluster_sync();  // read before it is written again, or a CTA ends
-    } else {
-      __syncthreads();
-#pragma unroll
-      for (int c = 1; c < kMaxCluster; ++c) cta_sums[c] = 0.0;
-      total = cta_sums[0] = cta_sum;
-    }
+    const double total = exchange(sum, round, cta_sums);
     if (!(total > 0.0)) {
       if (less) {  // nothing is left: the target's own distribution
         less = false;
         continue;
       }
       if (rank == 0 && tid == 0) p.out_tokens[at] = -1;
+      leave();
       return;
     }
+    leave();
     // ---- the share in which u_0 of the whole falls: the first whose end passes it (the
     // last with any mass, should a rounding leave none), CTAs first, then their warps.
     // All compute the same ends in the same order, so exactly one share is chosen.
     const double wanted = uniform_of(p.uniform[rows.first]) * total;
+    double before = 0.0;
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c)
+      if (c < rank) before += cta_sums[c];
     if (owner_of<kMaxCluster>(wanted, 0.0, [&](int c) { return cta_sums[c]; }) != rank) return;
-    if (owner_of<kSampleWarps>(wanted, before, [&](int w) { return sums[w]; }) != warp) return;
-    for (int w = 0; w < warp; ++w) before += sums[w];
+    if (owner_of<kSampleWarps>(wanted, before, [&](int w) { return sums[round][w]; }) != warp) return;
+    for (int w = 0; w < warp; ++w) before += sums[round][w];
     double upto = before;
     int found = -1, latest = -1;
     for (int64_t base = begin; base < end && found < 0; base += 32 * N) {
