@@ -522,7 +522,7 @@ enum {
 };
 
 typedef struct wq_verification {
-    int32_t rows, seqs, vocab;  /* vocab >= 1                                    */
+    int32_t rows, seqs, vocab;  /* vocab 1 .. 2^30                               */
     int32_t dtype;              /* of target and draft: WQ_OUT_F32, WQ_OUT_BF16  */
     uint32_t flags;             /* 0 or WQ_VERIFY_LOGITS                         */
     const int32_t *row_starts;  /* [seqs + 1] as in wq_kv4_batch, or NULL        */
@@ -549,13 +549,14 @@ typedef struct wq_verification {
                                  * rows, where the next wq_kv4_write goes on     */
 } wq_verification;
 
-/* Bytes of the workspace of a call with WQ_VERIFY_LOGITS (any contents, 16-byte
+/* Bytes of the workspace of a call with that many rows or fewer (any contents, 16-byte
  * aligned; calls that may run at the same time need different ones). */
 size_t wq_verify_workspace_bytes(int64_t rows);
 
-/* All masses and sums in binary64 (exponentials within 2^-43), so that the tokens are
- * those of exact arithmetic unless a number falls within 10^-12 of a border.
- * Probabilities need not sum to 1; negative ones and NaN count as 0, NaN logits as
+/* Masses that a token is sampled from and their sums are binary64 (exponentials within
+ * 2^-43): the token is that of exact arithmetic unless uniform_0 is within 10^-12 of a
+ * border.  A draft's p and q are those of probabilities exactly; of logits their
+ * sums of exponentials are good to 4 10^-7.  Probabilities need not sum to 1; negative ones and NaN count as 0, NaN logits as
  * -infinity; of logits of +infinity each has the same mass; a row without any mass
  * gives the token -1.  A sequence without rows gets accepted 0; rows behind the last
  * sequence are left as they were.  Two sequences' rows may not overlap.  Outputs may

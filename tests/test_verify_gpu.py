@@ -115,7 +115,8 @@ def make(seed, rows, vocab, dtype, hot=None, noise=0.5, behind=0, pad=0):
 SHAPES = [  # rows of the sequences, vocabulary, padding of a row
     ([1], 1, 0), ([2], 2, 0), ([5], 32000, 0), ([1, 4, 0, 7, 2, 1], 1003, 0), ([6] * 9, 8191, 0),
     ([3, 5], 8193, 5), ([4, 1, 6], 50021, 0), ([2, 3], 131072, 16), ([20], 300, 0),
-    ([3] * 70, 777, 2), ([2], 600_001, 0),
+    ([3] * 70, 777, 2), ([2], 600_001, 0), ([4] * 30, 50021, 0), ([3, 1, 0, 5, 2] * 8, 8193, 3),
+    ([2] * 24, 131072, 0), ([35, 70, 33, 34], 200, 0),
 ]
 
 
@@ -230,6 +231,10 @@ def test_masked_and_infinite_logits(dtype, hot):
     uniform[4], uniform[5] = 0.4, 0.6
     got, want = run(target, tokens, uniform, None, rows, True, torch.full((8,), hot, device="cuda"))
     assert got == want
+    # the same among many sequences, which take other kernels
+    many, _ = run(target.repeat(4, 1), tokens.repeat(4), uniform.repeat(4), None, rows * 4, True,
+                  torch.full((32,), hot, device="cuda"))
+    assert many[0] == got[0] * 4
     assert got[0][:2] == [-1, -1] and got[0][3] == 0 and got[0][7] == vocab - 1
     assert got[0][4:6] == ([17, 8500] if hot else [17, 17])
 
@@ -248,6 +253,26 @@ def test_rows_without_mass_and_equal_distributions():
     got, want = run(p, tokens, uniform, q, rows, logits=False)
     assert got == want
     assert got[0] == [13, -1, 700, -1, -1] and got[1] == [0, 0, 0]
+    many, _ = run(p.repeat(9, 1), tokens.repeat(9), uniform.repeat(9), q.repeat(9, 1), rows * 9,
+                  logits=False)
+    assert many[0] == got[0] * 9
+
+
+@pytest.mark.parametrize("seqs", [3, 40])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("changed", [0, 1, 500])
+def test_drafts_close_to_the_target(seqs, dtype, changed):
+    """Draft logits that are the target's but for a few tokens: p and q differ by a constant
+    factor close to 1 almost everywhere, on either side of it."""
+    rows, vocab = [2] * seqs, 4001
+    target, _, tokens, uniform = make(21, rows, vocab, dtype)
+    draft = target.roll(1, 0).clone()
+    for i in range(changed):
+        draft[1::2, (37 * i) % vocab] -= 0.001 * (i + 1) if i % 2 else -2.0
+    tokens[1::2] = 0 if changed == 1 else 37
+    uniform[1::2] = 1 - 2.0 ** -24                    # refused unless p >= q
+    got, want = run(target, tokens, uniform, draft, rows)
+    assert got == want
 
 
 @pytest.mark.parametrize("hot", [1e-3, 30.0, float("inf")])

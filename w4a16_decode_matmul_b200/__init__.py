@@ -869,7 +869,7 @@ def kv4_write_rotary(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, c
 
 
 def verify_workspace(rows: int, device: torch.device | str = "cuda") -> torch.Tensor:
-    """A workspace of ``verify_drafts`` for up to ``rows`` rows of logits.  One serves
+    """A workspace of ``verify_drafts`` for up to ``rows`` rows.  One serves
     all calls of a stream; calls that may run at the same time need one each."""
     return torch.empty(lib.wq_verify_workspace_bytes(rows), dtype=torch.uint8, device=device)
 
@@ -913,7 +913,7 @@ def verify_drafts(target: torch.Tensor, tokens: torch.Tensor, uniform: torch.Ten
     Returns (tokens int32 [rows]: the accepted drafts, the sampled token, -1s; accepted
     int32 [seqs]; ``seq_lens`` without the rejected rows, or None).  ``out`` is those
     three tensors; rows behind the last sequence are left as they were (-1 without
-    it).  ``workspace`` (``verify_workspace``) is used for logits; without it each call
+    it).  ``workspace`` is a ``verify_workspace`` that the caller keeps; without it each call
     makes its own."""
     if target.dtype is not torch.float32 and target.dtype is not _BF16 or target.dim() != 2:
         raise ValueError("target must be float32 or bfloat16 [rows, vocab]")
@@ -934,10 +934,9 @@ def verify_drafts(target: torch.Tensor, tokens: torch.Tensor, uniform: torch.Ten
         out = (torch.full((rows,), -1, dtype=_I32, device=target.device),
                torch.empty((seqs,), dtype=_I32, device=target.device),
                None if seq_lens is None else torch.empty_like(seq_lens))
-    if logits and workspace is None:
+    if workspace is None:
         workspace = verify_workspace(max(rows, 1), target.device)
-    if workspace is not None and (workspace.get_device() != index
-                                  or not workspace.is_contiguous()):
+    elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on target's device")
     if (out[2] is None) != (seq_lens is None):
         raise ValueError("seq_lens and out[2] go together")
@@ -953,9 +952,8 @@ def verify_drafts(target: torch.Tensor, tokens: torch.Tensor, uniform: torch.Ten
         _words(out[0], _I32, n_shape, index, "out[0]"),
         _words(out[1], _I32, b_shape, index, "out[1]"),
         _words(out[2], _I32, b_shape, index, "out[2]"))
-    _on(index, lib.wq_verify_drafts, "wq_verify_drafts", v,
-        0 if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.nbytes)
+    _on(index, lib.wq_verify_drafts, "wq_verify_drafts", v, workspace.data_ptr(),
+        workspace.nbytes)
     return out
 
 

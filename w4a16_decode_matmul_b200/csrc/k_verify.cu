@@ -10,52 +10,84 @@ namespace {
 
 namespace verify = wq::verify;
 
-template <typename T>
-cudaError_t launch(verify::Params p, bool logits, cudaStream_t s, int sms) {
-  constexpr int N = 16 / int(sizeof(T));
-  // CTAs of a sequence: one for 4,096 tokens, as long as all are on the GPU at once
-  p.ctas = 1;
-  while (p.ctas < verify::kMaxCluster && p.ctas * 4096 < p.vocab &&
-         int64_t(p.seqs) * p.ctas < 2 * sms)
-    p.ctas *= 2;
-  const int64_t clusters = int64_t(p.seqs) * p.ctas;
-  if (clusters >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  if (logits) {
-    // rows that do not begin on a 16-byte boundary have up to N - 1 elements in front
-    const int64_t tiles = (int64_t(p.vocab) + N - 1 + verify::kTile - 1) / verify::kTile;
-    const int64_t each = (tiles + verify::kPieces - 1) / verify::kPieces;
+// One launch, as a programmatic dependent of the one before where `after` is true, in
+// clusters of `cluster` CTAs.
+template <class Kernel>
+cudaError_t launch_one(Kernel kernel, const verify::Params& p, int64_t ctas, int threads,
+                       int cluster, bool after, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(ctas));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  if (cluster > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs++].val.clusterDim = {unsigned(cluster), 1, 1};
+  }
+  if (after) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cfg.attrs = attr;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <typename T, bool LOGITS>
+cudaError_t launch(verify::Params p, cudaStream_t s, int sms) {
+  constexpr int N = 16 / int(sizeof(T)), kStep = 32 * N;
+  // rows that do not begin on a 16-byte boundary have up to N - 1 elements in front
+  const int64_t most = int64_t(p.vocab) + N - 1;
+  if (LOGITS) {
+    const int64_t each = ((most + verify::kTile - 1) / verify::kTile + verify::kPieces - 1) /
+                         verify::kPieces;
     p.piece = int(each * verify::kTile);
-    const bool aligned = p.target_stride % N == 0 && (p.draft == nullptr || p.draft_stride % N == 0);
-    p.n_pieces = int((int64_t(p.vocab) + (aligned ? 0 : N - 1) + p.piece - 1) / p.piece);
+    const bool aligned =
+        p.target_stride % N == 0 && (p.draft == nullptr || p.draft_stride % N == 0);
+    p.n_pieces = int(((aligned ? p.vocab : most) + p.piece - 1) / p.piece);
     const int64_t ctas = int64_t(p.n_pieces) * p.rows * (p.draft != nullptr ? 2 : 1);
     if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     verify::stats_kernel<T><<<unsigned(ctas), verify::kThreads, 0, s>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(clusters));
-  cfg.blockDim = dim3(verify::kSampleThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  if (p.ctas > 1) {
-    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-    attr[cfg.numAttrs++].val.clusterDim = {unsigned(p.ctas), 1, 1};
+  if (int64_t(p.seqs) * verify::kMaxCluster <= sms) {
+    p.ctas = 1;
+    while (p.ctas < verify::kMaxCluster && p.ctas * 4096 < p.vocab) p.ctas *= 2;
+    return launch_one(verify::verify_kernel<T, LOGITS, 16>, p, int64_t(p.seqs) * p.ctas, 512,
+                      p.ctas, LOGITS, s);
   }
-  if (logits) {
-    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  cfg.attrs = attr;
-  return logits ? cudaLaunchKernelEx(&cfg, verify::verify_kernel<T, true>, p)
-                : cudaLaunchKernelEx(&cfg, verify::verify_kernel<T, false>, p);
+  p.share = int(std::max<int64_t>(verify::kShareLeast,
+                                  ((most + verify::kShares - 1) / verify::kShares + kStep - 1) /
+                                      kStep * kStep));
+  p.n_shares = int((most + p.share - 1) / p.share);
+  const int64_t ctas =
+      int64_t(p.seqs) * ((p.n_shares + verify::kShareWarps - 1) / verify::kShareWarps);
+  if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+  cudaError_t e = launch_one(verify::decide_kernel<T, LOGITS>, p, p.seqs,
+                             verify::kDecideWarps * 32, 1, LOGITS, s);
+  if (e == cudaSuccess)
+    e = launch_one(verify::share_kernel<T, LOGITS>, p, ctas, verify::kShareWarps * 32, 1, true, s);
+  if (e == cudaSuccess)
+    e = launch_one(verify::find_kernel<T, LOGITS>, p, p.seqs, verify::kFindWarps * 32, 1, true, s);
+  return e;
+}
+
+// Where the parts of the workspace begin.
+struct Workspace {
+  size_t decisions, shares, bytes;
+};
+
+Workspace layout(int64_t rows) {
+  Workspace w;
+  w.decisions = size_t(rows) * 2 * verify::kPieces * sizeof(verify::Piece);
+  w.shares = w.decisions + round_up(size_t(rows) * sizeof(verify::Decision), 16);
+  w.bytes = w.shares + size_t(rows) * verify::kShares * sizeof(verify::Share);
+  return w;
 }
 
 }  // namespace
 
-size_t verify_workspace_bytes(int64_t rows) {
-  return size_t(rows) * 2 * verify::kPieces * sizeof(verify::Piece);
-}
+size_t verify_workspace_bytes(int64_t rows) { return layout(rows).bytes; }
 
 cudaError_t run_verify_drafts(const wq_verification& v, void* workspace, cudaStream_t s,
                               int sms) {
@@ -72,7 +104,11 @@ cudaError_t run_verify_drafts(const wq_verification& v, void* workspace, cudaStr
   p.out_tokens = v.out_tokens;
   p.accepted = v.accepted;
   p.out_lens = v.out_lens;
-  p.pieces = static_cast<verify::Piece*>(workspace);
+  const Workspace w = layout(v.rows);
+  unsigned char* const base = static_cast<unsigned char*>(workspace);
+  p.pieces = reinterpret_cast<verify::Piece*>(base);
+  p.decisions = reinterpret_cast<verify::Decision*>(base + w.decisions);
+  p.shares = reinterpret_cast<verify::Share*>(base + w.shares);
   p.rows = v.rows;
   p.seqs = v.seqs;
   p.rows_per_seq = v.row_starts ? 0 : v.rows / v.seqs;
@@ -80,8 +116,9 @@ cudaError_t run_verify_drafts(const wq_verification& v, void* workspace, cudaStr
   p.status = status_address();
   if (p.status == nullptr) return cudaErrorInitializationError;
   const bool logits = (v.flags & WQ_VERIFY_LOGITS) != 0;
-  return v.dtype == WQ_OUT_BF16 ? launch<__nv_bfloat16>(p, logits, s, sms)
-                                : launch<float>(p, logits, s, sms);
+  if (v.dtype == WQ_OUT_BF16)
+    return logits ? launch<__nv_bfloat16, true>(p, s, sms) : launch<__nv_bfloat16, false>(p, s, sms);
+  return logits ? launch<float, true>(p, s, sms) : launch<float, false>(p, s, sms);
 }
 
 }  // namespace wqh

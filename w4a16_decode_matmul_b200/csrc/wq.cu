@@ -807,7 +807,7 @@ wq_status wq_verify_drafts(const wq_verification* v, void* workspace, size_t wor
                            wq_stream_t stream) {
   if (!v || v->rows < 0) return WQ_ERR_INVALID_ARG;
   if (v->rows == 0) return WQ_OK;
-  if (v->seqs < 1 || v->vocab < 1 || (!v->row_starts && v->rows % v->seqs != 0))
+  if (v->seqs < 1 || v->vocab < 1 || v->vocab > (1 << 30) || (!v->row_starts && v->rows % v->seqs != 0))
     return WQ_ERR_INVALID_ARG;
   if (v->dtype != WQ_OUT_F32 && v->dtype != WQ_OUT_BF16) return WQ_ERR_INVALID_ARG;
   if ((v->flags & ~uint32_t(WQ_VERIFY_LOGITS)) != 0) return WQ_ERR_INVALID_ARG;
@@ -817,9 +817,9 @@ wq_status wq_verify_drafts(const wq_verification* v, void* workspace, size_t wor
     return WQ_ERR_INVALID_ARG;
   if (v->target_stride < v->vocab || (v->draft && v->draft_stride < v->vocab))
     return WQ_ERR_INVALID_ARG;
-  if (logits && (!workspace || workspace_bytes < wqh::verify_workspace_bytes(v->rows)))
+  if (!workspace || workspace_bytes < wqh::verify_workspace_bytes(v->rows))
     return WQ_ERR_INVALID_ARG;
-  if (!aligned16(v->target) || !aligned16(v->draft) || (logits && !aligned16(workspace)))
+  if (!aligned16(v->target) || !aligned16(v->draft) || !aligned16(workspace))
     return WQ_ERR_ALIGNMENT;
   const void* const words[] = {v->row_starts, v->tokens,     v->uniform,  v->temperature,
                                v->seq_lens,   v->out_tokens, v->accepted, v->out_lens};
