@@ -405,7 +405,7 @@ wq_status wq_kv4_update_bounds(const wq_kv4_cache *cache, const wq_kv4_bounds *b
  * q_heads a multiple of kv_heads, at most 256 times; 0 <= first, 1 <= last, first +
  * last <= max_pages.  Errors as wq_kv4_attention, and WQ_ERR_INVALID_ARG for the
  * selection's sizes, WQ_ERR_UNSUPPORTED for a larger group and for a table_width
- * above 425,984 pages. */
+ * above 53,248 pages. */
 wq_status wq_kv4_select(const void *Q, int64_t q_stride, int32_t q_heads,
                         const wq_kv4_cache *cache, const wq_kv4_bounds *bounds,
                         const wq_kv4_batch *batch, const wq_kv4_selection *selection,

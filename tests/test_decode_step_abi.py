@@ -227,7 +227,7 @@ def test_selection_refusals(base):
     for kw in (dict(first=-1), dict(last=0), dict(first=3), dict(first=2 ** 31 - 1, last=2 ** 31 - 1)):
         got = paged(base, s=selection(base, **kw))
         assert got[1] == INVALID and got[3] == INVALID
-    got = paged(base, b=batch(base, table_width=425985, table_stride=425985))
+    got = paged(base, b=batch(base, table_width=53249, table_stride=53249))
     assert got[1] == UNSUPPORTED and got[3] == UNSUPPORTED
     got = paged(base, heads=514, qs=514 * 64, os=514 * 64)
     assert got[1] == UNSUPPORTED and got[3] == UNSUPPORTED

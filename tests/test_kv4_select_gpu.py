@@ -235,13 +235,15 @@ def test_ties_and_queries_of_every_size(what, length):
         choose(q, cache, bounds, lens, rows, table, max_pages)
 
 
-def test_more_pages_than_one_cta_holds():
-    """4.6 million tokens: the keys of a cluster of eight."""
-    page, n = 16, 4_600_000
+@pytest.mark.parametrize("rows", [1, 200])
+def test_the_most_pages(rows):
+    """850,000 tokens in pages of 16, by a cluster and, for many rows, by one CTA."""
+    page, n = 16, 53_248 * 16 - 5
     cache = wq().kv4_cache(500, 1, 64, page_size=page, group=32)
     bounds = random_bounds(7, cache)
-    table = np.random.default_rng(1).integers(0, 500, (1, 300_000)).astype(np.int32)
-    choose(queries(8, 1, 2, 64), cache, bounds, [n], [1], table, 100)
+    table = np.random.default_rng(1).integers(0, 500, (rows, 53_248)).astype(np.int32)
+    lens = [n] + [4000] * (rows - 1)
+    choose(queries(8, rows, 2, 64), cache, bounds, lens, [1] * rows, table, 100)
 
 
 def test_uniform_rows_and_queries_as_a_slice():

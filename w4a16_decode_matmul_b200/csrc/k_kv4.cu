@@ -61,7 +61,7 @@ struct ReadOp {
 };
 
 template <int D, int G, int NT, int WARPS, int TILES>
-cudaError_t launch_attn(const kv4::AttnParams& p, cudaStream_t s, int sms) {
+cudaError_t launch_attn(const kv4::AttnParams& p, bool after, cudaStream_t s, int sms) {
   using C = kv4::AttnConfig<D, G, NT, WARPS>;
   constexpr size_t smem = C::kOffCtl + C::kCtlBytes;
   static_assert(smem <= 232448, "shared memory of one CTA");
@@ -69,8 +69,22 @@ cudaError_t launch_attn(const kv4::AttnParams& p, cudaStream_t s, int sms) {
   auto kernel = kv4::attn_kernel<D, G, NT, WARPS, TILES>;
   const cudaError_t e = configure_smem(kernel, configured, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<unsigned(std::min(sms, kv4::kMaxCtas)), C::kThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  const unsigned ctas = unsigned(std::min(sms, kv4::kMaxCtas));
+  if (!after) {
+    kernel<<<ctas, C::kThreads, smem, s>>>(p);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 // Warps of a CTA and 16-token tiles per softmax step, by the registers that the
@@ -86,13 +100,14 @@ cudaError_t launch_attn(const kv4::AttnParams& p, cudaStream_t s, int sms) {
 // warps 63 us, 12 warps 55).
 template <int D, int G>
 struct AttnOp {
-  static cudaError_t run(const kv4::AttnParams& p, int max_columns, cudaStream_t s, int sms) {
+  static cudaError_t run(const kv4::AttnParams& p, int max_columns, bool after, cudaStream_t s,
+                         int sms) {
     constexpr int kTiles = D / G == 4 ? 1 : 2;
-    if (max_columns > 8) return launch_attn<D, G, 2, D == 64 ? 12 : 8, 1>(p, s, sms);
+    if (max_columns > 8) return launch_attn<D, G, 2, D == 64 ? 12 : 8, 1>(p, after, s, sms);
     const int64_t units =
         int64_t(p.batch.seqs) * p.cache.kv_heads * (p.batch.max_len / kv4::kUnit + 1);
-    if (units <= int64_t(4) * 8 * sms) return launch_attn<D, G, 1, 8, kTiles>(p, s, sms);
-    return launch_attn<D, G, 1, 12, kTiles>(p, s, sms);
+    if (units <= int64_t(4) * 8 * sms) return launch_attn<D, G, 1, 8, kTiles>(p, after, s, sms);
+    return launch_attn<D, G, 1, 12, kTiles>(p, after, s, sms);
   }
 };
 
@@ -190,14 +205,14 @@ cudaError_t run_kv4_attention(const void* Q, int64_t q_stride, int q_heads,
     p.max_columns = kFew;  // a ragged batch may hold both kinds
   }
   const int max_columns = int(std::min<int64_t>(bound * p.gqa, kFew));
-  return dispatch_kv4<AttnOp>(cache.head_dim, cache.group, p, max_columns, s, dev.sms);
+  return dispatch_kv4<AttnOp>(cache.head_dim, cache.group, p, max_columns, false, s, dev.sms);
 }
 
 cudaError_t run_kv4_attention_pages(const void* Q, int64_t q_stride, int q_heads,
                                     const wq_kv4_cache& cache, int rows,
                                     const wq_kv4_selection& sel, float scale, void* O,
-                                    int64_t o_stride, void* workspace, cudaStream_t s,
-                                    const DeviceInfo& dev) {
+                                    int64_t o_stride, void* workspace, bool after,
+                                    cudaStream_t s, const DeviceInfo& dev) {
   kv4::AttnParams p = attn_params(Q, q_stride, q_heads, cache, scale, O, o_stride, workspace);
   const wq_kv4_batch each_row = {rows,       rows,      nullptr,
                                  sel.lens,   sel.lists, sel.max_pages,
@@ -205,8 +220,8 @@ cudaError_t run_kv4_attention_pages(const void* Q, int64_t q_stride, int q_heads
   p.batch = device_batch(each_row, cache.page_size);
   if (p.batch.status == nullptr) return cudaErrorInitializationError;
   p.head_stride = sel.max_pages;
-  return dispatch_kv4<AttnOp>(cache.head_dim, cache.group, p, std::min(p.gqa, kv4::kMaxRows), s,
-                              dev.sms);
+  return dispatch_kv4<AttnOp>(cache.head_dim, cache.group, p, std::min(p.gqa, kv4::kMaxRows),
+                              after, s, dev.sms);
 }
 
 }  // namespace wqh

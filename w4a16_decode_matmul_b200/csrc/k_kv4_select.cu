@@ -20,23 +20,23 @@ struct BoundsOp {
   }
 };
 
-// CTAs of a cluster: one for each 256 pages that a sequence can have, as long as the
-// grid is not full without; at least as many as hold the keys.
+// CTAs of a cluster: one for each 256 pages that a sequence can have, as long as there is
+// an SM for each.
 int select_ctas(int64_t width, int64_t units, int sms) {
   int ctas = 1;
-  while (ctas < kv4::kMaxCluster && ctas * 256 < width && units * ctas < 4 * sms) ctas *= 2;
-  while (ctas < kv4::kMaxCluster && int64_t(ctas) * kv4_select_slice() < width) ctas *= 2;
+  while (ctas < kv4::kMaxCluster && ctas * 256 < width && units * ctas * 2 <= sms) ctas *= 2;
   return ctas;
 }
 
 template <int D>
-cudaError_t launch_select(kv4::SelectParams p, int64_t width, cudaStream_t s, int sms) {
+cudaError_t launch_select(kv4::SelectParams p, int64_t width, bool after, cudaStream_t s,
+                          int sms) {
   const int64_t units = int64_t(p.rows) * p.kv_heads;
   p.ctas = select_ctas(width, units, sms);
-  const size_t smem = round_up(size_t((width + p.ctas - 1) / p.ctas) * 4, 16);
+  const size_t smem = round_up(size_t(width) * 4, 16);
   static int configured[kMaxDevices] = {};
   auto kernel = kv4::select_kernel<D>;
-  const cudaError_t e = configure_smem(kernel, configured, size_t(kv4_select_slice()) * 4);
+  const cudaError_t e = configure_smem(kernel, configured, size_t(kv4::kMaxSelectPages) * 4);
   if (e != cudaSuccess) return e;
   if ((units + 1) * p.ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
@@ -45,22 +45,22 @@ cudaError_t launch_select(kv4::SelectParams p, int64_t width, cudaStream_t s, in
   cfg.blockDim = dim3(kv4::kSelectThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   if (p.ctas > 1) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {unsigned(p.ctas), 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs++].val.clusterDim = {unsigned(p.ctas), 1, 1};
   }
+  if (after) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cfg.attrs = attr;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace
 
-// Pages of one CTA: their keys and the kernel's own 5 KB fit the shared memory.
-int kv4_select_slice() { return 53248; }
-
-int64_t kv4_select_max_pages() { return int64_t(kv4_select_slice()) * kv4::kMaxCluster; }
+int64_t kv4_select_max_pages() { return kv4::kMaxSelectPages; }
 
 int kv4_select_max_group() { return kv4::kMaxGroupHeads; }
 
@@ -82,7 +82,7 @@ cudaError_t run_kv4_update_bounds(const wq_kv4_cache& cache, const wq_kv4_bounds
 
 cudaError_t run_kv4_select(const void* Q, int64_t q_stride, int q_heads,
                            const wq_kv4_cache& cache, const wq_kv4_bounds& bounds,
-                           const wq_kv4_batch& batch, const wq_kv4_selection& sel,
+                           const wq_kv4_batch& batch, const wq_kv4_selection& sel, bool after,
                            cudaStream_t s, int sms) {
   kv4::SelectParams p = {};
   p.batch = device_batch(batch, cache.page_size);
@@ -104,8 +104,8 @@ cudaError_t run_kv4_select(const void* Q, int64_t q_stride, int q_heads,
   // what the longest sequence can have
   const int64_t width =
       std::min<int64_t>(batch.table_width, (int64_t(p.batch.max_len) >> p.page_shift) + 1);
-  return cache.head_dim == 64 ? launch_select<64>(p, width, s, sms)
-                              : launch_select<128>(p, width, s, sms);
+  return cache.head_dim == 64 ? launch_select<64>(p, width, after, s, sms)
+                              : launch_select<128>(p, width, after, s, sms);
 }
 
 }  // namespace wqh

@@ -349,6 +349,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
     ctl->pieces[warp] = 0u;
   }
   __syncwarp();
+  grid_dependency_wait();  // where it is launched as a dependent of what makes its lists
 
   // ---- the units of the batch.  Up to 32 sequences: every warp counts them
   // by itself, lane b sequence b.  More: thread i counts those of a contiguous

@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(kBoundThreads) bounds_kernel(const BoundsParam
   __shared__ float top_s[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int shift = p.cache.page_shift, page_tokens = 1 << shift;
+  grid_dependents_launch();
   const int item = int(blockIdx.x) / p.cache.kv_heads;
   const int head = int(blockIdx.x) - item * p.cache.kv_heads;
   if (item >= p.items) {
@@ -166,11 +167,13 @@ __global__ void __launch_bounds__(kBoundThreads) bounds_kernel(const BoundsParam
   if (threadIdx.x == 0) p.grid[page * p.cache.kv_heads + head] = __uint_as_float(e << 23);
 }
 
-constexpr int kSelectThreads = 256;
+constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxGroupHeads = 256;  // 127 * 256 fits 16 bits
-constexpr int kDigits = 4;           // radix passes of 8 bits
+constexpr int kMaxGroupHeads = 256;    // 127 * 256 fits 16 bits
+constexpr int kMaxSelectPages = 53248; // whose keys fit the shared memory of one CTA
+constexpr int kBinBits = 11, kBins = 1 << kBinBits;
+constexpr int kHeldHeads = 4;          // queries that a thread keeps from one pass to the next
 
 struct SelectParams {
   Batch batch;
@@ -182,8 +185,8 @@ struct SelectParams {
   int page_shift, kv_heads, gqa;
   int max_pages, first, last;
   int rows, ctas;  // ctas: of a cluster
-  int* lists;  // [rows][kv_heads][max_pages]
-  int* lens;   // [rows]
+  int* lists;      // [rows][kv_heads][max_pages]
+  int* lens;       // [rows]
 };
 
 // Order-preserving unsigned of a binary32.
@@ -192,30 +195,32 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
 }
 
-__device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_dsmem_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 struct SelectControl {
-  uint32_t hist[kDigits][256];
-  uint32_t warp_sum[kSelectWarps];
-  uint32_t found[2];      // digit, pages above it
-  uint32_t counts[2];     // pages of this CTA above the threshold, and at it
+  uint32_t hist[kBins];
+  uint32_t warp_sum[kSelectWarps], low[kSelectWarps], high[kSelectWarps];
+  uint32_t bin, above, inside;  // found by one thread
   float top[kSelectWarps];
-  alignas(16) int16_t plus[128], minus[128];
+  int plus[128], minus[128];
+  alignas(16) int16_t plus16[128], minus16[128];
 };
 
-// The pages of one row and kv head: a cluster of CTAs, each with a slice of the
-// sequence's pages, whose keys stay in shared memory.  Scores are integer dot products
-// of 256 bytes a page (eight lanes a page of 128-wide heads); the smallest key that is
-// chosen is found digit by digit, the cluster's histograms added through distributed
-// shared memory; then each CTA writes its chosen pages behind those of the CTAs
-// before it, in the order of their tokens.
+// The pages of one row and kv head: a cluster of CTAs, each of which scores a slice of the
+// sequence's pages (integer dot products of 256 bytes a page, eight lanes a page of 128-wide
+// heads) and leaves the keys in the first CTA's shared memory.  That CTA finds the
+// smallest key that is chosen, 11 bits of the range of keys a pass -- two passes as a rule,
+// since it stops when the pages of a bin are all chosen -- and writes the chosen pages in
+// the order of their tokens.
+//
+// With histograms of all CTAs added through distributed shared memory in four passes of 8
+// bits it was 20,800 cycles for 2,048 pages, half of them the cluster's barriers.
 template <int D>
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectParams p) {
-  constexpr int LPP = D / 16, PPW = 32 / LPP, kUnroll = 4;
+__global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectParams p) {
+  constexpr int LPP = D / 16, PPW = 32 / LPP, kUnroll = 2;
+  constexpr int kHeadStep = kSelectThreads / D;  // heads that are looked at at once
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ SelectControl ctl;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -224,10 +229,21 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
   const int r = unit / p.kv_heads, head = unit - r * p.kv_heads;
   if (r >= p.rows) {  // a cluster behind the rows
     check_sequences(p.batch, rank * kSelectWarps + warp, p.ctas * kSelectWarps, lane);
+    grid_dependency_wait();
     return;
   }
+  grid_dependents_launch();
+  if (p.ctas > 1) cluster_arrive();  // the first CTA runs before its shared memory is written
+  // ---- queries, on their way while the sequence is looked up
+  const __nv_bfloat16* const q =
+      p.Q + int64_t(r) * p.q_stride + int64_t(head) * p.gqa * D + tid % D;
+  float held[kHeldHeads];
+#pragma unroll
+  for (int i = 0; i < kHeldHeads; ++i) {
+    const int h = tid / D + i * kHeadStep;
+    held[i] = h < p.gqa ? __bfloat162float(q[h * D]) : 0.f;
+  }
   int* const list = p.lists + int64_t(unit) * p.max_pages;
-
   const int b = find_sequence(p.batch, r, lane);
   Sequence seq = {0, 0, 0};
   if (b >= 0) seq = load_sequence(p.batch, b);
@@ -240,60 +256,89 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
   const int* const table = p.batch.page_table + int64_t(max(b, 0)) * p.batch.table_stride;
   if (rank == 0)
     for (int i = count + tid; i < p.max_pages; i += kSelectThreads) list[i] = -1;
-  if (n <= p.max_pages) {
-    for (int i = rank * kSelectThreads + tid; i < n; i += p.ctas * kSelectThreads) {
-      const int page = table[i];
+  auto copy_pages = [&](int to, int from, int many) {
+    for (int i = tid; i < many; i += kSelectThreads) {
+      const int page = table[from + i];
       if (page < 0 || page >= p.pages) record_status(kStatusInvalid, p.batch.status);
-      list[i] = page;
+      list[to + i] = page;
     }
+  };
+  if (n <= p.max_pages) {
+    if (rank == 0) copy_pages(0, 0, n);
+    if (p.ctas > 1) cluster_wait();
+    grid_dependency_wait();  // the grid may not be over before the one that it depends on
     return;
   }
+  // ---- pages j0 .. j0 + m - 1 are this CTA's, of those that are not chosen in any case
+  const int middle = n - p.first - p.last, wanted = count - p.first - p.last;
+  const int per = (middle + p.ctas - 1) / p.ctas;
+  const int s0 = min(middle, rank * per), m = min(middle, s0 + per) - s0, j0 = p.first + s0;
+  const int part = lane % LPP, own = lane / LPP;
+  int next[kUnroll];
+  auto read_table = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int j = base + i * PPW + own;
+      next[i] = j < m ? table[j0 + j] : 0;
+    }
+  };
+  constexpr int kWarpPages = PPW * kUnroll;
+  read_table(warp * kWarpPages);
 
   // ---- the group's queries: largest magnitude, then the sums of their 8-bit values
-  const __nv_bfloat16* const q =
-      p.Q + int64_t(r) * p.q_stride + int64_t(head) * p.gqa * D;
-  for (int i = tid; i < kDigits * 256; i += kSelectThreads) (&ctl.hist[0][0])[i] = 0u;
   float top = 0.f;
-  for (int i = tid; i < p.gqa * D; i += kSelectThreads)
-    top = fmaxf(top, fabsf(__bfloat162float(q[i])));
 #pragma unroll
-  for (int m = 1; m < 32; m *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+  for (int i = 0; i < kHeldHeads; ++i) top = fmaxf(top, fabsf(held[i]));
+  for (int h = tid / D + kHeldHeads * kHeadStep; h < p.gqa; h += kHeadStep)
+    top = fmaxf(top, fabsf(__bfloat162float(q[h * D])));
+#pragma unroll
+  for (int k = 1; k < 32; k *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
   if (lane == 0) ctl.top[warp] = top;
+  if (tid < D) ctl.plus[tid] = ctl.minus[tid] = 0;
+  for (int i = tid; i < kBins; i += kSelectThreads) ctl.hist[i] = 0u;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kSelectWarps; ++w) top = fmaxf(top, ctl.top[w]);
-  if (tid < D) {
+  {
     // magnitudes whose grid would leave the normal binary32 are raised first, exactly
     const float raise = top < 0x1p-60f ? 0x1p66f : 1.f;
     const float inv = __uint_as_float((254u - grid_exponent(top * raise)) << 23);
     int plus = 0, minus = 0;
-    for (int h = 0; h < p.gqa; ++h) {
-      const float x = __bfloat162float(q[h * D + tid]) * raise * inv;
-      const int v = max(-127, min(127, __float2int_rn(x)));
+    auto add = [&](float x) {
+      const int v = max(-127, min(127, __float2int_rn(x * raise * inv)));
       plus += max(v, 0);
       minus += min(v, 0);
-    }
-    ctl.plus[tid] = int16_t(plus);
-    ctl.minus[tid] = int16_t(minus);
+    };
+#pragma unroll
+    for (int i = 0; i < kHeldHeads; ++i) add(held[i]);
+    for (int h = tid / D + kHeldHeads * kHeadStep; h < p.gqa; h += kHeadStep)
+      add(__bfloat162float(q[h * D]));
+    atomicAdd(&ctl.plus[tid % D], plus);
+    atomicAdd(&ctl.minus[tid % D], minus);
+  }
+  __syncthreads();
+  if (tid < D) {
+    ctl.plus16[tid] = int16_t(ctl.plus[tid]);
+    ctl.minus16[tid] = int16_t(ctl.minus[tid]);
   }
   __syncthreads();
 
-  // ---- scores of this CTA's pages
-  const int per = (n + p.ctas - 1) / p.ctas;
-  const int j0 = min(n, rank * per), m = min(n, j0 + per) - j0;
-  const int part = lane % LPP, own = lane / LPP;
+  // ---- scores
   int qp[8], qm[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    qp[i] = reinterpret_cast<const int*>(ctl.plus)[part * 8 + i];
-    qm[i] = reinterpret_cast<const int*>(ctl.minus)[part * 8 + i];
+    qp[i] = reinterpret_cast<const int*>(ctl.plus16)[part * 8 + i];
+    qm[i] = reinterpret_cast<const int*>(ctl.minus16)[part * 8 + i];
   }
-  for (int base = warp * (PPW * kUnroll); base < m; base += kSelectWarps * PPW * kUnroll) {
+  if (p.ctas > 1) cluster_wait();
+  grid_dependency_wait();  // the bounds (launched as a dependent of their update)
+  const uint32_t to =
+      p.ctas > 1 ? map_to_rank(smem_addr(keys + s0), 0u) : smem_addr(keys + s0);
+  for (int base = warp * kWarpPages; base < m; base += kSelectWarps * kWarpPages) {
     int64_t at[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const int j = base + i * PPW + own;
-      int page = j < m ? table[j0 + j] : 0;
+      int page = next[i];
       if (page < 0 || page >= p.pages) {
         record_status(kStatusInvalid, p.batch.status);
         page = 0;  // any page can be read
@@ -309,50 +354,74 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
       hi[i] = __ldg(box + D / 16);
       grid[i] = __ldg(p.grid + at[i]);
     }
+    read_table(base + kSelectWarps * kWarpPages);
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       const int l[4] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w};
       const int h[4] = {hi[i].x, hi[i].y, hi[i].z, hi[i].w};
-      int sum = 0;
+      int sum = 0, sum_low = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         sum = __dp2a_lo(qp[2 * k], h[k], sum);
+        sum_low = __dp2a_lo(qm[2 * k], l[k], sum_low);
         sum = __dp2a_hi(qp[2 * k + 1], h[k], sum);
-        sum = __dp2a_lo(qm[2 * k], l[k], sum);
-        sum = __dp2a_hi(qm[2 * k + 1], l[k], sum);
+        sum_low = __dp2a_hi(qm[2 * k + 1], l[k], sum_low);
       }
+      sum += sum_low;
 #pragma unroll
       for (int d = 1; d < LPP; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       const int j = base + i * PPW + own;
       if (part == 0 && j < m) {
-        const int page = j0 + j;
-        const bool always = page < p.first || page >= n - p.last;
-        keys[j] = always ? 0xffffffffu : order_key(float(sum) * grid[i]);
+        const uint32_t key = order_key(float(sum) * grid[i]);
+        if (p.ctas > 1)
+          st_dsmem_u32(to + 4u * uint32_t(j), key);
+        else
+          keys[j] = key;
       }
     }
   }
-  __syncthreads();
+  if (p.ctas > 1) {
+    __syncwarp();
+    cluster_sync();
+    if (rank != 0) return;
+  } else {
+    __syncthreads();
+  }
 
-  // ---- the smallest chosen key, eight bits a pass: `above` pages have a larger one
-  uint32_t prefix = 0u, above = 0u;
-  for (int pass = 0; pass < kDigits; ++pass) {
-    const int shift = 24 - 8 * pass;
-    for (int j = tid; j < m; j += kSelectThreads) {
-      const uint32_t key = keys[j];
-      if (pass == 0 || (key >> (shift + 8)) == prefix)
-        atomicAdd(&ctl.hist[pass][(key >> shift) & 255u], 1u);
-    }
-    uint32_t sum;  // of the bin 255 - tid
-    if (p.ctas > 1) {
-      cluster_sync();
-      sum = 0u;
-      const uint32_t here = smem_addr(&ctl.hist[pass][255 - tid]);
+  // ---- the range of the keys
+  uint32_t low = 0xffffffffu, high = 0u;
+  for (int j = tid; j < middle; j += kSelectThreads) {
+    low = min(low, keys[j]);
+    high = max(high, keys[j]);
+  }
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  if (lane == 0) ctl.low[warp] = low, ctl.high[warp] = high;
+  __syncthreads();
 #pragma unroll
-      for (int c = 0; c < kMaxCluster; ++c)
-        if (c < p.ctas) sum += ld_dsmem_u32(map_to_rank(here, uint32_t(c)));
-    } else {
-      __syncthreads();
-      sum = ctl.hist[pass][255 - tid];
+  for (int w = 0; w < kSelectWarps; ++w) {
+    low = min(low, ctl.low[w]);
+    high = max(high, ctl.high[w]);
+  }
+
+  // ---- the smallest chosen key, and how many pages of that key are chosen: in each pass
+  // the keys from low on in bins of 2^shift, `above` chosen pages behind the last bin
+  int shift = max(0, 32 - __clz(int(high - low)) - kBinBits);
+  uint32_t above = 0u, ties = 0u;
+  uint32_t span = 0u;  // of the keys looked at: low .. low + span
+  for (span = high - low; wanted > 0;) {
+    for (int j = tid; j < middle; j += kSelectThreads) {
+      const uint32_t off = keys[j] - low;
+      if (keys[j] >= low && off <= span) atomicAdd(&ctl.hist[off >> shift], 1u);
+    }
+    __syncthreads();
+    // thread t has bins kBins - 1 - 4 t downwards
+    constexpr int kEach = kBins / kSelectThreads;
+    uint32_t bins[kEach], sum = 0u;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      bins[i] = ctl.hist[kBins - 1 - (tid * kEach + i)];
+      sum += bins[i];
     }
     uint32_t upto = sum;
 #pragma unroll
@@ -365,64 +434,67 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
 #pragma unroll
     for (int w = 0; w < kSelectWarps; ++w)
       if (w < warp) upto += ctl.warp_sum[w];
-    // the bin in which the max_pages-th largest key lies
-    if (above + upto >= uint32_t(count) && above + upto - sum < uint32_t(count)) {
-      ctl.found[0] = uint32_t(255 - tid);
-      ctl.found[1] = above + upto - sum;
-    }
-    __syncthreads();
-    prefix = (prefix << 8) | ctl.found[0];
-    above = ctl.found[1];
-  }
-
-  // ---- pages of this CTA above the threshold and at it, and of those before it
-  uint32_t mine_above = 0u, mine_at = 0u;
-  for (int j0w = warp * 32; j0w < m; j0w += kSelectThreads) {
-    const uint32_t key = j0w + lane < m ? keys[j0w + lane] : 0u;
-    mine_above += __popc(__ballot_sync(0xffffffffu, j0w + lane < m && key > prefix));
-    mine_at += __popc(__ballot_sync(0xffffffffu, j0w + lane < m && key == prefix));
-  }
-  if (tid < 2) ctl.counts[tid] = 0u;
-  __syncthreads();
-  if (lane == 0) {
-    atomicAdd(&ctl.counts[0], mine_above);
-    atomicAdd(&ctl.counts[1], mine_at);
-  }
-  uint32_t before_above = 0u, before_at = 0u;
-  if (p.ctas > 1) {
-    cluster_sync();
-    const uint32_t here = smem_addr(&ctl.counts[0]);
+    // the bin in which the last chosen page lies
+    uint32_t before = above + upto - sum;
+    if (before < uint32_t(wanted) && above + upto >= uint32_t(wanted)) {
 #pragma unroll
-    for (int c = 0; c < kMaxCluster; ++c)
-      if (c < rank) {
-        before_above += ld_dsmem_u32(map_to_rank(here, uint32_t(c)));
-        before_at += ld_dsmem_u32(map_to_rank(here + 4, uint32_t(c)));
+      for (int i = 0; i < kEach; ++i) {
+        if (before < uint32_t(wanted) && before + bins[i] >= uint32_t(wanted)) {
+          ctl.bin = uint32_t(kBins - 1 - (tid * kEach + i));
+          ctl.above = before;
+          ctl.inside = bins[i];
+        }
+        before += bins[i];
       }
-  }
-  const uint32_t ties = uint32_t(count) - above;  // of the pages at it: the first ones
-  for (int base = 0; base < m; base += kSelectThreads) {
-    const int j = base + tid;
-    const uint32_t key = j < m ? keys[j] : 0u;
-    const bool over = j < m && key > prefix, at = j < m && key == prefix;
-    const uint32_t over_mask = __ballot_sync(0xffffffffu, over);
-    const uint32_t at_mask = __ballot_sync(0xffffffffu, at);
-    __syncthreads();  // the sums of the round before have been read
-    if (lane == 0) ctl.warp_sum[warp] = uint32_t(__popc(over_mask)) | uint32_t(__popc(at_mask)) << 16;
-    __syncthreads();
-    uint32_t my_above = before_above + __popc(over_mask & ((1u << lane) - 1u));
-    uint32_t my_at = before_at + __popc(at_mask & ((1u << lane) - 1u));
+    }
 #pragma unroll
-    for (int w = 0; w < kSelectWarps; ++w) {
-      const uint32_t s = ctl.warp_sum[w];
-      if (w < warp) my_above += s & 0xffffu, my_at += s >> 16;
-      before_above += s & 0xffffu, before_at += s >> 16;
-    }
-    if (over || (at && my_at < ties)) {
-      const uint32_t to = my_above + min(my_at, ties);
-      if (to < uint32_t(count)) list[to] = table[j0 + j];
-    }
+    for (int i = 0; i < kEach; ++i) ctl.hist[kBins - 1 - (tid * kEach + i)] = 0u;
+    __syncthreads();
+    low += ctl.bin << shift;
+    above = ctl.above;
+    ties = uint32_t(wanted) - above;
+    if (shift == 0 || ctl.inside == ties) break;  // one key, or all of the bin
+    span = (1u << shift) - 1u;
+    shift = max(0, shift - kBinBits);
+    __syncthreads();  // the bin has been read
   }
-  if (p.ctas > 1) cluster_sync();  // no CTA ends while its counts are read
+  // chosen: keys above `limit_key`, and the first `ties` of those equal to it
+  const bool all = wanted == 0 || shift > 0 || ctl.inside == ties;
+  const uint32_t limit_key = wanted == 0 ? 0xffffffffu : all ? low - 1u : low;
+  if (all) ties = 0u;
+
+  // ---- the pages.  Warp w has a contiguous part of the middle ones.
+  copy_pages(0, 0, p.first);
+  copy_pages(count - p.last, n - p.last, p.last);
+  const int chunk = ((middle + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
+  const int c0 = min(middle, warp * chunk), c1 = min(middle, c0 + chunk);
+  uint32_t over = 0u, equal = 0u;
+  for (int j = c0 + lane; j - lane < c1; j += 32) {
+    const uint32_t key = j < c1 ? keys[j] : 0u;
+    over += __popc(__ballot_sync(0xffffffffu, j < c1 && key > limit_key));
+    equal += __popc(__ballot_sync(0xffffffffu, j < c1 && key == limit_key));
+  }
+  __syncthreads();
+  if (lane == 0) ctl.warp_sum[warp] = over, ctl.low[warp] = equal;
+  __syncthreads();
+  over = equal = 0u;
+#pragma unroll
+  for (int w = 0; w < kSelectWarps; ++w)
+    if (w < warp) over += ctl.warp_sum[w], equal += ctl.low[w];
+  for (int j = c0 + lane; j - lane < c1; j += 32) {
+    const uint32_t key = j < c1 ? keys[j] : 0u;
+    const bool is_over = j < c1 && key > limit_key, is_equal = j < c1 && key == limit_key;
+    const uint32_t over_mask = __ballot_sync(0xffffffffu, is_over);
+    const uint32_t equal_mask = __ballot_sync(0xffffffffu, is_equal);
+    const uint32_t below = (1u << lane) - 1u;
+    const uint32_t my_equal = equal + __popc(equal_mask & below);
+    if (is_over || (is_equal && my_equal < ties)) {
+      const uint32_t to = over + __popc(over_mask & below) + min(my_equal, ties);
+      if (to < uint32_t(wanted)) list[p.first + to] = table[p.first + j];
+    }
+    over += __popc(over_mask);
+    equal += __popc(equal_mask);
+  }
 }
 
 }  // namespace kv4

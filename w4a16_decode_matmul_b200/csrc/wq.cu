@@ -665,7 +665,7 @@ wq_status wq_kv4_select(const void* Q, int64_t q_stride, int32_t q_heads,
   DeviceInfo dev;
   if (!wqh::device_info(&dev)) return WQ_ERR_CUDA;
   return from_cuda(wqh::run_kv4_select(Q, q_stride, q_heads, *cache, *bounds, *batch, *selection,
-                                       reinterpret_cast<cudaStream_t>(stream), dev.sms));
+                                       false, reinterpret_cast<cudaStream_t>(stream), dev.sms));
 }
 
 wq_status wq_kv4_attention_pages(const void* Q, int64_t q_stride, int32_t q_heads,
@@ -685,7 +685,7 @@ wq_status wq_kv4_attention_pages(const void* Q, int64_t q_stride, int32_t q_head
   DeviceInfo dev;
   if (!wqh::device_info(&dev)) return WQ_ERR_CUDA;
   return from_cuda(wqh::run_kv4_attention_pages(Q, q_stride, q_heads, *cache, rows, *selection,
-                                                scale, O, o_stride, workspace,
+                                                scale, O, o_stride, workspace, false,
                                                 reinterpret_cast<cudaStream_t>(stream), dev));
 }
 
@@ -713,11 +713,11 @@ wq_status wq_kv4_sparse_attention(const void* Q, int64_t q_stride, int32_t q_hea
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if ((st = from_cuda(wqh::run_kv4_update_bounds(*cache, *bounds, *batch, s))) != WQ_OK) return st;
   if ((st = from_cuda(wqh::run_kv4_select(Q, q_stride, q_heads, *cache, *bounds, *batch,
-                                          *selection, s, dev.sms))) != WQ_OK)
+                                          *selection, true, s, dev.sms))) != WQ_OK)
     return st;
   return from_cuda(wqh::run_kv4_attention_pages(Q, q_stride, q_heads, *cache, batch->rows,
-                                                *selection, scale, O, o_stride, workspace, s,
-                                                dev));
+                                                *selection, scale, O, o_stride, workspace, true,
+                                                s, dev));
 }
 
 // --------------------------------------------------------- rotary positions
