@@ -463,9 +463,12 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectP
   const uint32_t limit_key = wanted == 0 ? 0xffffffffu : all ? low - 1u : low;
   if (all) ties = 0u;
 
-  // ---- the pages.  Warp w has a contiguous part of the middle ones.
+  // ---- the pages.  Warp w has a contiguous part of the middle ones.  Their places are
+  // gathered first (where they fit the histogram's memory), so that the look-ups in the
+  // page table are on their way together.
   copy_pages(0, 0, p.first);
   copy_pages(count - p.last, n - p.last, p.last);
+  const bool gather = wanted <= kBins;
   const int chunk = ((middle + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
   const int c0 = min(middle, warp * chunk), c1 = min(middle, c0 + chunk);
   uint32_t over = 0u, equal = 0u;
@@ -490,10 +493,20 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectP
     const uint32_t my_equal = equal + __popc(equal_mask & below);
     if (is_over || (is_equal && my_equal < ties)) {
       const uint32_t to = over + __popc(over_mask & below) + min(my_equal, ties);
-      if (to < uint32_t(wanted)) list[p.first + to] = table[p.first + j];
+      if (to < uint32_t(wanted)) {
+        if (gather)
+          ctl.hist[to] = uint32_t(p.first + j);
+        else
+          list[p.first + to] = table[p.first + j];
+      }
     }
     over += __popc(over_mask);
     equal += __popc(equal_mask);
+  }
+  if (gather) {
+    __syncthreads();
+    for (int i = tid; i < wanted; i += kSelectThreads)
+      list[p.first + i] = table[min(ctl.hist[i], uint32_t(n - 1))];
   }
 }
 
