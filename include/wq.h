@@ -479,7 +479,7 @@ enum { WQ_ROTARY_TRANSPOSE = 1 /* -s in s's place: the gradient of a rotation */
  * binary32, rounded once to bfloat16 (half a step 2^-8).  Y may be X itself (the
  * same address and stride), else they may not overlap.  heads may be several tensors'
  * side by side (queries and keys of a fused projection).
- * head_dim a multiple of 8, at most 512.  WQ_ERR_INVALID_ARG for sizes, pointers and
+ * heads at most 65,536, head_dim a multiple of 8, at most 512.  WQ_ERR_INVALID_ARG for sizes, pointers and
  * flags outside this, WQ_ERR_UNSUPPORTED for another head_dim, WQ_ERR_ALIGNMENT for
  * X, Y, positions or freqs not 16-byte (positions: 4-byte) aligned and strides that
  * are no multiple of 8.  rows = 0 is a call without work. */

@@ -16,21 +16,26 @@ rotary::Spec device_spec(const wq_rotary_spec& s) { return {s.freqs, s.dim, s.am
 template <int D, int G>
 struct WriteRotaryOp {
   static cudaError_t run(rotary::WriteParams p, const wq_kv4_cache& c, int interleaved,
-                         cudaStream_t s) {
+                         cudaStream_t s, int sms) {
     p.chunks = (c.kv_heads * (D / 16) + 31) / 32;
     const int per_head = interleaved ? (p.copy_q ? D : p.spec.dim) / 8
                                      : p.spec.dim / 16 + (p.copy_q ? (D - p.spec.dim) / 8 : 0);
     const int64_t units = int64_t(p.q_heads) * per_head, share = 32 * rotary::kQueryUnits;
-    const int items = p.chunks + int((units + share - 1) / share);
-    const int warps = std::min(items, rotary::kMaxWarps);
+    const int shares = p.chunks + int((units + share - 1) / share);
+    // rows of a CTA: several as soon as the GPU is full (four CTAs an SM) with that many
+    p.by_head = fast_div(uint32_t(std::max(per_head, 1)));
+    p.rows_each = 1;
+    while (p.rows_each < rotary::kWriteRows && p.batch.rows >= p.rows_each * 8 * sms)
+      p.rows_each *= 2;
+    const int warps = std::min(shares * p.rows_each, rotary::kWriteWarps);
     // CTAs behind the rows' check the sequences, 32 a warp
     const int64_t check =
         std::min<int64_t>((int64_t(p.batch.seqs) + 32 * warps - 1) / (32 * warps), 1024);
-    const unsigned ctas = unsigned(p.batch.rows + check);
+    const unsigned ctas = unsigned((p.batch.rows + p.rows_each - 1) / p.rows_each + check);
     if (interleaved)
-      rotary::write_rotary_kernel<D, G, true><<<ctas, warps * 32, 0, s>>>(p, items);
+      rotary::write_rotary_kernel<D, G, true><<<ctas, warps * 32, 0, s>>>(p, shares);
     else
-      rotary::write_rotary_kernel<D, G, false><<<ctas, warps * 32, 0, s>>>(p, items);
+      rotary::write_rotary_kernel<D, G, false><<<ctas, warps * 32, 0, s>>>(p, shares);
     return cudaGetLastError();
   }
 };
@@ -47,11 +52,13 @@ cudaError_t run_rotary(const void* X, int64_t x_stride, int rows, int heads, int
   p.y_stride = y_stride;
   p.positions = positions;
   p.spec = device_spec(spec);
+  p.rows = rows;
   p.heads = heads;
   p.head_dim = head_dim;
   p.copy = X != Y;
   p.sign = transpose ? -1.f : 1.f;
-  const bool pairs = !spec.interleaved && spec.dim % 16 != 0;
+  // (rows of angles lie on 16-byte boundaries where dim is a multiple of 4)
+  const bool pairs = spec.dim % (spec.interleaved ? 4 : 16) != 0;
   int per_head;
   if (pairs)
     per_head = spec.dim / 2 + (p.copy ? head_dim - spec.dim : 0);
@@ -60,15 +67,21 @@ cudaError_t run_rotary(const void* X, int64_t x_stride, int rows, int heads, int
   else
     per_head = spec.dim / 16 + (p.copy ? (head_dim - spec.dim) / 8 : 0);
   const int64_t units = int64_t(heads) * per_head;
-  // One CTA a row, as many threads as its units need in whole rounds; where there
-  // are fewer rows than SMs a row's units are spread over CTAs of 128.
+  // Rows of a CTA: several as soon as the GPU is full with that many and their angles fit;
+  // where there are fewer rows than SMs a row's units are spread over CTAs of 128.
+  p.rows_each = 1;
+  while (p.rows_each < 4 && rows >= p.rows_each * 8 * sms &&
+         p.rows_each * 2 * spec.dim <= rotary::kTurns)
+    p.rows_each *= 2;
   const int64_t split = std::min<int64_t>(std::max(1, 2 * sms / rows), (units + 127) / 128);
-  const int64_t mine = (units + split - 1) / split;
+  const int64_t mine = (units * p.rows_each + split - 1) / split;
   const int64_t rounds = (mine + 511) / 512;
   const int threads = int(((mine + rounds - 1) / rounds + 31) / 32 * 32);
-  const dim3 grid{unsigned(rows), unsigned(split)};
+  p.by_row = fast_div(uint32_t(units));
+  p.by_head = fast_div(uint32_t(per_head));
+  const dim3 grid{unsigned((rows + p.rows_each - 1) / p.rows_each), unsigned(split)};
   if (pairs)
-    rotary::rotary_pair_kernel<<<grid, threads, 0, s>>>(p);
+    rotary::rotary_pair_kernel<<<grid, threads, 0, s>>>(p, spec.interleaved != 0);
   else if (spec.interleaved)
     rotary::rotary_kernel<true><<<grid, threads, 0, s>>>(p);
   else
@@ -80,7 +93,7 @@ cudaError_t run_kv4_write_rotary(const void* Q, int64_t q_stride, int q_heads, v
                                  int64_t qo_stride, const void* K, int64_t k_stride,
                                  const void* V, int64_t v_stride, const wq_rotary_spec& spec,
                                  const int* positions, const wq_kv4_cache& cache,
-                                 const wq_kv4_batch& batch, cudaStream_t s) {
+                                 const wq_kv4_batch& batch, cudaStream_t s, int sms) {
   rotary::WriteParams p = {};
   p.Q = static_cast<const __nv_bfloat16*>(Q);
   p.q_stride = q_stride;
@@ -97,7 +110,8 @@ cudaError_t run_kv4_write_rotary(const void* Q, int64_t q_stride, int q_heads, v
   p.cache = device_cache(cache);
   p.batch = device_batch(batch, cache.page_size);
   if (p.batch.status == nullptr) return cudaErrorInitializationError;
-  return dispatch_kv4<WriteRotaryOp>(cache.head_dim, cache.group, p, cache, spec.interleaved, s);
+  return dispatch_kv4<WriteRotaryOp>(cache.head_dim, cache.group, p, cache, spec.interleaved, s,
+                                     sms);
 }
 
 }  // namespace wqh

@@ -16,7 +16,7 @@
 // a whole step of the value that the cache holds.
 #pragma once
 
-#include "kv4.cuh"
+#include "kv4_attn.cuh"
 
 namespace wq {
 namespace rotary {
@@ -30,8 +30,9 @@ struct Spec {
 // (c, s) of one position and frequency, in binary64 arithmetic that all heads share.
 // The angle less a multiple of pi/2 that is held in two parts (W. J. Cody and W. Waite,
 // 1980), then the series of sine and cosine to the 15th and 16th power: for |r| <= pi/4
-// the next terms are below 2^-54.
-__device__ __forceinline__ float2 turn_of(int position, float freq, float amplitude) {
+// the next terms are below 2^-54.  (A function of its own: its registers are not the
+// kernels', which keep their loads in flight meanwhile.)
+static __device__ __noinline__ float2 turn_of(int position, float freq, float amplitude) {
   const double a = double(position) * double(freq);
   const double k = rint(a * 0.6366197723675814);         // 2/pi
   double r = fma(-k, 1.5707963267948966, a);             // pi/2 ...
@@ -64,10 +65,29 @@ __device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// One pair in binary32.
-__device__ __forceinline__ float2 turn_pair(float x1, float x2, float2 t) {
-  return make_float2(fmaf(x1, t.x, -(x2 * t.y)), fmaf(x2, t.x, x1 * t.y));
+// The angles of a row as the kernels read them, an entry for each turned element e of a
+// head: y_e = x_e c_e + z_e n_e, z_e the other element of its pair, n_e = -s for the
+// first element of the pair and s for the second.
+__device__ __forceinline__ void put_turn(float2 t, int j, int half, bool interleaved, float* c,
+                                         float* n) {
+  const int one = interleaved ? 2 * j : j, two = interleaved ? 2 * j + 1 : j + half;
+  c[one] = c[two] = t.x;
+  n[one] = -t.y;
+  n[two] = t.y;
 }
+
+__device__ __forceinline__ float2 negative(float2 x) { return mul2(x, make_float2(-1.f, -1.f)); }
+
+// Eight entries.
+struct Eight {
+  float2 of[4];
+  __device__ __forceinline__ explicit Eight(const float* from) {
+    const float4 a = reinterpret_cast<const float4*>(from)[0];
+    const float4 b = reinterpret_cast<const float4*>(from)[1];
+    of[0] = make_float2(a.x, a.y), of[1] = make_float2(a.z, a.w);
+    of[2] = make_float2(b.x, b.y), of[3] = make_float2(b.z, b.w);
+  }
+};
 
 // What one thread turns at a time: eight pairs (two runs of eight elements, or one
 // of eight for interleaved pairs, which are four), or eight elements that stay.
@@ -86,35 +106,39 @@ struct Units {
   }
 };
 
-__device__ __forceinline__ void turn_runs(uint4& a, uint4& b, const float2* turn) {
+// Two runs of eight elements that are each other's pairs; c and n at the first's.
+__device__ __forceinline__ void turn_runs(uint4& a, uint4& b, const float* c, const float* n) {
+  const Eight cs(c), ns(n);
   uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 p = kv4::bf16x2_to_float2(x[i]), q = kv4::bf16x2_to_float2(y[i]);
-    const float4 t = *reinterpret_cast<const float4*>(turn + 2 * i);
-    const float2 lo = turn_pair(p.x, q.x, make_float2(t.x, t.y));
-    const float2 hi = turn_pair(p.y, q.y, make_float2(t.z, t.w));
-    x[i] = pack_bf162(lo.x, hi.x);
-    y[i] = pack_bf162(lo.y, hi.y);
+    const float2 one = fma2(q, ns.of[i], mul2(p, cs.of[i]));
+    const float2 two = fma2(p, negative(ns.of[i]), mul2(q, cs.of[i]));
+    x[i] = pack_bf162(one.x, one.y);
+    y[i] = pack_bf162(two.x, two.y);
   }
   a = make_uint4(x[0], x[1], x[2], x[3]);
   b = make_uint4(y[0], y[1], y[2], y[3]);
 }
 
 // Pairs side by side; the first `pairs` of the run's four turn.
-__device__ __forceinline__ void turn_interleaved(uint4& a, const float2* turn, int pairs) {
+__device__ __forceinline__ void turn_interleaved(uint4& a, const float* c, const float* n,
+                                                 int pairs) {
+  const Eight cs(c), ns(n);
   uint32_t x[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (i < pairs) {
       const float2 p = kv4::bf16x2_to_float2(x[i]);
-      const float2 y = turn_pair(p.x, p.y, turn[i]);
+      const float2 y = fma2(make_float2(p.y, p.x), ns.of[i], mul2(p, cs.of[i]));
       x[i] = pack_bf162(y.x, y.y);
     }
   a = make_uint4(x[0], x[1], x[2], x[3]);
 }
 
 constexpr int kMaxHead = 512;
+constexpr int kTurns = 1024;  // entries of turned elements that a CTA holds: of several rows
 
 struct RotaryParams {
   const __nv_bfloat16* X;  // [rows][heads][head_dim], rows x_stride elements apart
@@ -123,82 +147,102 @@ struct RotaryParams {
   int64_t y_stride;
   const int* positions;  // [rows]
   Spec spec;
-  int heads, head_dim;
+  int rows, heads, head_dim;
+  int rows_each;  // rows of a CTA
+  kv4::FastDiv by_row, by_head;  // by the units of a row and of a head
   bool copy;      // Y is other memory: the elements that stay are copied
   float sign;     // -1: the transpose
 };
 
-// A CTA takes one row (blockIdx.x) and, where there are few rows, a part of its
-// units (blockIdx.y): the loads of each thread's first unit, the row's angles, then
-// all heads.  HBM bound, two bytes in and two out an element.
-template <bool INTERLEAVED>
-__global__ void __launch_bounds__(512, 2) rotary_kernel(const RotaryParams p) {
-  __shared__ __align__(16) float2 turn[kMaxHead / 2];
-  const int64_t r = blockIdx.x;
-  const Units<INTERLEAVED> u(p.spec.dim, p.head_dim, p.copy);
-  const unsigned units = unsigned(p.heads) * unsigned(u.all);
-  const unsigned step = gridDim.y * blockDim.x;
-  const __nv_bfloat16* const from = p.X + r * p.x_stride;
-  __nv_bfloat16* const to = p.Y + r * p.y_stride;
-  bool ready = false;
-  for (unsigned i = blockIdx.y * blockDim.x + threadIdx.x;; i += step) {
-    const bool there = i < units;
-    const unsigned head = i / unsigned(u.all);
-    const int k = int(i - head * unsigned(u.all));
-    const int64_t at = int64_t(head) * p.head_dim + u.offset(k);
-    const bool turned = k < u.turned;
-    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-    if (there) {
-      a = *reinterpret_cast<const uint4*>(from + at);
-      if (!INTERLEAVED && turned) b = *reinterpret_cast<const uint4*>(from + at + u.half);
-    }
-    if (!ready) {
-      ready = true;
-      const int position = p.positions[r];
-      for (int j = threadIdx.x; j < u.half; j += blockDim.x) {
-        const float2 t = turn_of(position, p.spec.freqs[j], p.spec.amplitude);
-        turn[j] = make_float2(t.x, p.sign * t.y);
-      }
-      __syncthreads();
-    }
-    if (!there) return;
-    if (turned) {
-      if (INTERLEAVED) {
-        turn_interleaved(a, turn + 4 * k, u.half - 4 * k);
-      } else {
-        turn_runs(a, b, turn + 8 * k);
-        *reinterpret_cast<uint4*>(to + at + u.half) = b;
-      }
-    }
-    *reinterpret_cast<uint4*>(to + at) = a;
+struct RotaryTurns {
+  // (a head whose turned part ends inside a run of eight is read to the run's end)
+  alignas(16) float c[kTurns + 8], n[kTurns + 8];
+};
+
+// The angles of a CTA's rows r0 .. r0 + count - 1, all threads together.
+__device__ __forceinline__ void make_turns(const RotaryParams& p, bool interleaved, int64_t r0,
+                                           int count, RotaryTurns& t) {
+  const int half = p.spec.dim / 2;
+  for (int j = threadIdx.x; j < count * half; j += blockDim.x) {
+    const int row = j / half, f = j - row * half;
+    float2 cs = turn_of(p.positions[r0 + row], p.spec.freqs[f], p.spec.amplitude);
+    cs.y *= p.sign;
+    put_turn(cs, f, half, interleaved, t.c + row * p.spec.dim, t.n + row * p.spec.dim);
   }
 }
 
-// The same for half layouts whose halves are not whole runs of eight elements
-// (dim not a multiple of 16): a pair, or an element that stays, at a time.
-static __global__ void __launch_bounds__(512, 2) rotary_pair_kernel(const RotaryParams p) {
-  __shared__ __align__(16) float2 turn[kMaxHead / 2];
-  const int64_t r = blockIdx.x;
-  const int half = p.spec.dim / 2;
-  const unsigned all = unsigned(half + (p.copy ? p.head_dim - 2 * half : 0));
-  const unsigned units = unsigned(p.heads) * all;
-  const int position = p.positions[r];
-  for (int j = threadIdx.x; j < half; j += blockDim.x) {
-    const float2 t = turn_of(position, p.spec.freqs[j], p.spec.amplitude);
-    turn[j] = make_float2(t.x, p.sign * t.y);
+// A CTA takes a few rows (blockIdx.x) -- the angles' arithmetic, a chain of some 60 dependent
+// operations in binary64, is then paid once for all of them -- or, where there are few
+// rows, a part of one row's units (blockIdx.y).  The loads of each thread's first unit are
+// on their way meanwhile.  HBM bound, two bytes in and two out an element.
+template <bool INTERLEAVED>
+__global__ void __launch_bounds__(512, 3) rotary_kernel(const RotaryParams p) {
+  __shared__ RotaryTurns turns;
+  const int64_t r0 = int64_t(blockIdx.x) * p.rows_each;
+  const int n = int(min(int64_t(p.rows_each), p.rows - r0));
+  const Units<INTERLEAVED> u(p.spec.dim, p.head_dim, p.copy);
+  const int each = p.heads * u.all, units = each * n;
+  const int step = int(gridDim.y * blockDim.x);
+  bool ready = false;
+  for (int i = int(blockIdx.y * blockDim.x + threadIdx.x);; i += step) {
+    const bool there = i < units;
+    const int row = p.by_row(i), in_row = i - row * each, head = p.by_head(in_row);
+    const int k = in_row - head * u.all;
+    const int64_t at = int64_t(head) * p.head_dim + u.offset(k);
+    const __nv_bfloat16* const from = p.X + (r0 + row) * p.x_stride + at;
+    const bool turned = k < u.turned;
+    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+    if (there) {
+      a = *reinterpret_cast<const uint4*>(from);
+      if (!INTERLEAVED && turned) b = *reinterpret_cast<const uint4*>(from + u.half);
+    }
+    if (!ready) {
+      ready = true;
+      make_turns(p, INTERLEAVED, r0, n, turns);
+      __syncthreads();
+    }
+    if (!there) return;
+    __nv_bfloat16* const to = p.Y + (r0 + row) * p.y_stride + at;
+    if (turned) {
+      const int e = row * p.spec.dim + 8 * k;
+      if (INTERLEAVED) {
+        turn_interleaved(a, turns.c + e, turns.n + e, u.half - 4 * k);
+      } else {
+        turn_runs(a, b, turns.c + e, turns.n + e);
+        *reinterpret_cast<uint4*>(to + u.half) = b;
+      }
+    }
+    *reinterpret_cast<uint4*>(to) = a;
   }
+}
+
+// The same where a thread's unit would not lie on 16-byte boundaries of the angles or the
+// row (dim not a multiple of 16 in halves, of 8 side by side): a pair, or an element
+// that stays, at a time.
+static __global__ void __launch_bounds__(512, 3) rotary_pair_kernel(const RotaryParams p,
+                                                                     bool interleaved) {
+  __shared__ RotaryTurns turns;
+  const int64_t r0 = int64_t(blockIdx.x) * p.rows_each;
+  const int n = int(min(int64_t(p.rows_each), p.rows - r0));
+  const int half = p.spec.dim / 2;
+  const int all = half + (p.copy ? p.head_dim - 2 * half : 0);
+  const int each = p.heads * all, units = each * n;
+  make_turns(p, interleaved, r0, n, turns);
   __syncthreads();
-  for (unsigned i = blockIdx.y * blockDim.x + threadIdx.x; i < units;
-       i += gridDim.y * blockDim.x) {
-    const unsigned head = i / all;
-    const int k = int(i - head * all);
-    const __nv_bfloat16* const from = p.X + r * p.x_stride + int64_t(head) * p.head_dim;
-    __nv_bfloat16* const to = p.Y + r * p.y_stride + int64_t(head) * p.head_dim;
+  for (int i = int(blockIdx.y * blockDim.x + threadIdx.x); i < units;
+       i += int(gridDim.y * blockDim.x)) {
+    const int row = p.by_row(i), in_row = i - row * each, head = p.by_head(in_row);
+    const int k = in_row - head * all;
+    const int64_t at = int64_t(head) * p.head_dim;
+    const __nv_bfloat16* const from = p.X + (r0 + row) * p.x_stride + at;
+    __nv_bfloat16* const to = p.Y + (r0 + row) * p.y_stride + at;
     if (k < half) {
-      const float2 y = turn_pair(__bfloat162float(from[k]), __bfloat162float(from[k + half]),
-                                 turn[k]);
-      to[k] = __float2bfloat16_rn(y.x);
-      to[k + half] = __float2bfloat16_rn(y.y);
+      const int one = interleaved ? 2 * k : k, two = interleaved ? one + 1 : k + half;
+      const float* const c = turns.c + row * 2 * half;
+      const float* const s = turns.n + row * 2 * half;
+      const float x = __bfloat162float(from[one]), y = __bfloat162float(from[two]);
+      to[one] = __float2bfloat16_rn(fmaf(y, s[one], x * c[one]));
+      to[two] = __float2bfloat16_rn(fmaf(x, s[two], y * c[two]));
     } else {
       to[k + half] = from[k + half];
     }
@@ -214,37 +258,45 @@ __device__ __forceinline__ float2 split16(float c) {
   return make_float2(hi, c - hi);
 }
 
-// x c - z s rounded once to binary32: the leading products are exact, the error of
-// their difference is found exactly (Knuth's two-sum), and what the low parts add is
-// 2^-16 of the products with an error of 2^-24 of that.
-__device__ __forceinline__ float turned_exactly(float x, float z, const float4& t) {
-  const float a = x * t.x, b = z * t.z;
-  const float d = a - b;
-  const float back = d - a;
-  const float err = (a - (d - back)) - (b + back);
-  const float low = fmaf(x, t.y, -(z * t.w));
-  const float y = d + (err + low);
-  return fabsf(d) <= 3.4028234e38f ? y : d;  // infinite or NaN
-}
+// The entries of a row's angles with both factors split.
+template <int D>
+struct SplitTurns {
+  alignas(16) float c[D], n[D], c_high[D], c_low[D], n_high[D], n_low[D];
+};
 
-// Eight keys (two words each of x and, for runs, of the partners z), turned.
-template <bool INTERLEAVED>
-__device__ __forceinline__ uint4 turn_keys(const uint4& x, const uint4& z, float sign,
-                                           const float4* split) {
-  const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, zs[4] = {z.x, z.y, z.z, z.w};
-  uint32_t y[4];
+// Eight keys, two at a time: x c + z n rounded once to binary32.  The leading products are
+// exact, the error of their sum is found exactly (Knuth's two-sum), and what the low parts
+// add is 2^-16 of the products with an error of 2^-24 of that.  z: the other elements of
+// the pairs; e: the first key's entry.
+template <int D>
+__device__ __forceinline__ uint4 turn_keys(const uint4& xs, const uint4& zs,
+                                           const SplitTurns<D>& t, int e) {
+  const uint32_t xw[4] = {xs.x, xs.y, xs.z, xs.w}, zw[4] = {zs.x, zs.y, zs.z, zs.w};
+  const Eight ch(t.c_high + e), cl(t.c_low + e), nh(t.n_high + e), nl(t.n_low + e);
+  float2 y[4], lead[4];
+  float most = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 p = kv4::bf16x2_to_float2(xs[i]), q = kv4::bf16x2_to_float2(zs[i]);
-    if (INTERLEAVED) {
-      const float4 t = split[i];
-      y[i] = pack_bf162(turned_exactly(p.x, p.y, t), turned_exactly(p.y, -p.x, t));
-    } else {
-      y[i] = pack_bf162(turned_exactly(p.x, sign * q.x, split[2 * i]),
-                        turned_exactly(p.y, sign * q.y, split[2 * i + 1]));
+    const float2 x = kv4::bf16x2_to_float2(xw[i]), z = kv4::bf16x2_to_float2(zw[i]);
+    const float2 minus = make_float2(-1.f, -1.f);
+    const float2 a = mul2(x, ch.of[i]), b = mul2(z, nh.of[i]);
+    const float2 d = add2(a, b);
+    const float2 back = fma2(a, minus, d);
+    const float2 err = add2(fma2(fma2(back, minus, d), minus, a), fma2(back, minus, b));
+    const float2 low = fma2(x, cl.of[i], mul2(z, nl.of[i]));
+    y[i] = add2(d, add2(err, low));
+    lead[i] = d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(most) : "f"(d.x), "f"(d.y), "f"(most));
+  }
+  if (!(most <= 3.4028234e38f)) {  // infinite or NaN
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!(fabsf(lead[i].x) <= 3.4028234e38f)) y[i].x = lead[i].x;
+      if (!(fabsf(lead[i].y) <= 3.4028234e38f)) y[i].y = lead[i].y;
     }
   }
-  return make_uint4(y[0], y[1], y[2], y[3]);
+  return make_uint4(pack_bf162(y[0].x, y[0].y), pack_bf162(y[1].x, y[1].y),
+                    pack_bf162(y[2].x, y[2].y), pack_bf162(y[3].x, y[3].y));
 }
 
 // The place of a lane in a row's keys and values: 16 elements of one head, the row's
@@ -268,57 +320,86 @@ struct WriteParams {
   kv4::Batch batch;
   int q_heads, chunks;  // chunks: warps' shares of a row's keys and values
   bool copy_q;          // Q_out is other memory than Q
+  int rows_each;        // rows of a CTA
+  kv4::FastDiv by_head; // by the units of a head
 };
 
-constexpr int kMaxWarps = 8;
+constexpr int kWriteWarps = 8;
+constexpr int kWriteRows = 4;   // rows of a CTA, at most
 constexpr int kQueryUnits = 2;  // units of queries a lane has in flight
 
-// Queries turned, keys turned and quantized, values quantized: one CTA a row, whose
-// angles its warps share; the first `chunks` shares are 512 keys and values each, the
-// others 64 units of queries.  CTAs behind the
-// rows check the sequences.
+// What a CTA knows of one of its rows: page -1 where nothing is written, seq -1 where the row
+// is left alone.
+struct RowPlace {
+  int64_t page;
+  int seq, slot, position;
+};
+
+// Queries turned, keys turned and quantized, values quantized.  A CTA takes p.rows_each
+// rows: a warp finds each row's place, all threads make the rows' angles, then the warps
+// take the rows' shares in turn: the first `chunks` shares of a row are 512 keys and
+// values each, the others 64 units of queries.  A warp's first share is on its way
+// meanwhile.  CTAs behind the rows check the sequences.
+//
+// Measured on B200 (15,609 rows, 32 + 2 * 8 heads of 128, half of each turned, 330 MB): with
+// a row a CTA, 102 us; this way @@ us.
 template <int D, int G, bool INTERLEAVED>
-__global__ void __launch_bounds__(kMaxWarps * 32, 4)
-    write_rotary_kernel(const WriteParams p, int warps_of_rows) {
+__global__ void __launch_bounds__(kWriteWarps * 32, 4)
+    write_rotary_kernel(const WriteParams p, int shares) {
   using L = KeyLane<D, G>;
-  __shared__ __align__(16) float2 turn[D / 2];
-  __shared__ float4 split[D / 2];
+  __shared__ SplitTurns<D> turns[kWriteRows];
+  __shared__ RowPlace places[kWriteRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  if (int(blockIdx.x) >= p.batch.rows) {
-    kv4::check_sequences(p.batch, (int(blockIdx.x) - p.batch.rows) * warps + warp,
-                         (int(gridDim.x) - p.batch.rows) * warps, lane);
+  const int ctas = (p.batch.rows + p.rows_each - 1) / p.rows_each;
+  if (int(blockIdx.x) >= ctas) {
+    kv4::check_sequences(p.batch, (int(blockIdx.x) - ctas) * warps + warp,
+                         (int(gridDim.x) - ctas) * warps, lane);
     return;
   }
-  const int r = blockIdx.x;
+  const int r0 = int(blockIdx.x) * p.rows_each, n = min(p.rows_each, p.batch.rows - r0);
   const Units<INTERLEAVED> u(p.spec.dim, D, p.copy_q);
-  const unsigned units = unsigned(p.q_heads) * unsigned(u.all);
-  const int b = kv4::find_sequence(p.batch, r, lane);
-  if (b < 0) return;
-  const kv4::Sequence seq = kv4::load_sequence(p.batch, b);
-  if (r < seq.row0 || r >= seq.row0 + seq.rows) return;
-  const int token = seq.len - seq.rows + (r - seq.row0);
+  const int units = p.q_heads * u.all;
   bool ready = false;
-  auto make_turns = [&] {
+  auto prepare = [&] {
     if (ready) return;
     ready = true;
-    const int position = p.positions != nullptr ? p.positions[r] : token;
-    for (int j = threadIdx.x; j < u.half; j += blockDim.x) {
-      const float2 t = turn_of(position, p.spec.freqs[j], p.spec.amplitude);
+    for (int i = warp; i < n; i += warps) {
+      const int r = r0 + i, b = kv4::find_sequence(p.batch, r, lane);
+      RowPlace at = {-1, -1, 0, 0};
+      if (b >= 0) {
+        const kv4::Sequence seq = kv4::load_sequence(p.batch, b);
+        if (r >= seq.row0 && r < seq.row0 + seq.rows) {
+          const int token = seq.len - seq.rows + (r - seq.row0);
+          at.seq = b;
+          at.position = p.positions != nullptr ? p.positions[r] : token;
+          if (token >= 0) at.page = kv4::load_page(p.batch, p.cache, b, token);
+          at.slot = token & ((1 << p.cache.page_shift) - 1);
+        }
+      }
+      if (lane == 0) places[i] = at;
+    }
+    __syncthreads();
+    for (int j = threadIdx.x; j < n * u.half; j += blockDim.x) {
+      const int i = j / u.half, f = j - i * u.half;
+      if (places[i].seq < 0) continue;
+      const float2 t = turn_of(places[i].position, p.spec.freqs[f], p.spec.amplitude);
       const float2 c = split16(t.x), s = split16(t.y);
-      turn[j] = t;
-      split[j] = make_float4(c.x, c.y, s.x, s.y);
+      put_turn(t, f, u.half, INTERLEAVED, turns[i].c, turns[i].n);
+      put_turn(make_float2(c.x, s.x), f, u.half, INTERLEAVED, turns[i].c_high, turns[i].n_high);
+      put_turn(make_float2(c.y, s.y), f, u.half, INTERLEAVED, turns[i].c_low, turns[i].n_low);
     }
     __syncthreads();
   };
-  for (int item = warp; item < warps_of_rows; item += warps) {
+  for (int work = warp; work < n * shares; work += warps) {
+    const int row = work / shares, item = work - row * shares, r = r0 + row;
+    const SplitTurns<D>& t = turns[row];
     if (item >= p.chunks) {
-      // ---- queries
-      const unsigned i0 = unsigned(item - p.chunks) * (32 * kQueryUnits) + lane;
+    // ---- queries
+      const int i0 = (item - p.chunks) * (32 * kQueryUnits) + lane;
       uint4 a[kQueryUnits], c[kQueryUnits];
 #pragma unroll
       for (int k = 0; k < kQueryUnits; ++k) {
-        const unsigned i = i0 + 32 * k, head = i / unsigned(u.all);
-        const int unit = int(i - head * unsigned(u.all));
+        const int i = i0 + 32 * k, head = p.by_head(i), unit = i - head * u.all;
         const __nv_bfloat16* from =
             p.Q + int64_t(r) * p.q_stride + int64_t(head) * D + u.offset(unit);
         a[k] = c[k] = make_uint4(0, 0, 0, 0);
@@ -328,18 +409,18 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4)
             c[k] = *reinterpret_cast<const uint4*>(from + u.half);
         }
       }
-      make_turns();
+      prepare();
+      if (places[row].seq < 0) continue;
 #pragma unroll
       for (int k = 0; k < kQueryUnits; ++k) {
-        const unsigned i = i0 + 32 * k, head = i / unsigned(u.all);
-        const int unit = int(i - head * unsigned(u.all));
+        const int i = i0 + 32 * k, head = p.by_head(i), unit = i - head * u.all;
         if (i >= units) continue;
         __nv_bfloat16* to = p.Q_out + int64_t(r) * p.qo_stride + int64_t(head) * D + u.offset(unit);
         if (unit < u.turned) {
           if (INTERLEAVED) {
-            turn_interleaved(a[k], turn + 4 * unit, 4);
+            turn_interleaved(a[k], t.c + 8 * unit, t.n + 8 * unit, 4);
           } else {
-            turn_runs(a[k], c[k], turn + 8 * unit);
+            turn_runs(a[k], c[k], t.c + 8 * unit, t.n + 8 * unit);
             *reinterpret_cast<uint4*>(to + u.half) = c[k];
           }
         }
@@ -355,32 +436,29 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4)
     const __nv_bfloat16* from_v = p.V + int64_t(r) * p.v_stride + my.head * D + my.elem;
     // a run of eight keys lies in the first half of the turned elements, in the
     // second, or behind them (dim is a multiple of 16)
-    int run_at[2];
-    float sign[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int e = my.elem + 8 * i;
-      run_at[i] = e >= p.spec.dim ? -1 : INTERLEAVED ? e / 2 : e >= u.half ? e - u.half : e;
-      sign[i] = e < u.half ? 1.f : -1.f;
       k[i] = v[i] = z[i] = make_uint4(0, 0, 0, 0);
       if (there) {
         k[i] = *reinterpret_cast<const uint4*>(from_k + 8 * i);
         v[i] = *reinterpret_cast<const uint4*>(from_v + 8 * i);
-        if (!INTERLEAVED && run_at[i] >= 0)
-          z[i] = *reinterpret_cast<const uint4*>(from_k + 8 * i +
-                                                 (sign[i] > 0.f ? u.half : -u.half));
+        if (!INTERLEAVED && e < p.spec.dim)
+          z[i] = *reinterpret_cast<const uint4*>(from_k + 8 * i + (e < u.half ? u.half : -u.half));
       }
     }
-    make_turns();
-    if (token < 0) continue;  // the row holds no token
-    const int64_t page = kv4::load_page(p.batch, p.cache, b, token);
-    if (page < 0) continue;
-    const int slot = token & ((1 << p.cache.page_shift) - 1);
+    prepare();
+    const int64_t page = places[row].page;
+    if (page < 0) continue;  // no token, no sequence, or a bad page
+    const int slot = places[row].slot;
     const int64_t at = ((page * p.cache.kv_heads + my.head) << p.cache.page_shift) + slot;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (run_at[i] >= 0)
-        k[i] = turn_keys<INTERLEAVED>(k[i], z[i], sign[i], split + run_at[i]);
+    for (int i = 0; i < 2; ++i) {
+      if (INTERLEAVED)
+        z[i] = make_uint4(__byte_perm(k[i].x, 0u, 0x1032), __byte_perm(k[i].y, 0u, 0x1032),
+                          __byte_perm(k[i].z, 0u, 0x1032), __byte_perm(k[i].w, 0u, 0x1032));
+      if (my.elem + 8 * i < p.spec.dim) k[i] = turn_keys<D>(k[i], z[i], t, my.elem + 8 * i);
+    }
     float ks, kz, vs, vz;
     const uint2 kw = kv4::quantize16<G / 16>(k, &ks, &kz);
     const uint2 vw = kv4::swap_chunks(kv4::quantize16<G / 16>(v, &vs, &vz), my.odd);

@@ -14,6 +14,6 @@ cudaError_t run_kv4_write_rotary(const void* Q, int64_t q_stride, int q_heads, v
                                  int64_t qo_stride, const void* K, int64_t k_stride,
                                  const void* V, int64_t v_stride, const wq_rotary_spec& spec,
                                  const int* positions, const wq_kv4_cache& cache,
-                                 const wq_kv4_batch& batch, cudaStream_t s);
+                                 const wq_kv4_batch& batch, cudaStream_t s, int sms);
 
 }  // namespace wqh

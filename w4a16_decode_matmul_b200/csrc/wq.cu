@@ -753,7 +753,7 @@ wq_status wq_rotary_frequencies(int32_t dim, double base, int32_t scaling, doubl
 wq_status wq_rotary(const void* X, int64_t x_stride, int32_t rows, int32_t heads,
                     int32_t head_dim, const int32_t* positions, const wq_rotary_spec* spec,
                     unsigned int flags, void* Y, int64_t y_stride, wq_stream_t stream) {
-  if (rows < 0 || heads < 1 || heads > (1 << 20) || head_dim < 1) return WQ_ERR_INVALID_ARG;
+  if (rows < 0 || heads < 1 || heads > (1 << 16) || head_dim < 1) return WQ_ERR_INVALID_ARG;
   if ((flags & ~unsigned(WQ_ROTARY_TRANSPOSE)) != 0) return WQ_ERR_INVALID_ARG;
   if (head_dim % 8 != 0 || head_dim > 512) return WQ_ERR_UNSUPPORTED;
   wq_status st = check_rotary(spec, head_dim);
@@ -792,9 +792,11 @@ wq_status wq_kv4_write_rotary(const void* Q, int64_t q_stride, int32_t q_heads, 
   }
   if ((st = check_kv4_rows(K, k_stride, cache->kv_heads, cache->head_dim)) != WQ_OK) return st;
   if ((st = check_kv4_rows(V, v_stride, cache->kv_heads, cache->head_dim)) != WQ_OK) return st;
+  DeviceInfo dev;
+  if (!wqh::device_info(&dev)) return WQ_ERR_CUDA;
   return from_cuda(wqh::run_kv4_write_rotary(Q, q_stride, q_heads, Q_out, qo_stride, K, k_stride,
                                              V, v_stride, *spec, positions, *cache, *batch,
-                                             reinterpret_cast<cudaStream_t>(stream)));
+                                             reinterpret_cast<cudaStream_t>(stream), dev.sms));
 }
 
 // -------------------------------------------- verification of drafted tokens
