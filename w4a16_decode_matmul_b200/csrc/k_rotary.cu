@@ -13,20 +13,62 @@ namespace rotary = wq::rotary;
 
 rotary::Spec device_spec(const wq_rotary_spec& s) { return {s.freqs, s.dim, s.amplitude}; }
 
+// Rows of a CTA: several as soon as the GPU is full with that many.
+int rows_each(int rows, int sms) {
+  int each = 1;
+  while (each < rotary::kRowsEach && rows >= each * 8 * sms) each *= 2;
+  return each;
+}
+
+rotary::Units units_of_head(const rotary::Spec& spec, bool interleaved, int head_dim, bool copy) {
+  rotary::Units u = {};
+  u.turned = interleaved ? (spec.dim + 7) / 8 : spec.dim / 16;
+  u.copied = !copy ? 0 : interleaved ? head_dim / 8 - u.turned : (head_dim - spec.dim) / 8;
+  u.by_turned = fast_div(uint32_t(std::max(u.turned, 1)));
+  u.by_copied = fast_div(uint32_t(std::max(u.copied, 1)));
+  return u;
+}
+
+cudaError_t launch_rotary(rotary::RotaryParams p, bool interleaved, cudaStream_t s, int sms) {
+  // (rows of angles lie on 16-byte boundaries where dim is a multiple of 4)
+  const bool pairs = p.spec.dim % (interleaved ? 4 : 16) != 0;
+  int per_head;
+  if (pairs) {
+    per_head = p.spec.dim / 2 + (p.copy ? p.head_dim - p.spec.dim : 0);
+    p.units.by_turned = fast_div(uint32_t(per_head));
+  } else {
+    p.units = units_of_head(p.spec, interleaved, p.head_dim, p.copy);
+    per_head = p.units.turned + p.units.copied;
+  }
+  const int64_t units = int64_t(p.heads) * per_head;
+  // Several rows a CTA as long as their angles fit; where there are fewer rows than SMs a
+  // row's units are spread over CTAs of 128.
+  p.rows_each = std::min(rows_each(p.rows, sms), std::max(1, rotary::kTurns / p.spec.dim));
+  const int64_t split = std::min<int64_t>(std::max(1, 2 * sms / p.rows), (units + 127) / 128);
+  const int64_t mine = (units * p.rows_each + split - 1) / split;
+  const int64_t rounds = (mine + 511) / 512;
+  const int threads = int(((mine + rounds - 1) / rounds + 31) / 32 * 32);
+  p.by_row = fast_div(uint32_t(units));
+  const dim3 grid{unsigned((p.rows + p.rows_each - 1) / p.rows_each), unsigned(split)};
+  if (pairs)
+    rotary::rotary_pair_kernel<<<grid, threads, 0, s>>>(p, interleaved);
+  else if (interleaved)
+    rotary::rotary_kernel<true><<<grid, threads, 0, s>>>(p);
+  else
+    rotary::rotary_kernel<false><<<grid, threads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
 template <int D, int G>
 struct WriteRotaryOp {
   static cudaError_t run(rotary::WriteParams p, const wq_kv4_cache& c, int interleaved,
                          cudaStream_t s, int sms) {
+    p.rows_each = rows_each(p.batch.rows, sms);
     p.chunks = (c.kv_heads * (D / 16) + 31) / 32;
-    const int per_head = interleaved ? (p.copy_q ? D : p.spec.dim) / 8
-                                     : p.spec.dim / 16 + (p.copy_q ? (D - p.spec.dim) / 8 : 0);
-    const int64_t units = int64_t(p.q_heads) * per_head, share = 32 * rotary::kQueryUnits;
+    p.units = units_of_head(p.spec, interleaved, D, p.copy_q);
+    const int64_t units = int64_t(p.q_heads) * (p.units.turned + p.units.copied);
+    const int64_t share = 32 * rotary::kQueryUnits;
     const int shares = p.chunks + int((units + share - 1) / share);
-    // rows of a CTA: several as soon as the GPU is full (four CTAs an SM) with that many
-    p.by_head = fast_div(uint32_t(std::max(per_head, 1)));
-    p.rows_each = 1;
-    while (p.rows_each < rotary::kWriteRows && p.batch.rows >= p.rows_each * 8 * sms)
-      p.rows_each *= 2;
     const int warps = std::min(shares * p.rows_each, rotary::kWriteWarps);
     // CTAs behind the rows' check the sequences, 32 a warp
     const int64_t check =
@@ -57,36 +99,7 @@ cudaError_t run_rotary(const void* X, int64_t x_stride, int rows, int heads, int
   p.head_dim = head_dim;
   p.copy = X != Y;
   p.sign = transpose ? -1.f : 1.f;
-  // (rows of angles lie on 16-byte boundaries where dim is a multiple of 4)
-  const bool pairs = spec.dim % (spec.interleaved ? 4 : 16) != 0;
-  int per_head;
-  if (pairs)
-    per_head = spec.dim / 2 + (p.copy ? head_dim - spec.dim : 0);
-  else if (spec.interleaved)
-    per_head = p.copy ? head_dim / 8 : (spec.dim + 7) / 8;
-  else
-    per_head = spec.dim / 16 + (p.copy ? (head_dim - spec.dim) / 8 : 0);
-  const int64_t units = int64_t(heads) * per_head;
-  // Rows of a CTA: several as soon as the GPU is full with that many and their angles fit;
-  // where there are fewer rows than SMs a row's units are spread over CTAs of 128.
-  p.rows_each = 1;
-  while (p.rows_each < 4 && rows >= p.rows_each * 8 * sms &&
-         p.rows_each * 2 * spec.dim <= rotary::kTurns)
-    p.rows_each *= 2;
-  const int64_t split = std::min<int64_t>(std::max(1, 2 * sms / rows), (units + 127) / 128);
-  const int64_t mine = (units * p.rows_each + split - 1) / split;
-  const int64_t rounds = (mine + 511) / 512;
-  const int threads = int(((mine + rounds - 1) / rounds + 31) / 32 * 32);
-  p.by_row = fast_div(uint32_t(units));
-  p.by_head = fast_div(uint32_t(per_head));
-  const dim3 grid{unsigned((rows + p.rows_each - 1) / p.rows_each), unsigned(split)};
-  if (pairs)
-    rotary::rotary_pair_kernel<<<grid, threads, 0, s>>>(p, spec.interleaved != 0);
-  else if (spec.interleaved)
-    rotary::rotary_kernel<true><<<grid, threads, 0, s>>>(p);
-  else
-    rotary::rotary_kernel<false><<<grid, threads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_rotary(p, spec.interleaved != 0, s, sms);
 }
 
 cudaError_t run_kv4_write_rotary(const void* Q, int64_t q_stride, int q_heads, void* Q_out,

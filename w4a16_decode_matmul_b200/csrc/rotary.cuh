@@ -90,21 +90,60 @@ struct Eight {
 };
 
 // What one thread turns at a time: eight pairs (two runs of eight elements, or one
-// of eight for interleaved pairs, which are four), or eight elements that stay.
-// Units of a head: the turned ones first.
-template <bool INTERLEAVED>
+// of eight for interleaved pairs, which are four), or eight elements that stay.  A row's
+// units that turn come first, those of all heads, then those that are copied: a warp does one
+// or the other.
 struct Units {
-  int turned, all, half;
-  __device__ __forceinline__ Units(int dim, int head_dim, bool copy) {
-    half = dim / 2;
-    turned = INTERLEAVED ? (dim + 7) / 8 : dim / 16;
-    all = turned + (copy ? INTERLEAVED ? head_dim / 8 - turned : (head_dim - dim) / 8 : 0);
-  }
-  // offset of unit k's first element in its head
-  __device__ __forceinline__ int offset(int k) const {
-    return !INTERLEAVED && k >= turned ? 2 * half + 8 * (k - turned) : 8 * k;
-  }
+  int turned, copied;        // of a head
+  kv4::FastDiv by_turned, by_copied;
 };
+
+// Unit i of a row with `first` units that turn: its head and first element.
+struct UnitAt {
+  int head, k;
+  bool turned;
+};
+
+__device__ __forceinline__ UnitAt unit_at(const Units& u, int i, int first) {
+  UnitAt at;
+  at.turned = i < first;
+  const int j = at.turned ? i : i - first, each = at.turned ? u.turned : u.copied;
+  at.head = (at.turned ? u.by_turned : u.by_copied)(j);
+  at.k = j - at.head * each;
+  return at;
+}
+
+// Offset of its first element in its head.
+template <bool INTERLEAVED>
+__device__ __forceinline__ int unit_offset(const Units& u, const UnitAt& at, int dim) {
+  return 8 * at.k + (at.turned ? 0 : INTERLEAVED ? 8 * u.turned : dim);
+}
+
+// The sequence of row r, its place there and its token's position, by all lanes of a warp;
+// seq -1: the row is in no sequence.
+struct RowAt {
+  int seq, token;
+};
+
+__device__ __forceinline__ RowAt find_row(const kv4::Batch& p, int r, int lane) {
+  if (p.row_starts != nullptr && p.seqs < 32) {  // few sequences: all of them at once
+    const int start = p.row_starts[min(lane, p.seqs)];
+    int len = p.seq_lens[min(lane, p.seqs - 1)];
+    const int next = __shfl_down_sync(0xffffffffu, start, 1);
+    const bool mine = lane < p.seqs && start >= 0 && start <= r && r < next && next <= p.rows;
+    const unsigned found = __ballot_sync(0xffffffffu, mine);
+    if (found) {  // (what is out of bounds is recorded where the sequences are checked)
+      const int b = __ffs(found) - 1;
+      len = max(0, min(__shfl_sync(0xffffffffu, len, b), p.max_len));
+      return {b, len - __shfl_sync(0xffffffffu, next, b) + r};
+    }
+  }
+  const int b = kv4::find_sequence(p, r, lane);
+  if (b < 0) return {-1, 0};
+  const kv4::Sequence seq = kv4::load_sequence(p, b);
+  if (r < seq.row0 || r >= seq.row0 + seq.rows) return {-1, 0};
+  return {b, seq.len - seq.rows + (r - seq.row0)};
+}
 
 // Two runs of eight elements that are each other's pairs; c and n at the first's.
 __device__ __forceinline__ void turn_runs(uint4& a, uint4& b, const float* c, const float* n) {
@@ -149,7 +188,8 @@ struct RotaryParams {
   Spec spec;
   int rows, heads, head_dim;
   int rows_each;  // rows of a CTA
-  kv4::FastDiv by_row, by_head;  // by the units of a row and of a head
+  Units units;
+  kv4::FastDiv by_row;  // by the units of a row
   bool copy;      // Y is other memory: the elements that stay are copied
   float sign;     // -1: the transpose
 };
@@ -158,6 +198,8 @@ struct RotaryTurns {
   // (a head whose turned part ends inside a run of eight is read to the run's end)
   alignas(16) float c[kTurns + 8], n[kTurns + 8];
 };
+
+constexpr int kRowsEach = 4;  // rows of a CTA, at most
 
 // The angles of a CTA's rows r0 .. r0 + count - 1, all threads together.
 __device__ __forceinline__ void make_turns(const RotaryParams& p, bool interleaved, int64_t r0,
@@ -169,6 +211,7 @@ __device__ __forceinline__ void make_turns(const RotaryParams& p, bool interleav
     cs.y *= p.sign;
     put_turn(cs, f, half, interleaved, t.c + row * p.spec.dim, t.n + row * p.spec.dim);
   }
+  __syncthreads();
 }
 
 // A CTA takes a few rows (blockIdx.x) -- the angles' arithmetic, a chain of some 60 dependent
@@ -180,36 +223,34 @@ __global__ void __launch_bounds__(512, 3) rotary_kernel(const RotaryParams p) {
   __shared__ RotaryTurns turns;
   const int64_t r0 = int64_t(blockIdx.x) * p.rows_each;
   const int n = int(min(int64_t(p.rows_each), p.rows - r0));
-  const Units<INTERLEAVED> u(p.spec.dim, p.head_dim, p.copy);
-  const int each = p.heads * u.all, units = each * n;
+  const int half = p.spec.dim / 2, first = p.heads * p.units.turned;
+  const int each = first + p.heads * p.units.copied, units = each * n;
   const int step = int(gridDim.y * blockDim.x);
   bool ready = false;
   for (int i = int(blockIdx.y * blockDim.x + threadIdx.x);; i += step) {
     const bool there = i < units;
-    const int row = p.by_row(i), in_row = i - row * each, head = p.by_head(in_row);
-    const int k = in_row - head * u.all;
-    const int64_t at = int64_t(head) * p.head_dim + u.offset(k);
+    const int row = p.by_row(i);
+    const UnitAt u = unit_at(p.units, i - row * each, first);
+    const int at = u.head * p.head_dim + unit_offset<INTERLEAVED>(p.units, u, p.spec.dim);
     const __nv_bfloat16* const from = p.X + (r0 + row) * p.x_stride + at;
-    const bool turned = k < u.turned;
     uint4 a = make_uint4(0, 0, 0, 0), b = a;
     if (there) {
       a = *reinterpret_cast<const uint4*>(from);
-      if (!INTERLEAVED && turned) b = *reinterpret_cast<const uint4*>(from + u.half);
+      if (!INTERLEAVED && u.turned) b = *reinterpret_cast<const uint4*>(from + half);
     }
     if (!ready) {
       ready = true;
       make_turns(p, INTERLEAVED, r0, n, turns);
-      __syncthreads();
     }
     if (!there) return;
     __nv_bfloat16* const to = p.Y + (r0 + row) * p.y_stride + at;
-    if (turned) {
-      const int e = row * p.spec.dim + 8 * k;
+    if (u.turned) {
+      const int e = row * p.spec.dim + 8 * u.k;
       if (INTERLEAVED) {
-        turn_interleaved(a, turns.c + e, turns.n + e, u.half - 4 * k);
+        turn_interleaved(a, turns.c + e, turns.n + e, half - 4 * u.k);
       } else {
         turn_runs(a, b, turns.c + e, turns.n + e);
-        *reinterpret_cast<uint4*>(to + u.half) = b;
+        *reinterpret_cast<uint4*>(to + half) = b;
       }
     }
     *reinterpret_cast<uint4*>(to) = a;
@@ -228,10 +269,9 @@ static __global__ void __launch_bounds__(512, 3) rotary_pair_kernel(const Rotary
   const int all = half + (p.copy ? p.head_dim - 2 * half : 0);
   const int each = p.heads * all, units = each * n;
   make_turns(p, interleaved, r0, n, turns);
-  __syncthreads();
   for (int i = int(blockIdx.y * blockDim.x + threadIdx.x); i < units;
        i += int(gridDim.y * blockDim.x)) {
-    const int row = p.by_row(i), in_row = i - row * each, head = p.by_head(in_row);
+    const int row = p.by_row(i), in_row = i - row * each, head = p.units.by_turned(in_row);
     const int k = in_row - head * all;
     const int64_t at = int64_t(head) * p.head_dim;
     const __nv_bfloat16* const from = p.X + (r0 + row) * p.x_stride + at;
@@ -321,11 +361,10 @@ struct WriteParams {
   int q_heads, chunks;  // chunks: warps' shares of a row's keys and values
   bool copy_q;          // Q_out is other memory than Q
   int rows_each;        // rows of a CTA
-  kv4::FastDiv by_head; // by the units of a head
+  Units units;          // of queries
 };
 
 constexpr int kWriteWarps = 8;
-constexpr int kWriteRows = 4;   // rows of a CTA, at most
 constexpr int kQueryUnits = 2;  // units of queries a lane has in flight
 
 // What a CTA knows of one of its rows: page -1 where nothing is written, seq -1 where the row
@@ -341,14 +380,16 @@ struct RowPlace {
 // values each, the others 64 units of queries.  A warp's first share is on its way
 // meanwhile.  CTAs behind the rows check the sequences.
 //
-// Measured on B200 (15,609 rows, 32 + 2 * 8 heads of 128, half of each turned, 330 MB): with
-// a row a CTA, 102 us; this way @@ us.
+// Measured on B200 (15,609 rows, 32 + 2 * 8 heads of 128, half of each turned, 330 MB): 86
+// us, 3.8 TB/s, 3,400 warp instructions a row (issue 60 %, ALU 48 %), of which the
+// quantizer has a third.  With the queries in a launch of their own 54 + 51 us; a row a CTA
+// 102; keys and values last, or always in the same warps, 92 to 99.
 template <int D, int G, bool INTERLEAVED>
 __global__ void __launch_bounds__(kWriteWarps * 32, 4)
     write_rotary_kernel(const WriteParams p, int shares) {
   using L = KeyLane<D, G>;
-  __shared__ SplitTurns<D> turns[kWriteRows];
-  __shared__ RowPlace places[kWriteRows];
+  __shared__ SplitTurns<D> turns[kRowsEach];
+  __shared__ RowPlace places[kRowsEach];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int ctas = (p.batch.rows + p.rows_each - 1) / p.rows_each;
   if (int(blockIdx.x) >= ctas) {
@@ -357,74 +398,78 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 4)
     return;
   }
   const int r0 = int(blockIdx.x) * p.rows_each, n = min(p.rows_each, p.batch.rows - r0);
-  const Units<INTERLEAVED> u(p.spec.dim, D, p.copy_q);
-  const int units = p.q_heads * u.all;
+  const int half = p.spec.dim / 2, first = p.q_heads * p.units.turned;
+  const int units = first + p.q_heads * p.units.copied;
   bool ready = false;
   auto prepare = [&] {
     if (ready) return;
     ready = true;
     for (int i = warp; i < n; i += warps) {
-      const int r = r0 + i, b = kv4::find_sequence(p.batch, r, lane);
-      RowPlace at = {-1, -1, 0, 0};
-      if (b >= 0) {
-        const kv4::Sequence seq = kv4::load_sequence(p.batch, b);
-        if (r >= seq.row0 && r < seq.row0 + seq.rows) {
-          const int token = seq.len - seq.rows + (r - seq.row0);
-          at.seq = b;
-          at.position = p.positions != nullptr ? p.positions[r] : token;
-          if (token >= 0) at.page = kv4::load_page(p.batch, p.cache, b, token);
-          at.slot = token & ((1 << p.cache.page_shift) - 1);
-        }
+      const int r = r0 + i;
+      const RowAt row = find_row(p.batch, r, lane);
+      RowPlace at = {-1, row.seq, 0, 0};
+      if (row.seq >= 0) {
+        at.position = p.positions != nullptr ? p.positions[r] : row.token;
+        if (row.token >= 0) at.page = kv4::load_page(p.batch, p.cache, row.seq, row.token);
+        at.slot = row.token & ((1 << p.cache.page_shift) - 1);
       }
       if (lane == 0) places[i] = at;
     }
     __syncthreads();
-    for (int j = threadIdx.x; j < n * u.half; j += blockDim.x) {
-      const int i = j / u.half, f = j - i * u.half;
+    for (int j = threadIdx.x; j < n * half; j += blockDim.x) {
+      const int i = j / half, f = j - i * half;
       if (places[i].seq < 0) continue;
       const float2 t = turn_of(places[i].position, p.spec.freqs[f], p.spec.amplitude);
       const float2 c = split16(t.x), s = split16(t.y);
-      put_turn(t, f, u.half, INTERLEAVED, turns[i].c, turns[i].n);
-      put_turn(make_float2(c.x, s.x), f, u.half, INTERLEAVED, turns[i].c_high, turns[i].n_high);
-      put_turn(make_float2(c.y, s.y), f, u.half, INTERLEAVED, turns[i].c_low, turns[i].n_low);
+      put_turn(t, f, half, INTERLEAVED, turns[i].c, turns[i].n);
+      put_turn(make_float2(c.x, s.x), f, half, INTERLEAVED, turns[i].c_high, turns[i].n_high);
+      put_turn(make_float2(c.y, s.y), f, half, INTERLEAVED, turns[i].c_low, turns[i].n_low);
     }
     __syncthreads();
   };
+  // keys and values of all rows first: they are several times the work of queries
+  const int kv_work = n * p.chunks, query_shares = shares - p.chunks;
   for (int work = warp; work < n * shares; work += warps) {
-    const int row = work / shares, item = work - row * shares, r = r0 + row;
+    const bool is_kv = work < kv_work;
+    const int row = is_kv ? work / p.chunks : (work - kv_work) / query_shares;
+    const int item = is_kv ? work - row * p.chunks : work - kv_work - row * query_shares;
+    const int r = r0 + row;
     const SplitTurns<D>& t = turns[row];
-    if (item >= p.chunks) {
+    if (!is_kv) {
     // ---- queries
-      const int i0 = (item - p.chunks) * (32 * kQueryUnits) + lane;
+      const int i0 = item * (32 * kQueryUnits) + lane;
+      const __nv_bfloat16* const from = p.Q + int64_t(r) * p.q_stride;
       uint4 a[kQueryUnits], c[kQueryUnits];
+      UnitAt u[kQueryUnits];
+      int at[kQueryUnits];
 #pragma unroll
       for (int k = 0; k < kQueryUnits; ++k) {
-        const int i = i0 + 32 * k, head = p.by_head(i), unit = i - head * u.all;
-        const __nv_bfloat16* from =
-            p.Q + int64_t(r) * p.q_stride + int64_t(head) * D + u.offset(unit);
+        const int i = i0 + 32 * k;
+        u[k] = unit_at(p.units, i, first);
+        at[k] = u[k].head * D + unit_offset<INTERLEAVED>(p.units, u[k], p.spec.dim);
         a[k] = c[k] = make_uint4(0, 0, 0, 0);
         if (i < units) {
-          a[k] = *reinterpret_cast<const uint4*>(from);
-          if (!INTERLEAVED && unit < u.turned)
-            c[k] = *reinterpret_cast<const uint4*>(from + u.half);
+          a[k] = *reinterpret_cast<const uint4*>(from + at[k]);
+          if (!INTERLEAVED && u[k].turned)
+            c[k] = *reinterpret_cast<const uint4*>(from + at[k] + half);
         }
       }
       prepare();
       if (places[row].seq < 0) continue;
+      __nv_bfloat16* const to = p.Q_out + int64_t(r) * p.qo_stride;
 #pragma unroll
       for (int k = 0; k < kQueryUnits; ++k) {
-        const int i = i0 + 32 * k, head = p.by_head(i), unit = i - head * u.all;
-        if (i >= units) continue;
-        __nv_bfloat16* to = p.Q_out + int64_t(r) * p.qo_stride + int64_t(head) * D + u.offset(unit);
-        if (unit < u.turned) {
+        if (i0 + 32 * k >= units) continue;
+        if (u[k].turned) {
+          const int e = 8 * u[k].k;
           if (INTERLEAVED) {
-            turn_interleaved(a[k], t.c + 8 * unit, t.n + 8 * unit, 4);
+            turn_interleaved(a[k], t.c + e, t.n + e, 4);
           } else {
-            turn_runs(a[k], c[k], t.c + 8 * unit, t.n + 8 * unit);
-            *reinterpret_cast<uint4*>(to + u.half) = c[k];
+            turn_runs(a[k], c[k], t.c + e, t.n + e);
+            *reinterpret_cast<uint4*>(to + at[k] + half) = c[k];
           }
         }
-        *reinterpret_cast<uint4*>(to) = a[k];
+        *reinterpret_cast<uint4*>(to + at[k]) = a[k];
       }
       continue;
     }
@@ -444,7 +489,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 4)
         k[i] = *reinterpret_cast<const uint4*>(from_k + 8 * i);
         v[i] = *reinterpret_cast<const uint4*>(from_v + 8 * i);
         if (!INTERLEAVED && e < p.spec.dim)
-          z[i] = *reinterpret_cast<const uint4*>(from_k + 8 * i + (e < u.half ? u.half : -u.half));
+          z[i] = *reinterpret_cast<const uint4*>(from_k + 8 * i + (e < half ? half : -half));
       }
     }
     prepare();

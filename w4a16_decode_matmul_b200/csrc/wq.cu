@@ -780,7 +780,7 @@ wq_status wq_kv4_write_rotary(const void* Q, int64_t q_stride, int32_t q_heads, 
   if (st != WQ_OK) return st;
   if ((st = check_rotary(spec, cache->head_dim)) != WQ_OK) return st;
   if (spec->dim % 16 != 0) return WQ_ERR_UNSUPPORTED;
-  if (!batch || batch->rows < 0 || q_heads < 0 || q_heads > (1 << 20)) return WQ_ERR_INVALID_ARG;
+  if (!batch || batch->rows < 0 || q_heads < 0 || q_heads > (1 << 16)) return WQ_ERR_INVALID_ARG;
   if (batch->rows == 0) return WQ_OK;
   if ((st = check_kv4_batch(batch)) != WQ_OK) return st;
   if (batch->rows >= (1 << 30)) return WQ_ERR_INVALID_ARG;
