@@ -56,9 +56,13 @@ cudaError_t launch(verify::Params p, cudaStream_t s, int sms) {
     return launch_one(verify::verify_kernel<T, LOGITS, 16>, p, int64_t(p.seqs) * p.ctas, 512,
                       p.ctas, LOGITS, s);
   }
-  p.share = int(std::max<int64_t>(verify::kShareLeast,
-                                  ((most + verify::kShares - 1) / verify::kShares + kStep - 1) /
-                                      kStep * kStep));
+  // Elements of a share: so many that there are 24 warps an SM, since a warp alone is bound by
+  // the latency of its exponentials, but not more than 1,024, for the balance of the last
+  // ones, nor so few that a row has more than kShares.
+  const auto steps = [](int64_t n) { return (n + kStep - 1) / kStep * kStep; };
+  const int64_t even = steps(most * p.seqs / (24 * int64_t(sms)) + 1);
+  p.share = int(std::max(std::min<int64_t>(verify::kShareMost, even),
+                         steps((most + verify::kShares - 1) / verify::kShares)));
   p.n_shares = int((most + p.share - 1) / p.share);
   const int64_t ctas =
       int64_t(p.seqs) * ((p.n_shares + verify::kShareWarps - 1) / verify::kShareWarps);

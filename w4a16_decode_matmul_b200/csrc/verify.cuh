@@ -51,7 +51,7 @@ constexpr int kMaxWarps = 16;    // of verify_kernel
 constexpr int kMaxCluster = 8;
 constexpr int kShares = 256;     // of a row, at most, in share_kernel
 constexpr int kShareWarps = 4;   // of its CTAs, a warp a share
-constexpr int kShareLeast = 1024; // elements of a share
+constexpr int kShareMost = 1024; // elements of a share, where a row's do not make more than kShares
 constexpr int kDecideWarps = 16;
 constexpr int kFindWarps = 16;
 
