@@ -522,7 +522,7 @@ enum {
 };
 
 typedef struct wq_verification {
-    int32_t rows, seqs, vocab;  /* vocab 1 .. 2^30                               */
+    int32_t rows, seqs, vocab;  /* rows and seqs up to 2^23, vocab 1 .. 2^30     */
     int32_t dtype;              /* of target and draft: WQ_OUT_F32, WQ_OUT_BF16  */
     uint32_t flags;             /* 0 or WQ_VERIFY_LOGITS                         */
     const int32_t *row_starts;  /* [seqs + 1] as in wq_kv4_batch, or NULL        */

@@ -931,9 +931,10 @@ def verify_drafts(target: torch.Tensor, tokens: torch.Tensor, uniform: torch.Ten
     ts = _verify_rows(target, rows, vocab, target.dtype, index, "target")
     ds = 0 if draft is None else _verify_rows(draft, rows, vocab, target.dtype, index, "draft")
     if out is None:
+        make = torch.empty if rows else torch.zeros       # without rows nothing is launched
         out = (torch.full((rows,), -1, dtype=_I32, device=target.device),
-               torch.empty((seqs,), dtype=_I32, device=target.device),
-               None if seq_lens is None else torch.empty_like(seq_lens))
+               make((seqs,), dtype=_I32, device=target.device),
+               None if seq_lens is None else seq_lens.clone())
     if workspace is None:
         workspace = verify_workspace(max(rows, 1), target.device)
     elif workspace.get_device() != index or not workspace.is_contiguous():

@@ -16,7 +16,7 @@ rotary::Spec device_spec(const wq_rotary_spec& s) { return {s.freqs, s.dim, s.am
 // Rows of a CTA: several as soon as the GPU is full with that many.
 int rows_each(int rows, int sms) {
   int each = 1;
-  while (each < rotary::kRowsEach && rows >= each * 8 * sms) each *= 2;
+  while (each < rotary::kRowsEach && rows >= int64_t(each) * 8 * sms) each *= 2;
   return each;
 }
 
@@ -49,7 +49,7 @@ cudaError_t launch_rotary(rotary::RotaryParams p, bool interleaved, cudaStream_t
   const int64_t rounds = (mine + 511) / 512;
   const int threads = int(((mine + rounds - 1) / rounds + 31) / 32 * 32);
   p.by_row = fast_div(uint32_t(units));
-  const dim3 grid{unsigned((p.rows + p.rows_each - 1) / p.rows_each), unsigned(split)};
+  const dim3 grid{unsigned((int64_t(p.rows) + p.rows_each - 1) / p.rows_each), unsigned(split)};
   if (pairs)
     rotary::rotary_pair_kernel<<<grid, threads, 0, s>>>(p, interleaved);
   else if (interleaved)

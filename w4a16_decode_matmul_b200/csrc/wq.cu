@@ -809,7 +809,8 @@ wq_status wq_verify_drafts(const wq_verification* v, void* workspace, size_t wor
                            wq_stream_t stream) {
   if (!v || v->rows < 0) return WQ_ERR_INVALID_ARG;
   if (v->rows == 0) return WQ_OK;
-  if (v->seqs < 1 || v->vocab < 1 || v->vocab > (1 << 30) || (!v->row_starts && v->rows % v->seqs != 0))
+  if (v->rows > (1 << 23) || v->seqs < 1 || v->seqs > (1 << 23) || v->vocab < 1 ||
+      v->vocab > (1 << 30) || (!v->row_starts && v->rows % v->seqs != 0))
     return WQ_ERR_INVALID_ARG;
   if (v->dtype != WQ_OUT_F32 && v->dtype != WQ_OUT_BF16) return WQ_ERR_INVALID_ARG;
   if ((v->flags & ~uint32_t(WQ_VERIFY_LOGITS)) != 0) return WQ_ERR_INVALID_ARG;
