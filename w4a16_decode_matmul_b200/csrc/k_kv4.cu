@@ -5,8 +5,7 @@
 #include <cmath>
 
 #include "kv4_host.h"
-#include "kv4_launch.cuh"
-#include "kv4_attn.cuh"
+#include "kv4_attn_launch.cuh"
 #include "kv4_prefill.cuh"
 
 namespace wqh {
@@ -60,57 +59,6 @@ struct ReadOp {
   }
 };
 
-template <int D, int G, int NT, int WARPS, int TILES>
-cudaError_t launch_attn(const kv4::AttnParams& p, bool after, cudaStream_t s, int sms) {
-  using C = kv4::AttnConfig<D, G, NT, WARPS>;
-  constexpr size_t smem = C::kOffCtl + C::kCtlBytes;
-  static_assert(smem <= 232448, "shared memory of one CTA");
-  static int configured[kMaxDevices] = {};
-  auto kernel = kv4::attn_kernel<D, G, NT, WARPS, TILES>;
-  const cudaError_t e = configure_smem(kernel, configured, smem);
-  if (e != cudaSuccess) return e;
-  const unsigned ctas = unsigned(std::min(sms, kv4::kMaxCtas));
-  if (!after) {
-    kernel<<<ctas, C::kThreads, smem, s>>>(p);
-    return cudaGetLastError();
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
-// Warps of a CTA and 16-token tiles per softmax step, by the registers that the
-// format needs (12 warps leave 168 a thread, 8 warps 255).  Measured on B200:
-//   one block of 8 columns, four groups: one tile 67 us, two (spilling) 118;
-//     one or two groups: 58 either way;
-//   two blocks of columns, groups of 64, head dim 128: 8 warps 46 us, 12
-//     (spilling) 72; head dim 64: 12 warps 34 us, 8 37.  Groups of 32 spill in
-//     both of the forms chosen (about 210 and 60 bytes).
-// A batch of up to four units of 32 tokens per warp takes 8 warps (one sequence
-// of 1,000 tokens, 8 kv heads: 10.1 us, with 12 warps 12.2; of 16,000: 16.7 and
-// 16.5); a larger one is limited by how many instructions are in flight (8
-// warps 63 us, 12 warps 55).
-template <int D, int G>
-struct AttnOp {
-  static cudaError_t run(const kv4::AttnParams& p, int max_columns, bool after, cudaStream_t s,
-                         int sms) {
-    constexpr int kTiles = D / G == 4 ? 1 : 2;
-    if (max_columns > 8) return launch_attn<D, G, 2, D == 64 ? 12 : 8, 1>(p, after, s, sms);
-    const int64_t units =
-        int64_t(p.batch.seqs) * p.cache.kv_heads * (p.batch.max_len / kv4::kUnit + 1);
-    if (units <= int64_t(4) * 8 * sms) return launch_attn<D, G, 1, 8, kTiles>(p, after, s, sms);
-    return launch_attn<D, G, 1, 12, kTiles>(p, after, s, sms);
-  }
-};
-
 // CTAs of the tensor-memory kernel that share a block's tokens: as many as fit
 // on the SMs together (each has a slot of the workspace), where that is two or
 // more.
@@ -140,7 +88,14 @@ bool prefer_prefill(const wq_kv4_batch& b, int kv_heads, int gqa, int sms) {
 
 constexpr size_t kCounterBytes = kv4::kMaxCtas * kv4::kMaxRows * 4;
 
-// The parameters that both forms of the attention share.
+}  // namespace
+
+size_t kv4_workspace_bytes() {
+  constexpr size_t few = kv4::AttnConfig<128, 32, 2, 8>::kPartialBytes;
+  constexpr size_t many = size_t(kv4::kMaxCtas) * kv4::kBlockRows * (128 + 2) * 4;
+  return round_up(kCounterBytes, 256) + std::max(few, many);
+}
+
 kv4::AttnParams attn_params(const void* Q, int64_t q_stride, int q_heads,
                             const wq_kv4_cache& cache, float scale, void* O, int64_t o_stride,
                             void* workspace) {
@@ -162,14 +117,6 @@ kv4::AttnParams attn_params(const void* Q, int64_t q_stride, int q_heads,
   p.wait_ns = g_kv4_wait_ns;
   p.max_columns = 1 << 30;
   return p;
-}
-
-}  // namespace
-
-size_t kv4_workspace_bytes() {
-  constexpr size_t few = kv4::AttnConfig<128, 32, 2, 8>::kPartialBytes;
-  constexpr size_t many = size_t(kv4::kMaxCtas) * kv4::kBlockRows * (128 + 2) * 4;
-  return round_up(kCounterBytes, 256) + std::max(few, many);
 }
 
 cudaError_t run_kv4_write(const void* K, int64_t k_stride, const void* V, int64_t v_stride,
@@ -205,23 +152,7 @@ cudaError_t run_kv4_attention(const void* Q, int64_t q_stride, int q_heads,
     p.max_columns = kFew;  // a ragged batch may hold both kinds
   }
   const int max_columns = int(std::min<int64_t>(bound * p.gqa, kFew));
-  return dispatch_kv4<AttnOp>(cache.head_dim, cache.group, p, max_columns, false, s, dev.sms);
-}
-
-cudaError_t run_kv4_attention_pages(const void* Q, int64_t q_stride, int q_heads,
-                                    const wq_kv4_cache& cache, int rows,
-                                    const wq_kv4_selection& sel, float scale, void* O,
-                                    int64_t o_stride, void* workspace, bool after,
-                                    cudaStream_t s, const DeviceInfo& dev) {
-  kv4::AttnParams p = attn_params(Q, q_stride, q_heads, cache, scale, O, o_stride, workspace);
-  const wq_kv4_batch each_row = {rows,       rows,      nullptr,
-                                 sel.lens,   sel.lists, sel.max_pages,
-                                 int64_t(sel.max_pages) * cache.kv_heads, 1};
-  p.batch = device_batch(each_row, cache.page_size);
-  if (p.batch.status == nullptr) return cudaErrorInitializationError;
-  p.head_stride = sel.max_pages;
-  return dispatch_kv4<AttnOp>(cache.head_dim, cache.group, p, std::min(p.gqa, kv4::kMaxRows),
-                              after, s, dev.sms);
+  return dispatch_kv4<Attn<false>::Op>(cache.head_dim, cache.group, p, max_columns, false, s, dev.sms);
 }
 
 }  // namespace wqh

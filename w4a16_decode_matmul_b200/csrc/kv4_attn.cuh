@@ -82,9 +82,8 @@ struct AttnParams {
   int64_t o_stride;
   int gqa;            // query heads per kv head
   int max_columns;    // sequences with more rows times gqa are another kernel's
-  // Elements from one kv head's pages to the next's in the page table: 0, or, where
-  // every head has a list of its own, its width.  There each row is a sequence, and one
-  // of negative length is left alone.
+  // With LISTS (every kv head has a page table of its own, each row is a sequence, and one
+  // of negative length is left alone): elements from one head's pages to the next's.
   int64_t head_stride;
   FastDiv by_gqa;
   float scale_log2;   // softmax scale times log2 e
@@ -148,10 +147,11 @@ struct AttnControl {
 };
 
 // Sequence b with its rows, none if it is another kernel's.
+template <bool LISTS>
 __device__ __forceinline__ Sequence attn_sequence(const AttnParams& p, int b) {
   Sequence s = load_sequence(p.batch, b);
   if (s.rows * p.gqa > p.max_columns) s.rows = 0;
-  if (p.head_stride != 0 && p.batch.seq_lens[b] < 0) s.rows = 0;
+  if (LISTS && p.batch.seq_lens[b] < 0) s.rows = 0;
   return s;
 }
 
@@ -182,7 +182,7 @@ __device__ __forceinline__ int64_t sequence_units(const AttnParams& p, const Seq
 }
 
 // The segment after s (its u0 follows); the caller knows that there is one.
-template <int ROWS>
+template <int ROWS, bool LISTS>
 __device__ __forceinline__ void next_segment(const AttnParams& p, Segment& s) {
   s.u0 += s.units;
   if (++s.h < p.cache.kv_heads) return;
@@ -191,7 +191,7 @@ __device__ __forceinline__ void next_segment(const AttnParams& p, Segment& s) {
   if (++s.rb >= row_blocks<ROWS>(q, p.gqa)) {
     s.rb = 0;
     do {
-      q = attn_sequence(p, ++s.b);
+      q = attn_sequence<LISTS>(p, ++s.b);
     } while (q.rows == 0);
     s.row0 = q.row0;
     s.rows = q.rows;
@@ -294,7 +294,7 @@ __device__ __forceinline__ int segment_at(const AttnParams& p, int b, const Sequ
 
 // The same for a warp that asks with all its lanes: the block's threads have
 // left the prefix sums of their sequences' units in shared memory.
-template <int ROWS, int WARPS>
+template <int ROWS, int WARPS, bool LISTS>
 __device__ __forceinline__ int find_segment(const AttnParams& p, const AttnControl<WARPS>& ctl,
                                             int per_thread, int64_t q, int lane, Segment* out) {
   int64_t sum = lane < WARPS ? ctl.warp_sum[lane] : 0;
@@ -311,12 +311,12 @@ __device__ __forceinline__ int find_segment(const AttnParams& p, const AttnContr
   const int64_t before = __shfl_up_sync(0xffffffffu, upto, 1);
   if (i > 0) rem -= __shfl_sync(0xffffffffu, before, i);
   int b = (w * 32 + i) * per_thread;
-  Sequence seq = attn_sequence(p, b);
+  Sequence seq = attn_sequence<LISTS>(p, b);
   while (per_thread > 1) {
     const int64_t n = sequence_units<ROWS>(p, seq);
     if (rem < n) break;
     rem -= n;
-    seq = attn_sequence(p, ++b);
+    seq = attn_sequence<LISTS>(p, ++b);
   }
   return segment_at<ROWS>(p, b, seq, rem, q, out);
 }
@@ -332,7 +332,7 @@ static __device__ __noinline__ void wait_for_copies(uint64_t* full, int stages, 
   }
 }
 
-template <int D, int G, int NT, int WARPS, int TILES>
+template <int D, int G, int NT, int WARPS, int TILES, bool LISTS>
 __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p) {
   using C = AttnConfig<D, G, NT, WARPS>;
   constexpr int NC = C::kChunks, NG = C::kGroups, ROWS = C::kRows, NS = C::kStages;
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
     ctl->pieces[warp] = 0u;
   }
   __syncwarp();
-  grid_dependency_wait();  // where it is launched as a dependent of what makes its lists
+  if (LISTS) grid_dependency_wait();  // launched as a dependent of what makes the lists
 
   // ---- the units of the batch.  Up to 32 sequences: every warp counts them
   // by itself, lane b sequence b.  More: thread i counts those of a contiguous
@@ -360,13 +360,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
   int64_t upto = 0, total = 0;
   if (few) {
     if (lane < p.batch.seqs) {
-      mine = attn_sequence(p, lane);
+      mine = attn_sequence<LISTS>(p, lane);
       upto = sequence_units<ROWS>(p, mine);
     }
   } else {
     const int b_begin = min(p.batch.seqs, tid * per_thread);
     const int b_end = min(p.batch.seqs, b_begin + per_thread);
-    for (int b = b_begin; b < b_end; ++b) upto += sequence_units<ROWS>(p, attn_sequence(p, b));
+    for (int b = b_begin; b < b_end; ++b) upto += sequence_units<ROWS>(p, attn_sequence<LISTS>(p, b));
   }
 #pragma unroll
   for (int m = 1; m < 32; m *= 2) {
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
                             __shfl_sync(0xffffffffu, mine.len, i)};
       unit = segment_at<ROWS>(p, i, seq, i > 0 ? q0 - skipped : q0, q0, &cs);
     } else {
-      unit = find_segment<ROWS>(p, *ctl, per_thread, q0, lane, &cs);
+      unit = find_segment<ROWS, WARPS, LISTS>(p, *ctl, per_thread, q0, lane, &cs);
     }
 
     // ---- copies.  Lane 4 sub + kind copies the codes or metadata of one run
@@ -437,7 +437,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
       const int pos = pf_unit * kUnit + (sub << sub_shift);
       if (sub < (kUnit >> sub_shift) && pos < pf.limit)
         pf_page = p.batch.page_table[int64_t(pf.b) * p.batch.table_stride +
-                                     pf.h * p.head_stride + (pos >> p.cache.page_shift)];
+                                     (LISTS ? pf.h * p.head_stride : 0) +
+                                     (pos >> p.cache.page_shift)];
     };
     auto copy_unit = [&](int s) {
       const int tok0 = pf_unit * kUnit;
@@ -460,7 +461,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
       }
       if (--to_copy > 0) {
         if (++pf_unit == pf.units) {
-          next_segment<ROWS>(p, pf);
+          next_segment<ROWS, LISTS>(p, pf);
           pf_unit = 0;
         }
         read_page();
@@ -909,7 +910,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
           }
         }
         if (left > 1) {
-          next_segment<ROWS>(p, cs);
+          next_segment<ROWS, LISTS>(p, cs);
           unit = 0;
           fresh = true;
           if (kAhead) load_queries(0);
