@@ -198,6 +198,7 @@ def queries(seed, n, heads, d):
     (3, 5, 16, [90_000], [1], 64, 1, 2),                       # a cluster of CTAs
     (8, 2, 32, [70_000, 40_000], [1, 1], 1000, 4, 4),
     (2, 2, 16, [40] * 45, [3] * 45, 2, 0, 1),
+    (1, 2, 16, [90_000, 70_000], [1, 1], 5000, 3, 2),          # more than the gathered places
     (1, 1, 16, [20_000] * 80, [8] * 80, 70, 1, 1),             # hundreds of rows
 ])
 def test_chosen_pages(d, heads, gqa, page, lens, rows, max_pages, first, last):

@@ -60,7 +60,7 @@ CASES = [  # rows, heads, head_dim, dim, interleaved
     (1, 1, 8, 2, False), (1, 40, 128, 128, False), (1, 40, 128, 128, True), (3, 5, 64, 64, False),
     (7, 3, 80, 34, False), (7, 3, 80, 34, True), (2, 9, 96, 20, True), (2, 9, 96, 20, False),
     (301, 8, 128, 64, False), (301, 8, 128, 66, False), (150, 1, 256, 256, True),
-    (40, 2, 512, 512, False), (40, 2, 512, 16, True), (1000, 40, 64, 64, True), (5, 200, 64, 48, False),
+    (40, 2, 512, 512, False), (3000, 3, 80, 34, False), (2500, 5, 64, 50, True), (1, 300, 512, 510, False), (40, 2, 512, 16, True), (1000, 40, 64, 64, True), (5, 200, 64, 48, False),
 ]
 
 

@@ -30,29 +30,28 @@ rotary::Units units_of_head(const rotary::Spec& spec, bool interleaved, int head
 }
 
 cudaError_t launch_rotary(rotary::RotaryParams p, bool interleaved, cudaStream_t s, int sms) {
-  // (rows of angles lie on 16-byte boundaries where dim is a multiple of 4)
-  const bool pairs = p.spec.dim % (interleaved ? 4 : 16) != 0;
-  int per_head;
-  if (pairs) {
-    per_head = p.spec.dim / 2 + (p.copy ? p.head_dim - p.spec.dim : 0);
-    p.units.by_turned = fast_div(uint32_t(per_head));
-  } else {
-    p.units = units_of_head(p.spec, interleaved, p.head_dim, p.copy);
-    per_head = p.units.turned + p.units.copied;
-  }
-  const int64_t units = int64_t(p.heads) * per_head;
   // Several rows a CTA as long as their angles fit; where there are fewer rows than SMs a
-  // row's units are spread over CTAs of 128.
+  // row is spread over several CTAs.
   p.rows_each = std::min(rows_each(p.rows, sms), std::max(1, rotary::kTurns / p.spec.dim));
-  const int64_t split = std::min<int64_t>(std::max(1, 2 * sms / p.rows), (units + 127) / 128);
+  const unsigned row_ctas = unsigned((int64_t(p.rows) + p.rows_each - 1) / p.rows_each);
+  const int few = std::max(1, 2 * sms / p.rows);
+  // (rows of angles lie on 16-byte boundaries where dim is a multiple of 4)
+  if (p.spec.dim % (interleaved ? 4 : 16) != 0) {
+    const dim3 grid{row_ctas, unsigned(std::min(few, p.heads))};
+    rotary::rotary_staged_kernel<<<grid, rotary::kStagedThreads, 0, s>>>(
+        p, interleaved, fast_div(uint32_t(p.head_dim / 8)), fast_div(uint32_t(p.heads)));
+    return cudaGetLastError();
+  }
+  p.units = units_of_head(p.spec, interleaved, p.head_dim, p.copy);
+  const int per_head = p.units.turned + p.units.copied;
+  const int64_t units = int64_t(p.heads) * per_head;
+  const int64_t split = std::min<int64_t>(few, (units + 127) / 128);
   const int64_t mine = (units * p.rows_each + split - 1) / split;
   const int64_t rounds = (mine + 511) / 512;
   const int threads = int(((mine + rounds - 1) / rounds + 31) / 32 * 32);
   p.by_row = fast_div(uint32_t(units));
-  const dim3 grid{unsigned((int64_t(p.rows) + p.rows_each - 1) / p.rows_each), unsigned(split)};
-  if (pairs)
-    rotary::rotary_pair_kernel<<<grid, threads, 0, s>>>(p, interleaved);
-  else if (interleaved)
+  const dim3 grid{row_ctas, unsigned(split)};
+  if (interleaved)
     rotary::rotary_kernel<true><<<grid, threads, 0, s>>>(p);
   else
     rotary::rotary_kernel<false><<<grid, threads, 0, s>>>(p);

@@ -237,11 +237,11 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectP
   // ---- queries, on their way while the sequence is looked up
   const __nv_bfloat16* const q =
       p.Q + int64_t(r) * p.q_stride + int64_t(head) * p.gqa * D + tid % D;
-  float held[kHeldHeads];
+  __nv_bfloat16 raw[kHeldHeads];
 #pragma unroll
   for (int i = 0; i < kHeldHeads; ++i) {
     const int h = tid / D + i * kHeadStep;
-    held[i] = h < p.gqa ? __bfloat162float(q[h * D]) : 0.f;
+    raw[i] = h < p.gqa ? q[h * D] : __ushort_as_bfloat16(0);
   }
   int* const list = p.lists + int64_t(unit) * p.max_pages;
   const int b = find_sequence(p.batch, r, lane);
@@ -256,15 +256,12 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectP
   const int* const table = p.batch.page_table + int64_t(max(b, 0)) * p.batch.table_stride;
   if (rank == 0)
     for (int i = count + tid; i < p.max_pages; i += kSelectThreads) list[i] = -1;
-  auto copy_pages = [&](int to, int from, int many) {
-    for (int i = tid; i < many; i += kSelectThreads) {
-      const int page = table[from + i];
-      if (page < 0 || page >= p.pages) record_status(kStatusInvalid, p.batch.status);
-      list[to + i] = page;
-    }
-  };
   if (n <= p.max_pages) {
-    if (rank == 0) copy_pages(0, 0, n);
+    for (int i = tid; rank == 0 && i < n; i += kSelectThreads) {
+      const int page = table[i];
+      if (page < 0 || page >= p.pages) record_status(kStatusInvalid, p.batch.status);
+      list[i] = page;
+    }
     if (p.ctas > 1) cluster_wait();
     grid_dependency_wait();  // the grid may not be over before the one that it depends on
     return;
@@ -286,9 +283,12 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectP
   read_table(warp * kWarpPages);
 
   // ---- the group's queries: largest magnitude, then the sums of their 8-bit values
-  float top = 0.f;
+  float top = 0.f, held[kHeldHeads];
 #pragma unroll
-  for (int i = 0; i < kHeldHeads; ++i) top = fmaxf(top, fabsf(held[i]));
+  for (int i = 0; i < kHeldHeads; ++i) {
+    held[i] = __bfloat162float(raw[i]);
+    top = fmaxf(top, fabsf(held[i]));
+  }
   for (int h = tid / D + kHeldHeads * kHeadStep; h < p.gqa; h += kHeadStep)
     top = fmaxf(top, fabsf(__bfloat162float(q[h * D])));
 #pragma unroll
@@ -463,12 +463,9 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectP
   const uint32_t limit_key = wanted == 0 ? 0xffffffffu : all ? low - 1u : low;
   if (all) ties = 0u;
 
-  // ---- the pages.  Warp w has a contiguous part of the middle ones.  Their places are
-  // gathered first (where they fit the histogram's memory), so that the look-ups in the
-  // page table are on their way together.
-  copy_pages(0, 0, p.first);
-  copy_pages(count - p.last, n - p.last, p.last);
-  const bool gather = wanted <= kBins;
+  // ---- the pages.  Warp w has a contiguous part of the middle ones; their places are
+  // gathered first, in the histogram's memory, as many as it holds at a time, so that the
+  // look-ups in the page table are on their way together.
   const int chunk = ((middle + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
   const int c0 = min(middle, warp * chunk), c1 = min(middle, c0 + chunk);
   uint32_t over = 0u, equal = 0u;
@@ -484,29 +481,42 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectP
 #pragma unroll
   for (int w = 0; w < kSelectWarps; ++w)
     if (w < warp) over += ctl.warp_sum[w], equal += ctl.low[w];
-  for (int j = c0 + lane; j - lane < c1; j += 32) {
-    const uint32_t key = j < c1 ? keys[j] : 0u;
-    const bool is_over = j < c1 && key > limit_key, is_equal = j < c1 && key == limit_key;
-    const uint32_t over_mask = __ballot_sync(0xffffffffu, is_over);
-    const uint32_t equal_mask = __ballot_sync(0xffffffffu, is_equal);
-    const uint32_t below = (1u << lane) - 1u;
-    const uint32_t my_equal = equal + __popc(equal_mask & below);
-    if (is_over || (is_equal && my_equal < ties)) {
-      const uint32_t to = over + __popc(over_mask & below) + min(my_equal, ties);
-      if (to < uint32_t(wanted)) {
-        if (gather)
-          ctl.hist[to] = uint32_t(p.first + j);
-        else
-          list[p.first + to] = table[p.first + j];
+  for (int g0 = 0; g0 == 0 || g0 < wanted; g0 += kBins) {
+    uint32_t passed = over, level = equal;
+    for (int j = c0 + lane; j - lane < c1; j += 32) {
+      const uint32_t key = j < c1 ? keys[j] : 0u;
+      const bool is_over = j < c1 && key > limit_key, is_equal = j < c1 && key == limit_key;
+      const uint32_t over_mask = __ballot_sync(0xffffffffu, is_over);
+      const uint32_t equal_mask = __ballot_sync(0xffffffffu, is_equal);
+      const uint32_t below = (1u << lane) - 1u;
+      const uint32_t my_equal = level + __popc(equal_mask & below);
+      if (is_over || (is_equal && my_equal < ties)) {
+        const int to = int(passed + __popc(over_mask & below) + min(my_equal, ties)) - g0;
+        if (to >= 0 && to < kBins) ctl.hist[to] = uint32_t(p.first + j);
       }
+      passed += __popc(over_mask);
+      level += __popc(equal_mask);
     }
-    over += __popc(over_mask);
-    equal += __popc(equal_mask);
-  }
-  if (gather) {
     __syncthreads();
-    for (int i = tid; i < wanted; i += kSelectThreads)
-      list[p.first + i] = table[min(ctl.hist[i], uint32_t(n - 1))];
+    // the first and the last pages with the first group
+    const int from = g0 == 0 ? 0 : p.first + g0;
+    const int upto = g0 == 0 ? count : min(p.first + g0 + kBins, count - p.last);
+    for (int i = from + tid; i < upto; i += kSelectThreads) {
+      const int mid = i - p.first - g0;  // of this group
+      int j;
+      if (i < p.first)
+        j = i;
+      else if (i >= count - p.last)
+        j = n - (count - i);
+      else if (mid < kBins)
+        j = int(min(ctl.hist[mid], uint32_t(n - 1)));
+      else
+        continue;
+      const int page = table[j];
+      if (page < 0 || page >= p.pages) record_status(kStatusInvalid, p.batch.status);
+      list[i] = page;
+    }
+    __syncthreads();
   }
 }
 

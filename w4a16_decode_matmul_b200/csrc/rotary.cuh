@@ -257,35 +257,61 @@ __global__ void __launch_bounds__(512, 3) rotary_kernel(const RotaryParams p) {
   }
 }
 
-// The same where a thread's unit would not lie on 16-byte boundaries of the angles or the
-// row (dim not a multiple of 16 in halves, of 8 side by side): a pair, or an element
-// that stays, at a time.
-static __global__ void __launch_bounds__(512, 3) rotary_pair_kernel(const RotaryParams p,
-                                                                     bool interleaved) {
+// The same where the other elements of a run's pairs, or its angles, do not lie on 16-byte
+// boundaries (dim not a multiple of 16 in halves, of 4 side by side).  Heads go through
+// shared memory, 16 KB of whole heads at a time, so that memory is read and written in
+// runs all the same (a pair a thread, two bytes at a time, took @@ times as long), and
+// each run is read by all before it is written where Y is X.
+constexpr int kStaged = 8192;  // elements
+constexpr int kStagedThreads = 256;
+
+static __global__ void __launch_bounds__(kStagedThreads, 4)
+    rotary_staged_kernel(const RotaryParams p, bool interleaved, kv4::FastDiv by_runs,
+                         kv4::FastDiv by_heads) {
   __shared__ RotaryTurns turns;
+  __shared__ __align__(16) __nv_bfloat16 staged[kStaged];
   const int64_t r0 = int64_t(blockIdx.x) * p.rows_each;
   const int n = int(min(int64_t(p.rows_each), p.rows - r0));
-  const int half = p.spec.dim / 2;
-  const int all = half + (p.copy ? p.head_dim - 2 * half : 0);
-  const int each = p.heads * all, units = each * n;
-  make_turns(p, interleaved, r0, n, turns);
-  for (int i = int(blockIdx.y * blockDim.x + threadIdx.x); i < units;
-       i += int(gridDim.y * blockDim.x)) {
-    const int row = p.by_row(i), in_row = i - row * each, head = p.units.by_turned(in_row);
-    const int k = in_row - head * all;
-    const int64_t at = int64_t(head) * p.head_dim;
-    const __nv_bfloat16* const from = p.X + (r0 + row) * p.x_stride + at;
-    __nv_bfloat16* const to = p.Y + (r0 + row) * p.y_stride + at;
-    if (k < half) {
-      const int one = interleaved ? 2 * k : k, two = interleaved ? one + 1 : k + half;
-      const float* const c = turns.c + row * 2 * half;
-      const float* const s = turns.n + row * 2 * half;
-      const float x = __bfloat162float(from[one]), y = __bfloat162float(from[two]);
-      to[one] = __float2bfloat16_rn(fmaf(y, s[one], x * c[one]));
-      to[two] = __float2bfloat16_rn(fmaf(x, s[two], y * c[two]));
-    } else {
-      to[k + half] = from[k + half];
+  const int dim = p.spec.dim, half = dim / 2, runs = p.head_dim / 8;
+  // heads of all rows of the CTA, a contiguous part of them for each blockIdx.y
+  const int all = n * p.heads, part = (all + int(gridDim.y) - 1) / int(gridDim.y);
+  const int begin = min(all, int(blockIdx.y) * part), end = min(all, begin + part);
+  const int tile = kStaged / p.head_dim;
+  for (int g0 = begin; g0 < end; g0 += tile) {
+    const int count = min(tile, end - g0) * runs;
+    for (int i = threadIdx.x; i < count; i += kStagedThreads) {
+      const int h = by_runs(i), g = g0 + h, row = by_heads(g);
+      reinterpret_cast<uint4*>(staged)[i] = *reinterpret_cast<const uint4*>(
+          p.X + (r0 + row) * p.x_stride + int64_t(g - row * p.heads) * p.head_dim +
+          8 * (i - h * runs));
     }
+    if (g0 == begin) make_turns(p, interleaved, r0, n, turns);  // synchronizes
+    else __syncthreads();
+    for (int i = threadIdx.x; i < count; i += kStagedThreads) {
+      const int h = by_runs(i), g = g0 + h, row = by_heads(g), e0 = 8 * (i - h * runs);
+      if (e0 >= dim && !p.copy) continue;
+      const __nv_bfloat16* const head = staged + h * p.head_dim;
+      const uint4 raw = reinterpret_cast<const uint4*>(staged)[i];
+      uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int e = e0 + 2 * k;  // dim is even: a word turns or stays as a whole
+        if (e >= dim) break;
+        const float2 x = kv4::bf16x2_to_float2(w[k]);
+        const float2 c = *reinterpret_cast<const float2*>(turns.c + row * dim + e);
+        const float2 s = *reinterpret_cast<const float2*>(turns.n + row * dim + e);
+        float2 z = make_float2(x.y, x.x);
+        if (!interleaved)
+          z = make_float2(__bfloat162float(head[e < half ? e + half : e - half]),
+                          __bfloat162float(head[e + 1 < half ? e + 1 + half : e + 1 - half]));
+        const float2 y = fma2(z, s, mul2(x, c));
+        w[k] = pack_bf162(y.x, y.y);
+      }
+      *reinterpret_cast<uint4*>(p.Y + (r0 + row) * p.y_stride +
+                                int64_t(g - row * p.heads) * p.head_dim + e0) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncthreads();  // read before the next heads come
   }
 }
 
