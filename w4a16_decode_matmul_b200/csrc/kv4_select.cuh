@@ -47,8 +47,8 @@ struct BoundsParams {
 // row_starts[b] / page + 2 b on: rows that begin inside a page touch at most
 // rows / page + 2 pages.
 //
-// Bound by the chain length -> page -> codes; 4.6 KB read a page of 64 and head of
-// 128, all of a thread's loads in flight at once.
+// Bound by the chain length -> page -> codes, 2 us for one page or 128; 4.6 KB read a page
+// of 64 and head of 128, all of a thread's loads in flight at once.
 template <int D, int G>
 __global__ void __launch_bounds__(kBoundThreads) bounds_kernel(const BoundsParams p) {
   constexpr int NC = D / 32, NG = D / G, kWords = D / 8;  // words of a row
@@ -215,8 +215,11 @@ struct SelectControl {
 // since it stops when the pages of a bin are all chosen -- and writes the chosen pages in
 // the order of their tokens.
 //
-// With histograms of all CTAs added through distributed shared memory in four passes of 8
-// bits it was 20,800 cycles for 2,048 pages, half of them the cluster's barriers.
+// Bound by latency: 2,048 pages of one sequence and head (532 KB) in 8 us on 8 CTAs, of
+// which look-ups of the sequence 1.2, queries 0.5, scores 2.1, the keys' range 0.5, two
+// passes 1.2, pages 1.5; 128 lists of about 650 pages (21 MB) 11.6 us.  With histograms of all
+// CTAs added through distributed shared memory in four passes of 8 bits it was 20,800
+// cycles for the one sequence, half of them the cluster's barriers.
 template <int D>
 __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectParams p) {
   constexpr int LPP = D / 16, PPW = 32 / LPP, kUnroll = 2;

