@@ -116,7 +116,8 @@ SHAPES = [  # rows of the sequences, vocabulary, padding of a row
     ([1], 1, 0), ([2], 2, 0), ([5], 32000, 0), ([1, 4, 0, 7, 2, 1], 1003, 0), ([6] * 9, 8191, 0),
     ([3, 5], 8193, 5), ([4, 1, 6], 50021, 0), ([2, 3], 131072, 16), ([20], 300, 0),
     ([3] * 70, 777, 2), ([2], 600_001, 0), ([4] * 30, 50021, 0), ([3, 1, 0, 5, 2] * 8, 8193, 3),
-    ([2] * 24, 131072, 0), ([35, 70, 33, 34], 200, 0),
+    ([2] * 24, 131072, 0), ([35, 70, 33, 34], 200, 0), ([3] * 30, 40_960, 0), ([2, 2], 40_961, 0),
+    ([40], 60_000, 0),
 ]
 
 

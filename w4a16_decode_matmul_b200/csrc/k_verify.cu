@@ -50,7 +50,14 @@ cudaError_t launch(verify::Params p, cudaStream_t s, int sms) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  if (int64_t(p.seqs) * verify::kMaxCluster <= sms) {
+  // A cluster a sequence while all are on the GPU at once (two CTAs an SM) and a warp's share
+  // of the row is a step or two of its loop; else three kernels.  Measured on B200, rows of 6,
+  // cluster and three kernels, us of a captured call: 32,000 binary32 logits, 1 sequence
+  // 13.3 and 14.0, 18: 19.9 and 20.7, 32: 26.6 and 29.0, 48: 38.8 and 34.6; 50,021: 17.5 and
+  // 15.1, 32.0 and 28.0, 38.7 and 37.2; 131,072: 25.3 and 16.5, 51.1 and 43.1, 68.8 and 63.1,
+  // 64: 116 and 103.  (The cluster is two launches less on the host.)
+  constexpr int kClusterVocab = 40960;
+  if (p.vocab <= kClusterVocab && int64_t(p.seqs) * verify::kMaxCluster <= 2 * sms) {
     p.ctas = 1;
     while (p.ctas < verify::kMaxCluster && p.ctas * 4096 < p.vocab) p.ctas *= 2;
     return launch_one(verify::verify_kernel<T, LOGITS, 16>, p, int64_t(p.seqs) * p.ctas, 512,

@@ -28,12 +28,12 @@
 // A share with an element that is nearer goes over its rows a second time.
 //
 // Kernels.  Logits first go through stats_kernel: largest logit and sum of exponentials
-// of every piece of every row, which reads each row once.  Then, for a few sequences,
-// verify_kernel, a cluster per sequence: it accepts, each warp sums its share of the
-// masses, and the warp in whose share the number falls looks for the token.  For many
-// sequences the same in three kernels (decide, share, find): what is to be summed
-// differs by a factor of five from one sequence to the next, and clusters left the SMs
-// idle for a third of their time.  Probabilities need no statistics.
+// of every piece of every row, which reads each row once.  Then, for few sequences of few
+// tokens, verify_kernel, a cluster per sequence: it accepts, each warp sums its share of
+// the masses, and the warp in whose share the number falls looks for the token.  Else the
+// same in three kernels (decide, share, find): what is to be summed differs by a factor of
+// five from one sequence to the next, and clusters left the SMs idle for a third of their
+// time.  Probabilities need no statistics.
 //
 // Measured on B200, 64 sequences of 6 rows of 131,072 binary32 logits, drafts too (369 MB):
 // statistics 62 us (5.9 TB/s, HBM bound), decisions 4, shares 28 (binary64 exponentials of
@@ -839,7 +839,7 @@ __device__ __forceinline__ float heat(const Params& p, bool logits, int b) {
   return logits && p.temperature != nullptr ? p.temperature[b] : 1.f;
 }
 
-// ---- few sequences: one a cluster -----------------------------------------------
+// ---- few sequences of few tokens: one a cluster -----------------------------------------------
 
 // What an exchange leaves: the sums of this CTA's warps, and of the cluster's CTAs.
 struct Sums {
@@ -939,7 +939,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) verify_kernel(const Pa
   });
 }
 
-// ---- many sequences: three kernels ------------------------------------------------
+// ---- the others: three kernels ------------------------------------------------
 
 template <typename T, bool LOGITS>
 __global__ void __launch_bounds__(kDecideWarps * 32) decide_kernel(const Params p) {
