@@ -255,6 +255,29 @@ def test_write_rotary_keys_of_every_size():
     assert_cache(cache, want)
 
 
+@pytest.mark.parametrize("rows", [1184, 1185, 2370, 2371, 4801])
+@pytest.mark.parametrize("q_heads", [0, 1])
+@pytest.mark.parametrize("d", [64, 128])
+def test_write_rotary_of_many_rows_with_few_heads(rows, q_heads, d):
+    """Several rows a CTA, the last CTA with fewer: fewer shares of work than warps."""
+    page = 64
+    lens, t = [rows - 300, 400], [rows - 300, 300]
+    table, pages = ref.random_batch(7, lens, page)
+    qkv = ref.keys(5, rows, q_heads + 2, d).cuda()
+    rot = wq().Rotary(wq().rotary_frequencies(d).cuda())
+    cache = new_cache(pages, 1, d, page, 64)
+    want = images(cache)
+    held, _ = ref.places(lens, t, table, page)
+    positions = [m - n + i for m, n in zip(lens, t) for i in range(n)]
+    expect(qkv[:, q_heads:-1], positions, rot, held, qkv[:, -1:], want, cache)
+    got = wq().kv4_write_rotary(qkv[:, :q_heads] if q_heads else None, qkv[:, q_heads:-1],
+                                qkv[:, -1:], cache, rot, ints(lens), ints(table),
+                                ints(starts_of(t)))
+    assert_cache(cache, want)
+    if q_heads:
+        check(got, qkv[:, :q_heads], positions, rot.freqs.cpu(), False)
+
+
 def test_write_rotary_matches_a_write_of_unturned_keys_at_position_zero():
     n, heads, d = 5, 4, 64
     k, v = ref.keys(1, n, heads, d).cuda(), ref.keys(2, n, heads, d).cuda()
