@@ -355,7 +355,13 @@ __device__ __forceinline__ uint4 ldg_stream128(const void* p) {
   return v;
 }
 
-// ---- two binary32 at once --------------------------------------------------
+// ---- two values at once ------------------------------------------------------
+
+__device__ __forceinline__ uint32_t bmax2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;

@@ -334,16 +334,46 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const Params p) {
                                 : static_cast<const T*>(p.target) + int64_t(r) * p.target_stride;
   const int begin = piece * p.piece - row_lead(row);
   const int end = min(begin + p.piece, p.vocab);
-  auto load = [&](int tile, float (&x)[kRuns][N]) {
+  // the elements stay in the registers as they are stored: half as many for bfloat16
+  constexpr uint32_t kNothing = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -inf
+  auto load = [&](int tile, uint32_t (&w)[kRuns][4]) {
     if (tile >= 0 && tile <= end - kTile) {
 #pragma unroll
-      for (int k = 0; k < kRuns; ++k)
-        load_16<T, N>(row + tile + (k * kThreads + tid) * N, x[k]);
+      for (int k = 0; k < kRuns; ++k) {
+        const uint4 v =
+            __ldg(reinterpret_cast<const uint4*>(row + tile + (k * kThreads + tid) * N));
+        w[k][0] = v.x, w[k][1] = v.y, w[k][2] = v.z, w[k][3] = v.w;
+      }
     } else {
 #pragma unroll
-      for (int k = 0; k < kRuns; ++k)
-        load_run<T, N>(row, tile + (k * kThreads + tid) * N, end, 0, -INFINITY, x[k]);
+      for (int k = 0; k < kRuns; ++k) {
+        const int at = tile + (k * kThreads + tid) * N;
+        if (at >= 0 && at <= end - N) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + at));
+          w[k][0] = v.x, w[k][1] = v.y, w[k][2] = v.z, w[k][3] = v.w;
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (sizeof(T) == 4) {
+            w[k][i] = at + i >= 0 && at + i < end ? __float_as_uint(row[at + i]) : kNothing;
+          } else {
+            const int e = at + 2 * i;
+            const uint32_t one = e >= 0 && e < end ? __bfloat16_as_ushort(row[e]) : kNothing & 0xffffu;
+            const uint32_t two =
+                e + 1 >= 0 && e + 1 < end ? __bfloat16_as_ushort(row[e + 1]) : kNothing >> 16;
+            w[k][i] = one | (two << 16);
+          }
+        }
+      }
     }
+  };
+  // element pair j of a run: (2j, 2j + 1)
+  auto pair_of = [](const uint32_t (&w)[4], int j) -> float2 {
+    if constexpr (sizeof(T) == 4)
+      return make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+    else
+      return make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
   };
   // log2(e) / temperature in two parts: a binary32 product would be off by 2^-24 of the
   // exponent, for all terms in the same direction
@@ -354,22 +384,35 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const Params p) {
   float top = -INFINITY;
   int first = 0x7fffffff;
   for (int tile = begin; tile < end; tile += kTile) {
-    float x[kRuns][N];
-    load(tile, x);
+    uint32_t w[kRuns][4];
+    load(tile, w);
     grid_dependents_launch();
     float high = -INFINITY;
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int k = 0; k < kRuns; ++k)
+      for (int k = 0; k < kRuns; ++k)
 #pragma unroll
-      for (int i = 0; i < N; ++i) high = fmaxf(high, x[k][i]);
+        for (int i = 0; i < 4; ++i) high = fmaxf(high, __uint_as_float(w[k][i]));
+    } else {
+      uint32_t most = kNothing;
+#pragma unroll
+      for (int k = 0; k < kRuns; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) most = bmax2(most, w[k][i]);
+      high = fmaxf(__uint_as_float(most << 16), __uint_as_float(most & 0xffff0000u));
+    }
     if (greedy) {
       if (high > top) {
         top = high;
 #pragma unroll
         for (int k = kRuns - 1; k >= 0; --k)
 #pragma unroll
-          for (int i = N - 1; i >= 0; --i)
-            if (x[k][i] == high) first = tile + (k * kThreads + tid) * N + i;
+          for (int j = N / 2 - 1; j >= 0; --j) {
+            const float2 x = pair_of(w[k], j);
+            const int at = tile + (k * kThreads + tid) * N + 2 * j;
+            if (x.y == high) first = at + 1;
+            if (x.x == high) first = at;
+          }
       }
       continue;
     }
@@ -384,20 +427,22 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const Params p) {
 #pragma unroll
       for (int k = 0; k < kRuns; ++k)
 #pragma unroll
-        for (int i = 0; i < N; ++i) part[0].x += x[k][i] == INFINITY ? 1.f : 0.f;
+        for (int j = 0; j < N / 2; ++j) {
+          const float2 x = pair_of(w[k], j);
+          part[0].x += (x.x == INFINITY ? 1.f : 0.f) + (x.y == INFINITY ? 1.f : 0.f);
+        }
     } else {
       const float2 below = make_float2(-top, -top), u = make_float2(unit, unit);
       const float2 u_low = make_float2(unit_low, unit_low);
 #pragma unroll
       for (int k = 0; k < kRuns; ++k)
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
+        for (int j = 0; j < N / 2; ++j) {
           // -inf and NaN end up at the lowest, whose exponential is 0
-          float2 d = add2(make_float2(x[k][i], x[k][i + 1]), below);
+          float2 d = add2(pair_of(w[k], j), below);
           d = make_float2(fmaxf(d.x, lowest), fmaxf(d.y, lowest));
           const float2 t = fma2(d, u, mul2(d, u_low));
-          part[i / 2 & 1] =
-              add2(part[i / 2 & 1], make_float2(exp2_approx(t.x), exp2_approx(t.y)));
+          part[j & 1] = add2(part[j & 1], make_float2(exp2_approx(t.x), exp2_approx(t.y)));
         }
     }
     part[0] = add2(part[0], part[1]);
