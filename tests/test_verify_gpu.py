@@ -276,6 +276,21 @@ def test_drafts_close_to_the_target(seqs, dtype, changed):
     assert got == want
 
 
+@pytest.mark.parametrize("seqs", [2, 40])
+@pytest.mark.parametrize("vocab", [1000, 8193, 50_001])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_refused_drafts_of_equal_logits(seqs, vocab, dtype):
+    """p = q in every bit: nothing is left of the difference, so p itself is sampled.  The
+    drafts are refused since they are outside the vocabulary, or have no mass."""
+    rows = [2] * seqs
+    target, _, tokens, uniform = make(23, rows, vocab, dtype)
+    target[0::4, 5] = float("-inf")
+    draft = target.roll(1, 0)
+    tokens[1::4], tokens[3::4] = 5, vocab
+    got, want = run(target, tokens, uniform, draft, rows)
+    assert got == want and got[1] == [0] * seqs
+
+
 @pytest.mark.parametrize("hot", [1e-3, 30.0, float("inf")])
 def test_temperatures_far_from_one(hot):
     rows = [3, 1, 4]

@@ -674,7 +674,9 @@ struct Masses {
       m[k] = p(x[k]);
       if (whole) continue;
       if (MODE == kWithoutOne && i0 + rows.lane * N + k == one) m[k] = 0.0;
-      if (MODE == kDifference) m[k] = fmax(fma(m[k], of_p, -(of_q * q(y[k]))), 0.0);
+      // (products rounded alike: of equal rows nothing is left)
+      if (MODE == kDifference)
+        m[k] = fmax(__dsub_rn(__dmul_rn(m[k], of_p), __dmul_rn(of_q, q(y[k]))), 0.0);
     }
   }
 
