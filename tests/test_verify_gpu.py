@@ -291,6 +291,26 @@ def test_refused_drafts_of_equal_logits(seqs, vocab, dtype):
     assert got == want and got[1] == [0] * seqs
 
 
+@pytest.mark.parametrize("seqs", [2, 40])
+@pytest.mark.parametrize("vocab", [1000, 50_001])
+@pytest.mark.parametrize("low", [-590.0, -598.0, -601.0, -646.0, -660.0, -689.0, -700.0])
+def test_what_is_left_is_next_to_nothing(seqs, vocab, low):
+    """p and q are alike but for logits far below the largest: those have the rest of the mass
+    where they are at most 600 below, else nothing is left, and p itself is sampled."""
+    rows = [2] * seqs
+    target = torch.full((2 * seqs, vocab), low, device="cuda")
+    target[:, 3] = 0.0
+    draft = torch.full_like(target, low - 5)
+    draft[:, 3], draft[:, 7] = 0.0, -580.0
+    tokens = ints([7] * (2 * seqs))                   # refused: p(7) is below q(7)
+    uniform = torch.rand(2 * seqs, generator=torch.Generator().manual_seed(3)).cuda()
+    uniform[1::2] = 0.99
+    got, want = run(target, tokens, uniform, draft, rows)
+    if low < -600:
+        want[0] = [3, -1] * seqs
+    assert got == want
+
+
 @pytest.mark.parametrize("hot", [1e-3, 30.0, float("inf")])
 def test_temperatures_far_from_one(hot):
     rows = [3, 1, 4]

@@ -132,15 +132,18 @@ __device__ __forceinline__ Rows load_rows(const Params& p, int b) {
 // r^3) a warp's look-up took six or seven cycles and was what bounded the sums.
 constexpr int kTable = 64, kCopies = 16;
 
-// Logits without mass come out as less than this, relative to the largest logit's mass of
-// 1: it is no mass (and adds nothing to a sum that has any).
-constexpr double kNoMass = 1e-280;
+// What is no mass, and adds nothing to a sum that has any: of 2^30 logits below the cut,
+// which come out as less than 2^-1022 each, the sum is still less.  Every other mass, every
+// difference of two (of 53 bits, the whole row's mass at most 2^30 of the largest's) and
+// every sum of them is more: e^-600 2^-30 2^-53 = 3e-286.
+constexpr double kNoMass = 1e-290;
+constexpr float kCut = 600.f;  // of the largest logit's mass, in e^-1
 
 struct Exp {
   const double* table;  // 2^(j/64), this lane's copy: kCopies apart
   double scale;         // 64 log2(e) / temperature
   double top;           // the largest logit
-  float cut;            // logits below it (e^-690 of the largest's mass) and NaN have no mass
+  float cut;            // logits below it (e^-kCut of the largest's mass) and NaN have no mass
   __device__ __forceinline__ double operator()(float x) const {
     const double d = double(x) - top;
     const double magic = 6755399441055744.0;  // 1.5 * 2^52: rounds to an integer, the low word
@@ -164,7 +167,7 @@ __device__ __forceinline__ double exp_scale(float hot) {
 }
 
 __device__ __forceinline__ Exp make_exp(const double* table, double scale, float top, float hot) {
-  return {table, scale, double(top), fmaxf(__fsub_ru(top, 690.f * hot), -3.4028234e38f)};
+  return {table, scale, double(top), fmaxf(__fsub_ru(top, kCut * hot), -3.4028234e38f)};
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -1134,10 +1137,10 @@ __global__ void __launch_bounds__(kFindWarps * 32, 2) find_kernel(const Params p
           }
           const unsigned past = __ballot_sync(0xffffffffu, incl > wanted && own > kNoMass);
           const unsigned held = __ballot_sync(0xffffffffu, own > kNoMass);
-          if (lane == (past ? __ffs(past) - 1 : 31 - __clz(held))) {
+          if (lane == (past ? __ffs(past) - 1 : held ? 31 - __clz(held) : 0)) {
             double before = incl - own;
             const int n = min(kEach, p.n_shares - lane * kEach);
-            chosen = lane * kEach + owner_of(masses + lane * kEach, n, wanted, before);
+            chosen = max(0, lane * kEach + owner_of(masses + lane * kEach, n, wanted, before));
             ends[0] = before;
           }
         }
