@@ -343,6 +343,27 @@ def test_lengths_in_place_and_own_workspace():
     assert lens.tolist() == [50 + 10 * b - 3 + a for b, a in enumerate(accepted.tolist())]
 
 
+@pytest.mark.parametrize("seqs", [3, 40])
+@pytest.mark.parametrize("logits", [True, False])
+def test_sequences_without_rows_alone(seqs, logits):
+    """A padded batch of which no sequence has rows: what follows on the stream finds the call
+    finished."""
+    target, draft, tokens, uniform = make(15, [1] * 8, 3000, torch.float32)
+    ws, starts = wq().verify_workspace(8), ints([0] * (seqs + 1))
+    for i in range(20):
+        lens = torch.arange(i, i + seqs, dtype=torch.int32, device="cuda")
+        out = tuple(torch.full((n,), 77, dtype=torch.int32, device="cuda")
+                    for n in (8, seqs, seqs))
+        wq().verify_drafts(target, tokens, uniform, draft, row_starts=starts, logits=logits,
+                           seq_lens=lens, out=out, workspace=ws)
+        copies = [x.clone() for x in out]
+        for x in out:
+            x.fill_(5)
+        assert copies[0].eq(77).all() and copies[1].eq(0).all() and copies[2].equal(lens)
+        assert all(x.eq(5).all() for x in out)
+    assert wq().get_device_error() == 0
+
+
 def test_bad_row_starts_are_recorded():
     rows = [2, 2, 2]
     target, draft, tokens, uniform = make(14, rows, 600, torch.float32)

@@ -942,6 +942,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) verify_kernel(const Pa
   if (rows.count == 0) {
     if (rank == 0 && tid == 0) no_rows(p, b);
     if (p.ctas > 1) cluster_wait();
+    if (LOGITS) grid_dependency_wait();  // no grid is over before the one it depends on
     return;
   }
   const float hot = heat(p, LOGITS, b);
@@ -1000,6 +1001,7 @@ __global__ void __launch_bounds__(kDecideWarps * 32) decide_kernel(const Params 
   const Rows rows = load_rows(p, b);
   if (rows.count == 0) {
     if (tid == 0) no_rows(p, b);
+    if (LOGITS) grid_dependency_wait();  // no grid is over before the one it depends on
     return;
   }
   const float hot = heat(p, LOGITS, b);
@@ -1024,10 +1026,10 @@ __global__ void __launch_bounds__(kShareWarps * 32, 6) share_kernel(const Params
   grid_dependents_launch();
   const Rows rows = load_rows(p, b);
   const float hot = heat(p, LOGITS, b);
-  if (rows.count == 0) return;
   if (LOGITS) fill_table(table_s);
   __syncthreads();
   grid_dependency_wait();
+  if (rows.count == 0) return;
   const Decision d = p.decisions[rows.first];
   if (d.mode == kDone || i >= p.n_shares) return;
   with_masses<T, LOGITS>(p, d, hot, exp_scale(hot), table_s + (lane & (kCopies - 1)), lane,
@@ -1062,7 +1064,10 @@ __global__ void __launch_bounds__(kFindWarps * 32, 2) find_kernel(const Params p
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = int(blockIdx.x);
   const Rows rows = load_rows(p, b);
   const float hot = heat(p, LOGITS, b);
-  if (rows.count == 0) return;
+  if (rows.count == 0) {
+    grid_dependency_wait();
+    return;
+  }
   const double number = uniform_of(p.uniform[rows.first]);
   if (LOGITS) fill_table(table_s);
   if (tid == 0) near_count = 0;
