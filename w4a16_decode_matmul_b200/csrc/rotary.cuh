@@ -459,14 +459,10 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 4)
   };
   // keys and values of all rows first: they are several times the work of queries
   const int kv_work = n * p.chunks, query_shares = shares - p.chunks;
-  for (int work = warp; work == warp || work < n * shares; work += warps) {
-    // (the last CTA can have fewer shares than warps, all of which make the angles: the
-    // others take queries behind the last)
-    const bool is_kv = work < kv_work, none = work >= n * shares;
-    const int row = is_kv ? work / p.chunks : none ? 0 : (work - kv_work) / query_shares;
-    const int item = is_kv  ? work - row * p.chunks
-                     : none ? query_shares
-                            : work - kv_work - row * query_shares;
+  for (int work = warp; work < n * shares; work += warps) {
+    const bool is_kv = work < kv_work;
+    const int row = is_kv ? work / p.chunks : (work - kv_work) / query_shares;
+    const int item = is_kv ? work - row * p.chunks : work - kv_work - row * query_shares;
     const int r = r0 + row;
     const SplitTurns<D>& t = turns[row];
     if (!is_kv) {
@@ -554,6 +550,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 4)
       }
     }
   }
+  prepare();  // (the last CTA can have fewer shares than warps, all of which make the angles)
 }
 
 }  // namespace rotary
