@@ -413,7 +413,8 @@ struct RowPlace {
 // Measured on B200 (15,609 rows, 32 + 2 * 8 heads of 128, half of each turned, 330 MB): 86
 // us, 3.8 TB/s, 3,400 warp instructions a row (issue 60 %, ALU 48 %), of which the
 // quantizer has a third.  With the queries in a launch of their own 54 + 51 us; a row a CTA
-// 102; keys and values last, or always in the same warps, 92 to 99.
+// 102; keys and values last, or always in the same warps, 92 to 99; three CTAs an SM, which
+// spill nothing, 94.
 template <int D, int G, bool INTERLEAVED>
 __global__ void __launch_bounds__(kWriteWarps * 32, 4)
     write_rotary_kernel(const WriteParams p, int shares) {

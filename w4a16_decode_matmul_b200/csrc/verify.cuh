@@ -38,7 +38,7 @@
 // Measured on B200, 64 sequences of 6 rows of 131,072 binary32 logits, drafts too (369 MB):
 // statistics 62 us (5.9 TB/s, HBM bound), decisions 4, shares 28 (binary64 exponentials of
 // 35 instructions each), tokens 4 to 8: 102 us in all.  With binary64 exponentials in the
-// statistics 288; clusters for all 126.  32 ragged sequences of 50,021 bfloat16 logits 29 us,
+// statistics 288; clusters for all 126.  32 ragged sequences of 50,021 bfloat16 logits 28 us,
 // of which none reaches a quarter of its kernel's rate: four short chains of look-ups.
 // One sequence of 5 rows of 32,000 probabilities 7 us.
 #pragma once
