@@ -554,14 +554,15 @@ typedef struct wq_verification {
 size_t wq_verify_workspace_bytes(int64_t rows);
 
 /* Masses that a token is sampled from and their sums are binary64 (exponentials within
- * 2^-43): the token is that of exact arithmetic unless uniform_0 is within 10^-12 of a
- * border.  A draft's p and q are those of probabilities exactly; of logits their
- * sums of exponentials are good to 4 10^-7.  Probabilities need not sum to 1; negative
- * ones and NaN count as 0, NaN logits as -infinity; a logit more than 600 temperatures
- * below its row's largest has no mass; of logits of +infinity each has the same mass; a row
- * without any mass gives the token -1.  A sequence without rows gets accepted 0; rows behind the last
- * sequence are left as they were.  Two sequences' rows may not overlap.  Outputs may
- * not overlap inputs, but out_lens may be seq_lens.
+ * 2^-43): the token is that of exact arithmetic unless uniform_0 times the whole is within
+ * 10^-12 of a border, in units of the distributions (where p and q are nearly alike the
+ * whole of max(p - q, 0) is far below 1).  A draft's p and q are those of probabilities
+ * exactly; of logits their sums of exponentials are good to 4 10^-7.  Probabilities need
+ * not sum to 1; negative ones and NaN count as 0, NaN logits as -infinity; a logit more than
+ * 600 temperatures below its row's largest has no mass; of logits of +infinity each has the
+ * same mass; a row without any mass gives the token -1.  A sequence without rows gets
+ * accepted 0; rows behind the last sequence are left as they were.  Two sequences' rows may
+ * not overlap.  Outputs may not overlap inputs, but out_lens may be seq_lens.
  *
  * Pointers 16-byte aligned, temperature, seq_lens, row_starts, tokens, uniform and
  * the outputs 4-byte.  Errors: WQ_ERR_INVALID_ARG for a size, pointer or flag outside
