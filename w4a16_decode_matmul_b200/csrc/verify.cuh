@@ -46,6 +46,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "verify_jobs.h"
 
 namespace wq {
 namespace verify {
@@ -808,28 +809,27 @@ __device__ __forceinline__ Decision decide(const Params& p, DecideShared& s, int
     const int n = min(drafts - base, kBlock);
     const double mine = tid < n ? uniform_of(p.uniform[rows.first + base + tid + 1]) : 0.0;
     // a job: its row, the token in question and that token's element
-    int r, token;
+    const int jobs = jobs_of(n);
+    Job at;
+    int token;
     bool known, one;
     float x;
     auto fetch = [&](int job) {
-      const bool is_draft = job > n;
-      const int i = base + (is_draft ? job - (n + 1) : job), token_row = is_draft ? i : i + 1;
-      r = rows.first + i;
-      token = token_row <= drafts ? p.tokens[rows.first + token_row] : -1;
+      at = job_of(job, n, base);
+      const int r = rows.first + at.row;
+      token = at.token_row <= drafts ? p.tokens[rows.first + at.token_row] : -1;
       known = token >= 0 && token < p.vocab;
-      one = is_draft && (p.draft == nullptr || !(hot > 0.f));
+      one = at.is_draft && (p.draft == nullptr || !(hot > 0.f));
       x = 0.f;
       if (known && !one)
-        x = to_float(is_draft
+        x = to_float(at.is_draft
                          ? static_cast<const T*>(p.draft)[int64_t(r) * p.draft_stride + token]
                          : static_cast<const T*>(p.target)[int64_t(r) * p.target_stride + token]);
     };
-    if (warp < 2 * (n + 1)) fetch(warp);
+    if (warp < jobs) fetch(warp);
     if (base == 0) wait();
-    for (int job = warp; job < 2 * (n + 1); job += WARPS) {
-      const bool is_draft = job > n;
+    for (int job = warp; job < jobs; job += WARPS) {
       if (job != warp) fetch(job);
-      if (job == n + 1) continue;  // the draft row of a token that stands
       RowStat stat;
       if (one) {
         // a draft without a distribution; greedy: whatever it is, the token is accepted if
@@ -838,10 +838,11 @@ __device__ __forceinline__ Decision decide(const Params& p, DecideShared& s, int
       } else if (!LOGITS) {
         stat = {1.0, known && x > 0.f ? double(x) : 0.0, 0.f, -1, kProbabilities};
       } else {
-        stat = join_pieces(p, (is_draft ? p.rows : 0) + r, hot, scale, table, x, token, lane);
+        const int r = rows.first + at.row;
+        stat = join_pieces(p, (at.is_draft ? p.rows : 0) + r, hot, scale, table, x, token, lane);
         if (!known) stat.of_token = 0.0;
       }
-      if (lane == 0) s.stats[is_draft][is_draft ? job - (n + 1) : job] = stat;
+      if (lane == 0) s.stats[at.is_draft][at.row - base] = stat;
     }
     __syncthreads();
     if (tid < n) {
