@@ -237,11 +237,15 @@ __device__ __forceinline__ uint32_t num_clusters_x() {
   return r;
 }
 
+// (aligned: all lanes of a warp execute these together, also behind code that they took
+// different ways through)
 __device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
