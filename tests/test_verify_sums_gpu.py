@@ -1,0 +1,45 @@
+"""Verification of drafts where every error of a row's sum of exponentials has the same
+sign: rows of two levels, whose many low logits all round alike."""
+import pytest
+import torch
+
+from tests.test_kv4_gpu import ints
+from tests.test_verify_gpu import run
+
+pytestmark = pytest.mark.gpu
+
+HIGH = 8.660868644714355
+LOW = (0.31713345646858215, 0.3171333372592926)  # neighbouring numbers of 32 bits: two steps apart
+
+
+def levels(n, vocab, low, stride=4096):
+    x = torch.full((n, vocab), low, device="cuda")
+    x[:, ::stride] = HIGH
+    return x
+
+
+@pytest.mark.parametrize("seqs,vocab", [(2, 32_768), (40, 32_768), (2, 131_072), (40, 131_072)])
+@pytest.mark.parametrize("swapped", [False, True])
+@pytest.mark.parametrize("stride", [512, 4096])
+def test_what_is_left_of_two_levels_that_differ_by_a_rounding(seqs, vocab, swapped, stride):
+    """A refused draft (outside the vocabulary) leaves max(p - q, 0), which lies on the low
+    tokens or on the high ones, by the true sums: p and q of the low ones differ by about
+    6 10^-8 of themselves."""
+    low = LOW[::-1] if swapped else LOW
+    rows = [2] * seqs
+    target, draft = levels(2 * seqs, vocab, low[0], stride), levels(2 * seqs, vocab, low[1], stride)
+    tokens = ints([vocab] * (2 * seqs))
+    # (numbers that end inside a token's mass)
+    uniform = torch.tensor([(i + 0.5) / (2 * seqs) for i in range(2 * seqs)], device="cuda")
+    uniform[0] = 0.2
+    got, want = run(target, tokens, uniform, draft, rows)
+    assert got[1:] == want[1:] and got[1] == [0] * seqs
+    high = [x % stride == 0 for x in got[0][::2]]
+    assert high == [x % stride == 0 for x in want[0][::2]]
+    # what is left is the same for each token of a level, so a number that falls inside a
+    # token's share gives that token.  The high ones are 2^k: numbers (i + 1/2) / n can fall on
+    # a border between two of them, where either is right.  The low ones: one further for the
+    # roundings of their running sum, one for a token without a share between.
+    for g, w, u, h in zip(got[0][::2], want[0][::2], uniform[::2].tolist(), high):
+        on_border = (u * (vocab // stride)).is_integer()
+        assert abs(g - w) <= (stride * on_border if h else 2)

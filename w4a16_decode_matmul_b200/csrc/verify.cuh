@@ -19,13 +19,15 @@
 // within 2^-43.  A draft's acceptance has one border: there the sums of exponentials
 // are binary32's, added in binary64 from 32 terms on, off by some 10^-7.
 //
-// max(p - q, 0) with one pass over the two rows.  stats_kernel's sums give p and q within
-// 4 10^-7, which is enough to tell where p > q wherever they differ by more than 2^-20 of
-// q.  So one pass forms the rows' sums Zp and Zq in binary64, and of the elements with
-// p > q the sum D of the differences and the sum P of the p, all by the approximate sums
-// Zp' = Zp / (1 + a), Zq' = Zq / (1 + b) (P binary64 too, though 10^-7 of it counts);
-// what is left is then D (1 + b) + (a - b) P with a and b for the factors 1/Zp and 1/Zq.
-// A share with an element that is nearer goes over its rows a second time.
+// max(p - q, 0) with one pass over the two rows.  One pass forms the rows' sums Zp and Zq in
+// binary64, and of the elements with p > q the sum D of the differences and the sum P of
+// the p, all by stats_kernel's approximate sums: factors 1/Zp' and 1/Zq' for 1/Zp =
+// (1 + a)/Zp' and 1/Zq = (1 + b)/Zq' (P binary64 too, though 10^-7 of it counts); what is
+// left is then D (1 + b) + (a - b) P.  An element's p - q is (1 + a)(p' - q') + (a - b) q', of
+// the sign of p' - q' where that is more than 2^-20 of q' and |a - b| is less; so a share with
+// an element that is nearer goes over its rows a second time, and where the exact sums say that
+// a and b are 2^-21 or more apart, all shares do (rounding errors of one sign throughout a row
+// only: for random logits a and b are some 3 10^-8).
 //
 // Kernels.  Logits first go through stats_kernel: largest logit and sum of exponentials
 // of every piece of every row, which reads each row once.  Then, for few sequences of few
@@ -696,13 +698,23 @@ struct Masses {
     return warp_sum(s);
   }
 
-  // The mass of a share.
-  __device__ __forceinline__ double finish(const Share& s, int begin, int end, double of_p,
-                                           double of_q) const {
+  // What the factors are above those by which the shares were formed, of themselves.
+  __device__ __forceinline__ double above_p(double of_p) const {
+    return (of_p - inverse_p) / inverse_p;
+  }
+  __device__ __forceinline__ double above_q(double of_q) const {
+    return inverse_q > 0.0 ? (of_q - inverse_q) / inverse_q : 0.0;
+  }
+
+  // Whether a share was formed by factors too far from the rows' to tell where p > q.
+  __device__ __forceinline__ bool unsure(const Share& s, double of_p, double of_q) const {
+    return kTwoSums && (s.near || fabs(above_p(of_p) - above_q(of_q)) >= 0x1p-21);
+  }
+
+  // The mass of any other share.
+  __device__ __forceinline__ double finish(const Share& s, double of_p, double of_q) const {
     if (!kTwoSums) return s.d;
-    if (s.near) return sum(begin, end, false, of_p, of_q);
-    const double a = (of_p - inverse_p) / inverse_p;
-    const double b = inverse_q > 0.0 ? (of_q - inverse_q) / inverse_q : 0.0;
+    const double a = above_p(of_p), b = above_q(of_q);
     return fmax(fma(s.d, b, s.d) + (a - b) * (inverse_p * s.p), 0.0);
   }
 
@@ -967,7 +979,9 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) verify_kernel(const Pa
     double of_p, of_q, z[2] = {share.zp, share.zq};
     if (M::kTwoSums) exchange<WARPS, 2>(sums, {share.zp, share.zq}, z, p.ctas, rank);
     m.factors(z[0], z[1], of_p, of_q);
-    double mass = m.finish(share, begin, end, of_p, of_q), total[1];
+    double total[1];
+    const double mass = m.unsure(share, of_p, of_q) ? m.sum(begin, end, false, of_p, of_q)
+                                                    : m.finish(share, of_p, of_q);
     exchange<WARPS, 1>(sums + 2, {mass}, total, p.ctas, rank);
     bool whole = false;
     Sums* of = sums + 2;
@@ -1100,20 +1114,26 @@ __global__ void __launch_bounds__(kFindWarps * 32, 2) find_kernel(const Params p
         }
         m.factors(zp, zq, of_p, of_q);
         if (tid < kShares) {
-          if (s.near) near[atomicAdd(&near_count, 1)] = tid;
-          s.near = 0;
-          masses[tid] = m.finish(s, 0, 0, of_p, of_q);
+          if (tid < p.n_shares && m.unsure(s, of_p, of_q)) near[atomicAdd(&near_count, 1)] = tid;
+          masses[tid] = m.finish(s, of_p, of_q);
         }
         __syncthreads();
-        for (int k = 0; k < near_count; ++k) {  // shares with elements too near to tell
-          int begin, end;
-          part(near[k], begin, end);
-          const int each = ((end - begin + M::R::kStep - 1) / M::R::kStep + kFindWarps - 1) /
-                           kFindWarps * M::R::kStep;
-          const int from = min(begin + warp * each, end), to = min(from + each, end);
+        // shares that have to be gone over again: a few, each by all warps, or a warp a share
+        const bool many = near_count >= kFindWarps;
+        for (int k0 = 0; k0 < near_count; k0 += many ? kFindWarps : 1) {
+          const int k = many ? k0 + warp : k0;
+          int begin = 0, end = 0;
+          if (k < near_count) part(near[k], begin, end);
+          const int steps = (end - begin + M::R::kStep - 1) / M::R::kStep;
+          const int each = (many ? steps : (steps + kFindWarps - 1) / kFindWarps) * M::R::kStep;
+          const int from = min(begin + (many ? 0 : warp * each), end), to = min(from + each, end);
           const double own = m.sum(from, to, false, of_p, of_q);
-          const double mass = block_sum<kFindWarps>(lane == 0 ? own : 0.0, scratch);
-          if (tid == 0) masses[near[k]] = mass;
+          if (many) {
+            if (lane == 0 && k < near_count) masses[near[k]] = own;
+          } else {
+            const double mass = block_sum<kFindWarps>(lane == 0 ? own : 0.0, scratch);
+            if (tid == 0) masses[near[k]] = mass;
+          }
         }
         __syncthreads();
         double total = block_sum<kFindWarps>(tid < p.n_shares ? masses[tid] : 0.0, scratch);
