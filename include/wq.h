@@ -557,7 +557,9 @@ size_t wq_verify_workspace_bytes(int64_t rows);
  * 2^-43): the token is that of exact arithmetic unless uniform_0 times the whole is within
  * 10^-12 of a border, in units of the distributions (where p and q are nearly alike the
  * whole of max(p - q, 0) is far below 1).  A draft's p and q are those of probabilities
- * exactly; of logits their sums of exponentials are good to 4 10^-7.  Probabilities need
+ * exactly; of logits their sums of exponentials are good to 1.3 10^-6 (some 3 10^-8 for logits
+ * that differ), and to 4 10^-7 more for every 2^18 tokens beyond the first: a draft whose u q is
+ * nearer to p than both sums' errors may be decided either way.  Probabilities need
  * not sum to 1; negative ones and NaN count as 0, NaN logits as -infinity; a logit more than
  * 600 temperatures below its row's largest has no mass; of logits of +infinity each has the
  * same mass; a row without any mass gives the token -1.  A sequence without rows gets

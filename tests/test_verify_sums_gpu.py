@@ -1,15 +1,19 @@
 """Verification of drafts where every error of a row's sum of exponentials has the same
 sign: rows of two levels, whose many low logits all round alike."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
+from tests.gpu_util import wq
 from tests.test_kv4_gpu import ints
 from tests.test_verify_gpu import run
 
 pytestmark = pytest.mark.gpu
 
 HIGH = 8.660868644714355
-LOW = (0.31713345646858215, 0.3171333372592926)  # neighbouring numbers of 32 bits: two steps apart
+LOW = (0.31713345646858215, 0.3171333372592926)  # four steps of 32 bits apart
 
 
 def levels(n, vocab, low, stride=4096):
@@ -43,3 +47,26 @@ def test_what_is_left_of_two_levels_that_differ_by_a_rounding(seqs, vocab, swapp
     for g, w, u, h in zip(got[0][::2], want[0][::2], uniform[::2].tolist(), high):
         on_border = (u * (vocab // stride)).is_integer()
         assert abs(g - w) <= (stride * on_border if h else 2)
+
+
+@pytest.mark.parametrize("seqs", [1, 40])
+@pytest.mark.parametrize("swapped", [False, True])
+def test_drafts_near_the_border_of_acceptance(seqs, swapped):
+    """u q = p but for 7 10^-7, on either side.  Threads whose logits are all alike sum ones,
+    exactly; what is left is one exponential between a thread's largest logit and the row's, off by
+    2^-22 and a rounding, 2^-24: 3 10^-7 for p, the same for q."""
+    vocab, x = 131_072, 1234
+    low = LOW[::-1] if swapped else LOW
+    rows = [2] * seqs
+    target, draft = levels(2 * seqs, vocab, low[0]), levels(2 * seqs, vocab, low[1])
+    draft[:, x] = low[1] + 0.5
+    p, q = (r.double().cpu() for r in (target[0], draft[1]))
+    ratio = math.exp(float(p[x] - torch.logsumexp(p, 0) - q[x] + torch.logsumexp(q, 0)))
+    for side in (-1, 1):
+        u = np.float32(ratio * (1 + side * 6.5e-7))
+        while abs(float(u) / ratio - 1) < 6e-7:
+            u = np.nextafter(u, np.float32(2 if side > 0 else 0))
+        uniform = torch.full((2 * seqs,), float(u), device="cuda")
+        tokens = ints([x] * (2 * seqs))
+        _, accepted, _ = wq().verify_drafts(target, tokens, uniform, draft, seqs=seqs, logits=True)
+        assert accepted.tolist() == [1 if side < 0 else 0] * seqs, side

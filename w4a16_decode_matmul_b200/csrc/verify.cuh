@@ -17,7 +17,13 @@
 // moves all boundaries of max(p - q, 0) at once and costs twenty times as much.  So the
 // sampled row's (and its draft row's) masses and sums are in binary64, exponentials
 // within 2^-43.  A draft's acceptance has one border: there the sums of exponentials
-// are binary32's, added in binary64 from 32 terms on, off by some 10^-7.
+// are binary32's, added in binary64 from 32 terms on.  For logits that round to either side
+// they are off by some 3 10^-8; where all errors have one sign by up to 21 of 2^-24 = 1.3 10^-6:
+// 4 for ex2's two units in the last place, 2 ln 2 t for the rounding of x - top and of the
+// exponent -t, of which the weighted mean is at most 2.7 among a thread's 32 elements, 9 for the
+// additions, 5 from a thread's largest logit to the CTA's.  From 2^18 tokens on a thread has
+// more than 32 elements, and each further tile costs 6.7 (4 10^-7) at most: 5 where it raises
+// the largest logit, and what t grows.
 //
 // max(p - q, 0) with one pass over the two rows.  One pass forms the rows' sums Zp and Zq in
 // binary64, and of the elements with p > q the sum D of the differences and the sum P of
@@ -177,6 +183,21 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// 2^((from - to) (unit + unit_low)), to >= from: what a sum of exponentials relative to one
+// logit is multiplied by to be relative to another.  All of a thread's elements share its
+// error, so the exponent is held in two parts (Knuth's two-sum, the product's own error): what
+// is left is ex2's 2^-22 and a rounding.  Where the exponent was one product, sums of two
+// levels 8.3 apart were off by 6 10^-7.  (32 ragged sequences: 29.2 us so, 29.6 now, 30.2 in
+// binary64.)
+__device__ __forceinline__ double rescale(float from, float to, float unit, float unit_low) {
+  const float d = from - to, back = d - from;
+  const float error = (from - (d - back)) - (to + back);
+  const float t = d * unit;
+  const float low = fmaf(d, unit, -t) + fmaf(d, unit_low, error * unit);
+  const float y = exp2_approx(t);
+  return t >= -120.f ? double(fmaf(y, low * 0.69314718f, y)) : 0.0;
 }
 
 // 2^(j/64) by the series of e^x, in the order of growing terms from the smallest.
@@ -425,7 +446,7 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const Params p) {
     // each thread relative to its own largest
     if (fmaxf(top, high) == -INFINITY) continue;
     if (high > top) {
-      sum *= double(exp2_approx(fmaxf(top - high, lowest) * unit));
+      if (sum > 0.0) sum *= rescale(top, high, unit, unit_low);
       top = high;
     }
     float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -463,7 +484,7 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const Params p) {
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) high = fmaxf(high, tops[w]);
   int at = top == high ? first : 0x7fffffff;
-  if (top != high) sum *= double(exp2_approx(fmaxf(top - high, lowest) * unit));
+  if (top != high) sum *= rescale(top, high, unit, unit_low);
 #pragma unroll
   for (int m = 1; m < 32; m *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
   at = __reduce_min_sync(0xffffffffu, at);
