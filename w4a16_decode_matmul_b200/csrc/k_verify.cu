@@ -65,11 +65,11 @@ cudaError_t launch(verify::Params p, cudaStream_t s, int sms) {
   }
   // Elements of a share: so many that there are 24 warps an SM, since a warp alone is bound by
   // the latency of its exponentials, but not more than 1,024, for the balance of the last
-  // ones, nor so few that a row has more than kShares.
+  // ones, nor so few that a sequence has more than its slots of the workspace.
   const auto steps = [](int64_t n) { return (n + kStep - 1) / kStep * kStep; };
   const int64_t even = steps(most * p.seqs / (24 * int64_t(sms)) + 1);
   p.share = int(std::max(std::min<int64_t>(verify::kShareMost, even),
-                         steps((most + verify::kShares - 1) / verify::kShares)));
+                         steps((most + p.slots - 1) / p.slots)));
   p.n_shares = int((most + p.share - 1) / p.share);
   const int64_t ctas =
       int64_t(p.seqs) * ((p.n_shares + verify::kShareWarps - 1) / verify::kShareWarps);
@@ -83,16 +83,20 @@ cudaError_t launch(verify::Params p, cudaStream_t s, int sms) {
   return e;
 }
 
-// Where the parts of the workspace begin.
+// Where the parts of the workspace begin, and how many shares it holds: as many as a row can
+// have for the first 1,024 rows, then so many that 16 a row are left -- many sequences fill
+// the GPU with few shares each (with 256 for every row it was 12 KB a row, 103 GB at most).
 struct Workspace {
   size_t decisions, shares, bytes;
+  int64_t slots;
 };
 
 Workspace layout(int64_t rows) {
   Workspace w;
+  w.slots = std::max(std::min<int64_t>(rows, 1024) * verify::kShares, rows * 16);
   w.decisions = size_t(rows) * 2 * verify::kPieces * sizeof(verify::Piece);
   w.shares = w.decisions + round_up(size_t(rows) * sizeof(verify::Decision), 16);
-  w.bytes = w.shares + size_t(rows) * verify::kShares * sizeof(verify::Share);
+  w.bytes = w.shares + size_t(w.slots) * sizeof(verify::Share);
   return w;
 }
 
@@ -120,6 +124,7 @@ cudaError_t run_verify_drafts(const wq_verification& v, void* workspace, cudaStr
   p.pieces = reinterpret_cast<verify::Piece*>(base);
   p.decisions = reinterpret_cast<verify::Decision*>(base + w.decisions);
   p.shares = reinterpret_cast<verify::Share*>(base + w.shares);
+  p.slots = int(std::min<int64_t>(verify::kShares, w.slots / std::min(v.rows, v.seqs)));
   p.rows = v.rows;
   p.seqs = v.seqs;
   p.rows_per_seq = v.row_starts ? 0 : v.rows / v.seqs;

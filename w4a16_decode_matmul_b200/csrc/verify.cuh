@@ -108,11 +108,13 @@ struct Params {
   const int* row_starts;             // [seqs + 1] or null: rows_per_seq each
   const int* seq_lens;               // [seqs] or null
   int *out_tokens, *accepted, *out_lens;
-  // The workspace: [2][rows][kPieces] (target, draft); [rows] and [rows][kShares], at a
-  // sequence's first row
+  // The workspace: [2][rows][kPieces] (target, draft); [rows], at a sequence's first row; a
+  // sequence's shares slots apart, by its number, or by its first row where there are
+  // fewer rows than sequences
   Piece* pieces;
   Decision* decisions;
   Share* shares;
+  int slots;
   int rows, seqs, rows_per_seq, vocab;
   int piece, n_pieces;               // elements of a piece, pieces of a row
   int share, n_shares;               // of share_kernel
@@ -914,6 +916,10 @@ __device__ __forceinline__ Decision decide(const Params& p, DecideShared& s, int
   return d;
 }
 
+__device__ __forceinline__ Share* shares_of(const Params& p, int b, const Rows& rows) {
+  return p.shares + int64_t(p.seqs <= p.rows ? b : rows.first) * p.slots;
+}
+
 __device__ __forceinline__ void no_rows(const Params& p, int b) {
   p.accepted[b] = 0;
   if (p.out_lens != nullptr) p.out_lens[b] = p.seq_lens[b];
@@ -1073,7 +1079,7 @@ __global__ void __launch_bounds__(kShareWarps * 32, 6) share_kernel(const Params
                            const int64_t first = int64_t(i) * p.share - m.rows.lead;
                            const Share s = m.share(int(min(first, int64_t(p.vocab))),
                                                    int(min(first + p.share, int64_t(p.vocab))));
-                           if (lane == 0) p.shares[int64_t(rows.first) * kShares + i] = s;
+                           if (lane == 0) shares_of(p, b, rows)[i] = s;
                          });
 }
 
@@ -1111,7 +1117,7 @@ __global__ void __launch_bounds__(kFindWarps * 32, 2) find_kernel(const Params p
   grid_dependency_wait();
   const Decision d = p.decisions[rows.first];
   if (d.mode == kDone) return;
-  const Share* const shares = p.shares + int64_t(rows.first) * kShares;
+  const Share* const shares = shares_of(p, b, rows);
   with_masses<T, LOGITS>(
       p, d, hot, exp_scale(hot), table_s + (lane & (kCopies - 1)), lane, [&](const auto& m) {
         using M = std::decay_t<decltype(m)>;
