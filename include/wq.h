@@ -490,9 +490,9 @@ wq_status wq_rotary(const void *X, int64_t x_stride, int32_t rows, int32_t heads
 /* Queries turned into Q_out, and wq_kv4_write of the turned keys and the values, in
  * one call.  Positions are those of the rows' tokens, or `positions` (int32
  * [rows], 4-byte aligned) where it is given.  Queries as wq_rotary's; keys are turned
- * exactly, rounded to binary32 and then to bfloat16 and quantized as wq_kv4_write
- * quantizes (a key that neither of its roundings can decide within 2^-40 may fall to
- * either side).  Q bfloat16 [rows][q_heads][head_dim]; Q_out may be Q itself (the
+ * exactly, but for 3 2^-39 of |x1 c| + |x2 s|, rounded to binary32 and then to bfloat16 and
+ * quantized as wq_kv4_write quantizes: a key that lies nearer than that to a border of one of
+ * its roundings may fall to either side.  Q bfloat16 [rows][q_heads][head_dim]; Q_out may be Q itself (the
  * same address and stride), else it may not overlap Q, K or V; q_heads 0: keys and
  * values alone, Q and Q_out not looked at.  A row of a sequence that holds no token
  * has its query turned and nothing written; rows behind the last sequence are left

@@ -11,9 +11,10 @@
 // and so are sine and cosine: a binary32 product is off by up to 2^-24 of
 // itself, 0.03 radians at position 10^6.  c and s are rounded to binary32, the
 // result to bfloat16.  Between the two, queries take a multiply-add in binary32;
-// keys that go into the cache are the exact result rounded to binary32 (but for
-// one in 2^20 or so), because a bit of a key next to a border between two codes is
-// a whole step of the value that the cache holds.
+// keys that go into the cache are the result to within 3 2^-39 of |x1 c| + |x2 s|,
+// rounded to binary32 (one in some 10^7 other than the exact result's), because a bit of
+// a key next to a border between two codes is a whole step of the value that the cache
+// holds.
 #pragma once
 
 #include "kv4_attn.cuh"
@@ -336,8 +337,8 @@ struct SplitTurns {
 
 // Eight keys, two at a time: x c + z n rounded once to binary32.  The leading products are
 // exact, the error of their sum is found exactly (Knuth's two-sum), and what the low parts
-// add is 2^-16 of the products with an error of 2^-24 of that.  z: the other elements of
-// the pairs; e: the first key's entry.
+// add is at most 2^-15 of the products, with two roundings of 2^-24 of that.  z: the
+// other elements of the pairs; e: the first key's entry.
 template <int D>
 __device__ __forceinline__ uint4 turn_keys(const uint4& xs, const uint4& zs,
                                            const SplitTurns<D>& t, int e) {
