@@ -370,8 +370,8 @@ typedef struct wq_kv4_bounds {
 } wq_kv4_bounds;
 
 /* The pages of every row and kv head, in the order of their tokens, and the
- * tokens that they hold (device memory, caller-owned).  Bit for bit the same on
- * every call. */
+ * tokens that they hold (device memory, caller-owned, 16-byte aligned).  Bit for bit the
+ * same on every call. */
 typedef struct wq_kv4_selection {
     int32_t max_pages;  /* pages of a list, 1 or more                          */
     int32_t first;      /* a sequence's first pages that are always chosen     */
@@ -441,8 +441,8 @@ wq_status wq_kv4_sparse_attention(const void *Q, int64_t q_stride, int32_t q_hea
  * is (i, i + dim/2), or (2i, 2i + 1) where interleaved is not 0, i < dim/2; the
  * elements from dim on stay as they are.
  *   y1 = x1 c - x2 s, y2 = x2 c + x1 s, c = amplitude cos(p f_i), s = amplitude sin(p f_i)
- * The angle is a binary64 product, c and s are rounded to binary32.  Used on
- * queries and keys before wq_kv4_write. */
+ * The angle is a binary64 product, c and s are rounded to binary32; a pair whose angle is
+ * 2^50 or more is unspecified.  Used on queries and keys before wq_kv4_write. */
 typedef struct wq_rotary_spec {
     const float *freqs;   /* [dim/2] radians a position, device memory         */
     int32_t dim;          /* even, 2 .. head_dim                               */

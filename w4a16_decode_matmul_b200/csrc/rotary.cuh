@@ -30,9 +30,10 @@ struct Spec {
 
 // (c, s) of one position and frequency, in binary64 arithmetic that all heads share.
 // The angle less a multiple of pi/2 that is held in two parts (W. J. Cody and W. Waite,
-// 1980), then the series of sine and cosine to the 15th and 16th power: for |r| <= pi/4
-// the next terms are below 2^-54.  (A function of its own: its registers are not the
-// kernels', which keep their loads in flight meanwhile.)
+// 1980; what the two leave of pi/2, 1.5 10^-33, counts from 2^60 on, and the multiple is the
+// nearest or next to it below 2^50), then the series of sine and cosine to the 15th and 16th
+// power: for |r| <= pi/4 the next terms are below 2^-54.  (A function of its own: its
+// registers are not the kernels', which keep their loads in flight meanwhile.)
 static __device__ __noinline__ float2 turn_of(int position, float freq, float amplitude) {
   const double a = double(position) * double(freq);
   const double k = rint(a * 0.6366197723675814);         // 2/pi
