@@ -70,3 +70,28 @@ def test_drafts_near_the_border_of_acceptance(seqs, swapped):
         tokens = ints([x] * (2 * seqs))
         _, accepted, _ = wq().verify_drafts(target, tokens, uniform, draft, seqs=seqs, logits=True)
         assert accepted.tolist() == [1 if side < 0 else 0] * seqs, side
+
+
+@pytest.mark.parametrize("seqs,vocab", [(2, 8192), (2, 32_768), (40, 8192), (40, 65_536)])
+@pytest.mark.parametrize("swapped", [False, True])
+@pytest.mark.parametrize("rows", ["far apart", "neighbours"])
+def test_sums_whose_errors_are_farthest_apart(seqs, vocab, swapped, rows):
+    """One large logit among the 32 of every thread: of many levels these gave the sums with the
+    largest errors measured, 4.3 10^-7 up and 4.4 10^-7 down (and 8.4 10^-7 between two
+    neighbours), so that all of a refused draft's rows are summed again."""
+    pair = {"far apart": ((1.0161354541778564, -5.315082550048828),
+                          (4.238065242767334, 0.17843985557556152)),
+            "neighbours": ((3.1992855072021484, -2.8756802082061768),
+                           (3.1992855072021484, -2.8756825923919678))}[rows]
+    at = torch.arange(vocab, device="cuda")
+    first = (at % 4 == 0) & (at % 4096 < 512)          # of a thread
+    p, q = (torch.where(first, hi, lo) for hi, lo in (pair[::-1] if swapped else pair))
+    n = 2 * seqs
+    tokens = ints([vocab] * n)
+    uniform = (torch.arange(n, device="cuda") + 0.37) / n
+    got, want = run(p.expand(n, vocab).contiguous(), tokens, uniform, q.expand(n, vocab).contiguous(),
+                    [2] * seqs)
+    assert got[1:] == want[1:] and got[1] == [0] * seqs
+    # the tokens of a level all have the same mass: a number next to a border (of 8,192 to
+    # 65,536 of them, within some 10^-11 of a mass) is the only one that could give a neighbour
+    assert got[0] == want[0]
