@@ -479,10 +479,10 @@ enum { WQ_ROTARY_TRANSPOSE = 1 /* -s in s's place: the gradient of a rotation */
  * binary32, rounded once to bfloat16 (half a step 2^-8).  Y may be X itself (the
  * same address and stride), else they may not overlap.  heads may be several tensors'
  * side by side (queries and keys of a fused projection).
- * heads at most 65,536, head_dim a multiple of 8, at most 512.  WQ_ERR_INVALID_ARG for sizes, pointers and
- * flags outside this, WQ_ERR_UNSUPPORTED for another head_dim, WQ_ERR_ALIGNMENT for
- * X, Y, positions or freqs not 16-byte (positions: 4-byte) aligned and strides that
- * are no multiple of 8.  rows = 0 is a call without work. */
+ * heads at most 65,536, head_dim a multiple of 8, at most 512.  WQ_ERR_INVALID_ARG for
+ * sizes, pointers and flags outside this, WQ_ERR_UNSUPPORTED for another head_dim,
+ * WQ_ERR_ALIGNMENT for X, Y, positions or freqs not 16-byte (positions: 4-byte) aligned and
+ * strides that are no multiple of 8.  rows = 0 is a call without work. */
 wq_status wq_rotary(const void *X, int64_t x_stride, int32_t rows, int32_t heads,
                     int32_t head_dim, const int32_t *positions, const wq_rotary_spec *spec,
                     unsigned int flags, void *Y, int64_t y_stride, wq_stream_t stream);
@@ -492,9 +492,9 @@ wq_status wq_rotary(const void *X, int64_t x_stride, int32_t rows, int32_t heads
  * [rows], 4-byte aligned) where it is given.  Queries as wq_rotary's; keys are turned
  * exactly, but for 3 2^-39 of |x1 c| + |x2 s|, rounded to binary32 and then to bfloat16 and
  * quantized as wq_kv4_write quantizes: a key that lies nearer than that to a border of one of
- * its roundings may fall to either side.  Q bfloat16 [rows][q_heads][head_dim]; Q_out may be Q itself (the
- * same address and stride), else it may not overlap Q, K or V; q_heads 0: keys and
- * values alone, Q and Q_out not looked at.  A row of a sequence that holds no token
+ * its roundings may fall to either side.  Q bfloat16 [rows][q_heads][head_dim]; Q_out may be
+ * Q itself (the same address and stride), else it may not overlap Q, K or V; q_heads 0: keys
+ * and values alone, Q and Q_out not looked at.  A row of a sequence that holds no token
  * has its query turned and nothing written; rows behind the last sequence are left
  * alone.  spec->dim a multiple of 16 (WQ_ERR_UNSUPPORTED otherwise: use wq_rotary and
  * wq_kv4_write).  Other errors as those two. */
@@ -558,11 +558,11 @@ size_t wq_verify_workspace_bytes(int64_t rows);
  * 2^-43): the token is that of exact arithmetic unless uniform_0 times the whole is within
  * 10^-12 of a border, in units of the distributions (where p and q are nearly alike the
  * whole of max(p - q, 0) is far below 1).  A draft's p and q are those of probabilities
- * exactly; of logits their sums of exponentials are good to 1.3 10^-6 (some 3 10^-8 for logits
- * that differ), and to 4 10^-7 more for every 2^18 tokens beyond the first: a draft whose u q is
- * nearer to p than both sums' errors may be decided either way.  Probabilities need
- * not sum to 1; negative ones and NaN count as 0, NaN logits as -infinity; a logit more than
- * 600 temperatures below its row's largest has no mass; of logits of +infinity each has the
+ * exactly; of logits their sums of exponentials are good to 1.3 10^-6 (10^-7 as a rule), and to
+ * 4 10^-7 more for every 2^18 tokens beyond the first: a draft whose u q is nearer to p than
+ * both sums' errors may be decided either way.  Probabilities are finite and need not sum to
+ * 1; negative ones and NaN count as 0, NaN logits as -infinity; a logit more than 600
+ * temperatures below its row's largest has no mass; of logits of +infinity each has the
  * same mass; a row without any mass gives the token -1.  A sequence without rows gets
  * accepted 0; rows behind the last sequence are left as they were.  Two sequences' rows may
  * not overlap.  Outputs may not overlap inputs, but out_lens may be seq_lens.

@@ -946,7 +946,8 @@ def verify_drafts(target: torch.Tensor, tokens: torch.Tensor, uniform: torch.Ten
         rows, seqs, vocab, WQ_OUT_BF16 if target.dtype is _BF16 else WQ_OUT_F32,
         WQ_VERIFY_LOGITS if logits else 0,
         _words(row_starts, _I32, (seqs + 1,), index, "row_starts"), target.data_ptr(), ts,
-        0 if draft is None else draft.data_ptr(), ds, _words(tokens, _I32, n_shape, index, "tokens"),
+        0 if draft is None else draft.data_ptr(), ds,
+        _words(tokens, _I32, n_shape, index, "tokens"),
         _words(uniform, torch.float32, n_shape, index, "uniform"),
         _words(temperature, torch.float32, b_shape, index, "temperature"),
         _words(seq_lens, _I32, b_shape, index, "seq_lens"),

@@ -152,7 +152,8 @@ cudaError_t run_kv4_attention(const void* Q, int64_t q_stride, int q_heads,
     p.max_columns = kFew;  // a ragged batch may hold both kinds
   }
   const int max_columns = int(std::min<int64_t>(bound * p.gqa, kFew));
-  return dispatch_kv4<Attn<false>::Op>(cache.head_dim, cache.group, p, max_columns, false, s, dev.sms);
+  return dispatch_kv4<Attn<false>::Op>(cache.head_dim, cache.group, p, max_columns, false, s,
+                                       dev.sms);
 }
 
 }  // namespace wqh

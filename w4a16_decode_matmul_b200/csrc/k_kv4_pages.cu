@@ -18,8 +18,8 @@ cudaError_t run_kv4_attention_pages(const void* Q, int64_t q_stride, int q_heads
   p.batch = device_batch(each_row, cache.page_size);
   if (p.batch.status == nullptr) return cudaErrorInitializationError;
   p.head_stride = sel.max_pages;
-  return dispatch_kv4<Attn<true>::Op>(cache.head_dim, cache.group, p, std::min(p.gqa, kv4::kMaxRows),
-                              after, s, dev.sms);
+  return dispatch_kv4<Attn<true>::Op>(cache.head_dim, cache.group, p,
+                                      std::min(p.gqa, kv4::kMaxRows), after, s, dev.sms);
 }
 
 }  // namespace wqh

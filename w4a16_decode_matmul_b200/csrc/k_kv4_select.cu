@@ -21,7 +21,10 @@ struct BoundsOp {
 };
 
 // CTAs of a cluster: one for each 256 pages that a sequence can have, as long as there is an
-// SM for each (128 lists of about 650 pages: 1 CTA each 11.6 us, 2 each 13.3).
+// SM for each (128 lists of about 650 pages: 1 CTA each 11.6 us, 2 each 13.3).  The keys'
+// shared memory goes by the page table's width, since the lengths are in device memory: 64
+// sequences of 250 pages and 8 kv heads take 20.7 us with a table of 250 and 28.9 with one of
+// 40,000, which leaves one CTA an SM; up to 16 such sequences there is no difference.
 int select_ctas(int64_t width, int64_t units, int sms) {
   int ctas = 1;
   while (ctas < kv4::kMaxCluster && ctas * 256 < width && units * ctas * 2 <= sms) ctas *= 2;

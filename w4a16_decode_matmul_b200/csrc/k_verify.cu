@@ -56,6 +56,12 @@ cudaError_t launch(verify::Params p, cudaStream_t s, int sms) {
   // 13.3 and 14.0, 18: 19.9 and 20.7, 32: 26.6 and 29.0, 48: 38.8 and 34.6; 50,021: 17.5 and
   // 15.1, 32.0 and 28.0, 38.7 and 37.2; 131,072: 25.3 and 16.5, 51.1 and 43.1, 68.8 and 63.1,
   // 64: 116 and 103.  (The cluster is two launches less on the host.)
+  // bfloat16 logits, 4, 18, 32, 37, 48 sequences: 32,000: 16.6 and 18.7, 22.8 and 24.8, 24.8 and
+  // 28.9, 32.0 and 31.0, 38.1 and 34.7; 50,021: 20.5 and 19.3, 29.6 and 26.9, 35.1 and 35.2,
+  // 42.1 and 39.2, 51.5 and 42.9.  Probabilities, one launch or three: binary32, 32,000: 8.8 and
+  // 10.4, 10.5 and 10.5, 10.4 and 12.5, 14.6 and 12.5, 15.0 and 12.5; 50,021: 14.5 and 10.5, 14.5
+  // and 12.5, 14.5 and 12.5, 18.7 and 14.6, 21.0 and 14.6; bfloat16, 32,000: 10.4 and 14.5, 10.5
+  // and 14.5, 10.4 and 14.7, 14.6 and 14.6, 15.6 and 14.7; 50,021: within 2 either way up to 37.
   constexpr int kClusterVocab = 40960;
   if (p.vocab <= kClusterVocab && int64_t(p.seqs) * verify::kMaxCluster <= 2 * sms) {
     p.ctas = 1;
@@ -133,7 +139,8 @@ cudaError_t run_verify_drafts(const wq_verification& v, void* workspace, cudaStr
   if (p.status == nullptr) return cudaErrorInitializationError;
   const bool logits = (v.flags & WQ_VERIFY_LOGITS) != 0;
   if (v.dtype == WQ_OUT_BF16)
-    return logits ? launch<__nv_bfloat16, true>(p, s, sms) : launch<__nv_bfloat16, false>(p, s, sms);
+    return logits ? launch<__nv_bfloat16, true>(p, s, sms)
+                  : launch<__nv_bfloat16, false>(p, s, sms);
   return logits ? launch<float, true>(p, s, sms) : launch<float, false>(p, s, sms);
 }
 

@@ -366,7 +366,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const AttnParams p)
   } else {
     const int b_begin = min(p.batch.seqs, tid * per_thread);
     const int b_end = min(p.batch.seqs, b_begin + per_thread);
-    for (int b = b_begin; b < b_end; ++b) upto += sequence_units<ROWS>(p, attn_sequence<LISTS>(p, b));
+    for (int b = b_begin; b < b_end; ++b)
+      upto += sequence_units<ROWS>(p, attn_sequence<LISTS>(p, b));
   }
 #pragma unroll
   for (int m = 1; m < 32; m *= 2) {

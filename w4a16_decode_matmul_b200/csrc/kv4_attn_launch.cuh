@@ -56,10 +56,12 @@ struct Attn {
     static cudaError_t run(const kv4::AttnParams& p, int max_columns, bool after, cudaStream_t s,
                            int sms) {
       constexpr int kTiles = D / G == 4 ? 1 : 2;
-      if (max_columns > 8) return launch_attn<D, G, 2, D == 64 ? 12 : 8, 1, LISTS>(p, after, s, sms);
+      if (max_columns > 8)
+        return launch_attn<D, G, 2, D == 64 ? 12 : 8, 1, LISTS>(p, after, s, sms);
       const int64_t units =
           int64_t(p.batch.seqs) * p.cache.kv_heads * (p.batch.max_len / kv4::kUnit + 1);
-      if (units <= int64_t(4) * 8 * sms) return launch_attn<D, G, 1, 8, kTiles, LISTS>(p, after, s, sms);
+      if (units <= int64_t(4) * 8 * sms)
+        return launch_attn<D, G, 1, 8, kTiles, LISTS>(p, after, s, sms);
       return launch_attn<D, G, 1, 12, kTiles, LISTS>(p, after, s, sms);
     }
   };

@@ -222,7 +222,9 @@ __device__ __forceinline__ void make_turns(const RotaryParams& p, bool interleav
 // on their way meanwhile.  HBM bound, two bytes in and two out an element.
 //
 // Measured on B200: 8,192 rows of 40 heads of 128 (168 MB) 33 us, 5.1 TB/s.  A row a CTA
-// 50; angles as (c, s) pairs and an element an instruction 41.
+// 50; angles as (c, s) pairs and an element an instruction 41.  3,001 rows of 24 heads of 64,
+// half of each side by side (18 MB): 5 us; 751 CTAs of 384 threads are 1.27 waves, and its
+// warps wait for the angles (two of five at the barrier) and for loads.
 template <bool INTERLEAVED>
 __global__ void __launch_bounds__(512, 3) rotary_kernel(const RotaryParams p) {
   __shared__ RotaryTurns turns;
@@ -267,7 +269,8 @@ __global__ void __launch_bounds__(512, 3) rotary_kernel(const RotaryParams p) {
 // shared memory, 16 KB of whole heads at a time, so that memory is read and written in
 // runs all the same, and each run is read by all before it is written where Y is X: 8,192
 // rows of 40 heads, 126 of 128 elements turned, 62 us (a pair a thread, two bytes at a
-// time, 84; 128 turned, rotary_kernel, 33).
+// time, 84; 128 turned, rotary_kernel, 33).  Shared memory bounds it (92 % of its rate): the
+// other element of each pair comes two bytes at a time, its angles eight.
 constexpr int kStaged = 8192;  // elements
 constexpr int kStagedThreads = 256;
 
@@ -413,10 +416,11 @@ struct RowPlace {
 // meanwhile.  CTAs behind the rows check the sequences.
 //
 // Measured on B200 (15,609 rows, 32 + 2 * 8 heads of 128, half of each turned, 330 MB): 86
-// us, 3.8 TB/s, 3,400 warp instructions a row (issue 60 %, ALU 48 %), of which the
-// quantizer has a third.  With the queries in a launch of their own 54 + 51 us; a row a CTA
-// 102; keys and values last, or always in the same warps, 92 to 99; three CTAs an SM, which
-// spill nothing, 94.
+// us, 3.8 TB/s, 3,400 warp instructions a row, of which the quantizer has a third.  Nothing
+// is full (issue 58 %, ALU 46 %, shared memory 60 %): of the 6.9 warps that a scheduler has
+// under 64 registers, 1.7 wait for loads, 0.9 for shared memory and 0.8 at barriers.  With
+// the queries in a launch of their own 54 + 51 us; a row a CTA 102; keys and values last,
+// or always in the same warps, 92 to 99; three CTAs an SM, which spill nothing, 94.
 template <int D, int G, bool INTERLEAVED>
 __global__ void __launch_bounds__(kWriteWarps * 32, 4)
     write_rotary_kernel(const WriteParams p, int shares) {

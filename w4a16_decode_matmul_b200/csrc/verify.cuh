@@ -17,8 +17,8 @@
 // moves all boundaries of max(p - q, 0) at once and costs twenty times as much.  So the
 // sampled row's (and its draft row's) masses and sums are in binary64, exponentials
 // within 2^-43.  A draft's acceptance has one border: there the sums of exponentials
-// are binary32's, added in binary64 from 32 terms on.  For logits that round to either side
-// they are off by some 3 10^-8; where all errors have one sign by up to 21 of 2^-24 = 1.3 10^-6:
+// are binary32's, added in binary64 from 32 terms on.  For random logits they are off by 5 to 8
+// 10^-8 (ex2 is low on average), where all errors have one sign by up to 21.7 2^-24 = 1.3 10^-6:
 // 4 for ex2's two units in the last place, 2 ln 2 t for the rounding of x - top and of the
 // exponent -t, of which the weighted mean is at most 2.7 among a thread's 32 elements, 9 for the
 // additions, 5 from a thread's largest logit to the CTA's.  From 2^18 tokens on a thread has
@@ -33,7 +33,7 @@
 // the sign of p' - q' where that is more than 2^-20 of q' and |a - b| is less; so a share with
 // an element that is nearer goes over its rows a second time, and where the exact sums say that
 // a and b are 2^-21 or more apart, all shares do (rounding errors of one sign throughout a row
-// only: for random logits a and b are some 3 10^-8).
+// only: for random logits both are 5 to 8 10^-8, in the same direction).
 //
 // Kernels.  Logits first go through stats_kernel: largest logit and sum of exponentials
 // of every piece of every row, which reads each row once.  Then, for few sequences of few
@@ -45,10 +45,13 @@
 //
 // Measured on B200, 64 sequences of 6 rows of 131,072 binary32 logits, drafts too (369 MB):
 // statistics 62 us (5.9 TB/s, HBM bound), decisions 4, shares 28 (binary64 exponentials of
-// 35 instructions each), tokens 4 to 8: 102 us in all.  With binary64 exponentials in the
-// statistics 288; clusters for all 126.  32 ragged sequences of 50,021 bfloat16 logits 28 us,
-// of which none reaches a quarter of its kernel's rate: four short chains of look-ups.
-// One sequence of 5 rows of 32,000 probabilities 7 us.
+// 35 instructions each), tokens 4 to 8: 103 us in all.  With binary64 exponentials in the
+// statistics 288; clusters for all 126.  32 ragged sequences of 50,021 bfloat16 logits 27 us;
+// one by one, with cold caches, its kernels take 11, 7, 12 and 16: statistics wait for
+// loads (half of the issue slots used), decisions and tokens are a CTA for each of 32 SMs
+// that waits for loads and barriers, and find_kernel spills 228 bytes at the 64 registers
+// that two CTAs an SM leave.  One sequence of 5 rows of 32,000 probabilities 8 us; 64 x 6
+// rows of 131,072 binary32 probabilities 25 (10.2 at the copy rate; three kernels).
 #pragma once
 
 #include <type_traits>
@@ -191,8 +194,8 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // logit is multiplied by to be relative to another.  All of a thread's elements share its
 // error, so the exponent is held in two parts (Knuth's two-sum, the product's own error): what
 // is left is ex2's 2^-22 and a rounding.  Where the exponent was one product, sums of two
-// levels 8.3 apart were off by 6 10^-7.  (32 ragged sequences: 29.2 us so, 29.6 now, 30.2 in
-// binary64.)
+// levels 8.3 apart were off by 6 10^-7.  (32 ragged sequences, a pass alone: 29.2 us so, 29.6
+// now, 30.2 in binary64.)
 __device__ __forceinline__ double rescale(float from, float to, float unit, float unit_low) {
   const float d = from - to, back = d - from;
   const float error = (from - (d - back)) - (to + back);
@@ -388,7 +391,8 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const Params p) {
             w[k][i] = at + i >= 0 && at + i < end ? __float_as_uint(row[at + i]) : kNothing;
           } else {
             const int e = at + 2 * i;
-            const uint32_t one = e >= 0 && e < end ? __bfloat16_as_ushort(row[e]) : kNothing & 0xffffu;
+            const uint32_t one =
+                e >= 0 && e < end ? __bfloat16_as_ushort(row[e]) : kNothing & 0xffffu;
             const uint32_t two =
                 e + 1 >= 0 && e + 1 < end ? __bfloat16_as_ushort(row[e + 1]) : kNothing >> 16;
             w[k][i] = one | (two << 16);

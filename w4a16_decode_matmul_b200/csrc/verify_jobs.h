@@ -24,7 +24,8 @@ struct Job {
 WQ_HOST_DEVICE constexpr int jobs_of(int n) { return 2 * n + 1; }
 
 WQ_HOST_DEVICE constexpr Job job_of(int job, int n, int base) {
-  return job > n ? Job{base + job - n, base + job - n, true} : Job{base + job, base + job + 1, false};
+  return job > n ? Job{base + job - n, base + job - n, true}
+                 : Job{base + job, base + job + 1, false};
 }
 
 }  // namespace verify
